@@ -17,4 +17,7 @@ from ._binding import (  # noqa: F401
     RBF_FLAG_BF16_CORPUS, RBF_FLAG_COSINE, RBF_OPT_CTAS_PER_SM, RBF_OPT_STAGE_BYTES, RBF_OPT_SMEM_BUDGET,
     RBF_OPT_TIMEOUT_NS, RBF_OPT_SCHEDULE, RBF_OPT_BATCH_SAMPLE, RBF_OPT_HOST_READ, FAULT_COPY, FAULT_LAUNCH,
 )
+from .ops import (  # noqa: F401
+    Ops, RBF_DTYPE_F32, RBF_DTYPE_BF16, RBF_DTYPE_F16, RBF_DTYPE_I32, RBF_OPS_MAX_DEPTH, RBF_OPS_MAX_VOCAB,
+)
 from ._build import build  # noqa: F401

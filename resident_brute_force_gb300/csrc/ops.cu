@@ -1,0 +1,274 @@
+// ops.cu -- the handle behind include/rbf_ops.h: workspace, argument checks,
+// and the order of launches of the scoring-head operators.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <new>
+
+#include "../../include/rbf_ops.h"
+#include "ops_internal.h"
+
+using namespace rbf;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 20;
+
+}  // namespace
+
+struct rbf_ops {
+  int device = 0;
+  int num_sms = 0;
+  cudaStream_t stream = nullptr;
+  bool own_stream = false;
+  int64_t max_rows = 0;
+  int max_depth = 0;
+
+  int8_t* rows_i8 = nullptr;  // linear_i8_dev: the quantised rows, max_rows x row_pitch
+  float* row_scale = nullptr;
+  int64_t row_pitch = 0;
+  int* errw = nullptr;  // error bits of the kernels since the last check
+
+  int last_cuda_error = 0;
+  int launches = 0;
+  int fault_count = 0;
+};
+
+namespace {
+
+rbf_status cuda_fail(rbf_ops* o, cudaError_t err) {
+  o->last_cuda_error = static_cast<int>(err);
+  return RBF_ERR_CUDA;
+}
+
+#define OPS_LAUNCH(o, call)                                              \
+  do {                                                                   \
+    if ((o)->fault_count > 0) {                                          \
+      --(o)->fault_count;                                                \
+      return cuda_fail((o), cudaErrorUnknown);                           \
+    }                                                                    \
+    const cudaError_t _st = (call);                                      \
+    if (_st != cudaSuccess) return cuda_fail((o), _st);                  \
+    ++(o)->launches;                                                     \
+  } while (0)
+
+void release(rbf_ops* o) {
+  if (o->stream) cudaStreamSynchronize(o->stream);
+  cudaFree(o->rows_i8);
+  cudaFree(o->row_scale);
+  cudaFree(o->errw);
+  if (o->own_stream && o->stream) cudaStreamDestroy(o->stream);
+  delete o;
+}
+
+bool float_dtype(rbf_dtype t) { return t == RBF_DTYPE_F32 || t == RBF_DTYPE_BF16 || t == RBF_DTYPE_F16; }
+
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0; }
+
+// A matrix argument: a pointer aligned to its element and a stride of at
+// least a row, in which no row's end passes what 64 bits address.
+bool matrix_ok(const void* p, int elem, int64_t rows, int64_t cols, int64_t ld) {
+  if (rows < 0 || cols < 0 || ld < cols) return false;
+  if (rows == 0 || cols == 0) return true;
+  if (!p || !aligned(p, elem)) return false;
+  return ld <= (INT64_MAX / 8) / std::max<int64_t>(rows, 1);
+}
+
+bool floats_ok(const void* p) { return !p || aligned(p, 4); }
+
+rbf_status check_matmul(const rbf_ops* o, const MatmulI8Launch& a) {
+  if (a.m < 0 || a.n < 0 || a.k < 0 || a.m > o->max_rows || a.n > INT32_MAX || a.k > o->max_depth)
+    return RBF_ERR_INVALID_VALUE;
+  if (!matrix_ok(a.b, 1, a.n, a.k, a.ld_b)) return RBF_ERR_INVALID_VALUE;
+  if (!matrix_ok(a.out, dtype_bytes(a.out_dtype), a.m, a.n, a.ld_out)) return RBF_ERR_INVALID_VALUE;
+  if (!floats_ok(a.a_scale) || !floats_ok(a.b_scale) || !floats_ok(a.bias)) return RBF_ERR_INVALID_VALUE;
+  return RBF_OK;
+}
+
+rbf_status run_matmul(rbf_ops* o, const MatmulI8Launch& a) {
+  OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
+  return RBF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream, rbf_ops** out) {
+  if (!out) return RBF_ERR_INVALID_VALUE;
+  if (max_rows < 1 || max_rows > kMaxRows || max_depth < 1 || max_depth > RBF_OPS_MAX_DEPTH)
+    return RBF_ERR_INVALID_VALUE;
+  rbf_ops* o = new (std::nothrow) rbf_ops();
+  if (!o) return RBF_ERR_OUT_OF_MEMORY;
+  cudaError_t st = cudaGetDevice(&o->device);
+  if (st == cudaSuccess) st = cudaDeviceGetAttribute(&o->num_sms, cudaDevAttrMultiProcessorCount, o->device);
+  if (st != cudaSuccess) {
+    delete o;
+    return RBF_ERR_CUDA;
+  }
+  o->max_rows = max_rows;
+  o->max_depth = max_depth;
+  o->row_pitch = (int64_t(max_depth) + 15) / 16 * 16;
+  if (cuda_stream) {
+    o->stream = static_cast<cudaStream_t>(cuda_stream);
+  } else {
+    if (cudaStreamCreateWithFlags(&o->stream, cudaStreamNonBlocking) != cudaSuccess) {
+      delete o;
+      return RBF_ERR_CUDA;
+    }
+    o->own_stream = true;
+  }
+  const bool ok = cudaMalloc(&o->rows_i8, static_cast<size_t>(max_rows) * o->row_pitch) == cudaSuccess &&
+                  cudaMalloc(&o->row_scale, static_cast<size_t>(max_rows) * sizeof(float)) == cudaSuccess &&
+                  cudaMalloc(&o->errw, 4 * sizeof(int)) == cudaSuccess;
+  if (!ok) {
+    cudaGetLastError();
+    release(o);
+    return RBF_ERR_OUT_OF_MEMORY;
+  }
+  if (cudaMemsetAsync(o->errw, 0, 4 * sizeof(int), o->stream) != cudaSuccess ||
+      cudaStreamSynchronize(o->stream) != cudaSuccess) {
+    release(o);
+    return RBF_ERR_CUDA;
+  }
+  *out = o;
+  return RBF_OK;
+}
+
+rbf_status rbf_ops_destroy(rbf_ops* o) {
+  if (o) release(o);
+  return RBF_OK;
+}
+
+void* rbf_ops_stream(rbf_ops* o) { return o ? o->stream : nullptr; }
+int32_t rbf_ops_last_cuda_error(rbf_ops* o) { return o ? o->last_cuda_error : 0; }
+int32_t rbf_ops_last_launches(rbf_ops* o) { return o ? o->launches : 0; }
+
+rbf_status rbf_ops_check_device_error(rbf_ops* o) {
+  if (!o) return RBF_ERR_INVALID_VALUE;
+  int e = 0;
+  cudaError_t st = cudaMemcpyAsync(&e, o->errw, sizeof(int), cudaMemcpyDeviceToHost, o->stream);
+  if (st == cudaSuccess) st = cudaStreamSynchronize(o->stream);
+  if (st == cudaSuccess && e != 0) st = cudaMemsetAsync(o->errw, 0, 4 * sizeof(int), o->stream);
+  if (st != cudaSuccess) return cuda_fail(o, st);
+  return e ? RBF_ERR_TIMEOUT : RBF_OK;
+}
+
+rbf_status rbf_ops_inject_host_fault(rbf_ops* o, int32_t count) {
+  if (!o || count < 0) return RBF_ERR_INVALID_VALUE;
+  o->fault_count = count;
+  return RBF_OK;
+}
+
+rbf_status quantize_rows_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t ld_x, int64_t rows,
+                                int32_t cols, int8_t* d_q, int64_t ld_q, float* d_scale) {
+  if (!o || !float_dtype(x_dtype) || rows < 0 || cols < 0 || rows > INT32_MAX) return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  if (!matrix_ok(d_x, dtype_bytes(x_dtype), rows, cols, ld_x) || !matrix_ok(d_q, 1, rows, cols, ld_q))
+    return RBF_ERR_INVALID_VALUE;
+  if (rows == 0) return RBF_OK;
+  if (!d_scale || !aligned(d_scale, 4)) return RBF_ERR_INVALID_VALUE;
+  QuantizeLaunch a;
+  a.x = d_x;
+  a.dtype = x_dtype;
+  a.ld_x = ld_x;
+  a.rows = rows;
+  a.cols = cols;
+  a.q = d_q;
+  a.ld_q = ld_q;
+  a.scale = d_scale;
+  OPS_LAUNCH(o, launch_quantize_rows(a, o->stream));
+  return RBF_OK;
+}
+
+rbf_status matmul_i8_dev(rbf_ops* o, const int8_t* d_a, int64_t ld_a, const float* d_a_scale, const int8_t* d_b,
+                         int64_t ld_b, const float* d_b_scale, const float* d_bias, void* d_out, rbf_dtype out_dtype,
+                         int64_t ld_out, int64_t m, int64_t n, int32_t k) {
+  if (!o || !(float_dtype(out_dtype) || out_dtype == RBF_DTYPE_I32)) return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  MatmulI8Launch a;
+  a.a = d_a;
+  a.ld_a = ld_a;
+  a.a_scale = d_a_scale;
+  a.b = d_b;
+  a.ld_b = ld_b;
+  a.b_scale = d_b_scale;
+  a.bias = d_bias;
+  a.out = d_out;
+  a.out_dtype = out_dtype;
+  a.ld_out = ld_out;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  if (rbf_status st = check_matmul(o, a)) return st;
+  if (!matrix_ok(d_a, 1, m, k, ld_a)) return RBF_ERR_INVALID_VALUE;
+  if (out_dtype == RBF_DTYPE_I32 && (d_a_scale || d_b_scale || d_bias)) return RBF_ERR_INVALID_VALUE;
+  if (m == 0 || n == 0) return RBF_OK;
+  return run_matmul(o, a);
+}
+
+rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t ld_x, const int8_t* d_w,
+                         int64_t ld_w, const float* d_w_scale, const float* d_bias, void* d_out, rbf_dtype out_dtype,
+                         int64_t ld_out, int64_t m, int64_t n, int32_t k) {
+  if (!o || !float_dtype(x_dtype) || !float_dtype(out_dtype)) return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  MatmulI8Launch a;
+  a.a = o->rows_i8;
+  a.ld_a = o->row_pitch;
+  a.a_scale = o->row_scale;
+  a.b = d_w;
+  a.ld_b = ld_w;
+  a.b_scale = d_w_scale;
+  a.bias = d_bias;
+  a.out = d_out;
+  a.out_dtype = out_dtype;
+  a.ld_out = ld_out;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  if (rbf_status st = check_matmul(o, a)) return st;
+  if (!matrix_ok(d_x, dtype_bytes(x_dtype), m, k, ld_x)) return RBF_ERR_INVALID_VALUE;
+  if (m == 0 || n == 0) return RBF_OK;
+  QuantizeLaunch q;
+  q.x = d_x;
+  q.dtype = x_dtype;
+  q.ld_x = ld_x;
+  q.rows = m;
+  q.cols = k;
+  q.q = o->rows_i8;
+  q.ld_q = o->row_pitch;
+  q.scale = o->row_scale;
+  OPS_LAUNCH(o, launch_quantize_rows(q, o->stream));
+  return run_matmul(o, a);
+}
+
+rbf_status sample_dev(rbf_ops* o, const void* d_logits, rbf_dtype dtype, int64_t ld, int64_t rows, int32_t vocab,
+                      const float* d_u, const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                      const float* d_min_p, int32_t* d_token, float* d_logprob) {
+  if (!o || !float_dtype(dtype) || rows < 0 || rows > INT32_MAX || vocab < 0 || vocab > RBF_OPS_MAX_VOCAB)
+    return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  if (!matrix_ok(d_logits, dtype_bytes(dtype), rows, vocab, ld)) return RBF_ERR_INVALID_VALUE;
+  if (rows == 0) return RBF_OK;
+  if (!d_u || !d_token || !floats_ok(d_u) || !floats_ok(d_temperature) || !floats_ok(d_top_k) || !floats_ok(d_top_p) ||
+      !floats_ok(d_min_p) || !floats_ok(d_token) || !floats_ok(d_logprob))
+    return RBF_ERR_INVALID_VALUE;
+  SampleLaunch a;
+  a.logits = d_logits;
+  a.dtype = dtype;
+  a.ld = ld;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.u = d_u;
+  a.temperature = d_temperature;
+  a.top_k = d_top_k;
+  a.top_p = d_top_p;
+  a.min_p = d_min_p;
+  a.token = d_token;
+  a.logprob = d_logprob;
+  OPS_LAUNCH(o, launch_sample(a, o->stream));
+  return RBF_OK;
+}
+
+}  // extern "C"

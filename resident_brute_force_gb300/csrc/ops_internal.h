@@ -1,0 +1,66 @@
+// ops_internal.h -- host-side launch interfaces between the translation units
+// of the scoring-head operators. Not part of the public ABI (include/rbf_ops.h).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace rbf {
+
+// Element types of floating-point tensors (the values of rbf_dtype).
+constexpr int kF32 = 0;
+constexpr int kBF16 = 1;
+constexpr int kF16 = 2;
+constexpr int kI32 = 3;
+
+inline int dtype_bytes(int dtype) { return dtype == kF32 || dtype == kI32 ? 4 : 2; }
+
+// Rows to 8-bit integers. The quantised row goes to `q` (int8, stride ld_q).
+struct QuantizeLaunch {
+  const void* x = nullptr;
+  int dtype = 0;
+  int64_t ld_x = 0;
+  int64_t rows = 0;
+  int cols = 0;
+  int8_t* q = nullptr;
+  int64_t ld_q = 0;
+  float* scale = nullptr;
+};
+cudaError_t launch_quantize_rows(const QuantizeLaunch& a, cudaStream_t stream);
+
+// out[i, j] = a_scale[i] * b_scale[j] * sum_k a[i, k] b[j, k] + bias[j].
+struct MatmulI8Launch {
+  const int8_t* a = nullptr;
+  int64_t ld_a = 0;
+  const float* a_scale = nullptr;
+  const int8_t* b = nullptr;
+  int64_t ld_b = 0;
+  const float* b_scale = nullptr;
+  const float* bias = nullptr;
+  void* out = nullptr;
+  int out_dtype = 0;
+  int64_t ld_out = 0;
+  int64_t m = 0;
+  int64_t n = 0;
+  int k = 0;
+};
+// Any strides and alignments.
+cudaError_t launch_matmul_i8_any(const MatmulI8Launch& a, cudaStream_t stream);
+
+struct SampleLaunch {
+  const void* logits = nullptr;
+  int dtype = 0;
+  int64_t ld = 0;
+  int64_t rows = 0;
+  int vocab = 0;
+  const float* u = nullptr;
+  const float* temperature = nullptr;
+  const int32_t* top_k = nullptr;
+  const float* top_p = nullptr;
+  const float* min_p = nullptr;
+  int32_t* token = nullptr;
+  float* logprob = nullptr;
+};
+cudaError_t launch_sample(const SampleLaunch& a, cudaStream_t stream);
+
+}  // namespace rbf

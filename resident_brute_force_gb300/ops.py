@@ -1,0 +1,191 @@
+"""ctypes binding of the scoring-head operators (include/rbf_ops.h), argument
+marshalling only: 8-bit row quantisation, the 8-bit integer product with a
+scale for each token and channel, a linear layer on 8-bit weights, and
+sampling from scores. All of it runs in the library's CUDA kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _binding
+from ._binding import RBF_OK, RbfError, _dev_ptr, _need, load_library
+
+RBF_DTYPE_F32 = 0
+RBF_DTYPE_BF16 = 1
+RBF_DTYPE_F16 = 2
+RBF_DTYPE_I32 = 3
+RBF_OPS_MAX_DEPTH = 65536
+RBF_OPS_MAX_VOCAB = 1 << 26
+
+_P = ctypes.c_void_p
+_I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+_S = ctypes.c_int
+_binding.SIGNATURES.update({
+    "rbf_ops_create": (_S, [_I64, _I32, _P, ctypes.POINTER(_P)]),
+    "rbf_ops_destroy": (_S, [_P]),
+    "rbf_ops_stream": (_P, [_P]),
+    "rbf_ops_last_cuda_error": (_I32, [_P]),
+    "rbf_ops_last_launches": (_I32, [_P]),
+    "rbf_ops_check_device_error": (_S, [_P]),
+    "rbf_ops_inject_host_fault": (_S, [_P, _I32]),
+    "quantize_rows_i8_dev": (_S, [_P, _P, _S, _I64, _I64, _I32, _P, _I64, _P]),
+    "matmul_i8_dev": (_S, [_P, _P, _I64, _P, _P, _I64, _P, _P, _P, _S, _I64, _I64, _I64, _I32]),
+    "linear_i8_dev": (_S, [_P, _P, _S, _I64, _P, _I64, _P, _P, _P, _S, _I64, _I64, _I64, _I32]),
+    "sample_dev": (_S, [_P, _P, _S, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
+})
+
+_STREAM_LEGACY = 1  # cudaStreamLegacy: the default stream, named explicitly
+_DTYPES: dict = {}
+
+
+def _dtype(t, what: str, integers: bool = False) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: RBF_DTYPE_F32, torch.bfloat16: RBF_DTYPE_BF16, torch.float16: RBF_DTYPE_F16,
+                        torch.int32: RBF_DTYPE_I32})
+    code = _DTYPES.get(t.dtype)
+    if code is None or (code == RBF_DTYPE_I32 and not integers):
+        raise TypeError(f"{what} is {t.dtype}: expected float32, bfloat16 or float16"
+                        + (" or int32" if integers else ""))
+    return code
+
+
+def _matrix(t, what: str) -> tuple[int, int]:
+    """Device pointer and row stride of a 2-D CUDA tensor with contiguous rows."""
+    _need(t.dim() == 2, f"{what} is a 2-D tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    rows, cols = t.shape
+    _need(cols <= 1 or t.stride(1) == 1, f"{what}: the values of a row must be contiguous")
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    _need(ld >= cols, f"{what}: rows overlap")
+    return t.data_ptr(), ld
+
+
+def _i8(t, what: str):
+    import torch
+    if t.dtype != torch.int8:
+        raise TypeError(f"{what} is {t.dtype}: expected int8")
+    return _matrix(t, what)
+
+
+def _vector(t, count: int, what: str, dtype: str = "float32", optional: bool = True):
+    if t is None:
+        _need(optional, f"{what} is required")
+        return None
+    _need(t.numel() == count, f"{what} has {t.numel()} entries, expected {count}")
+    return _dev_ptr(t, dtype)
+
+
+class Ops:
+    """A handle with its stream and workspace (``rbf_ops_create``): products of
+    up to ``max_rows`` rows of up to ``max_depth`` values. Like an engine, one
+    handle serves one call at a time; every call is enqueued on the handle's
+    stream (``stream``: a torch stream or a raw handle; None: a stream of its
+    own). Outputs are given by the caller; a tensor used here must not be
+    handed to another stream before this one has reached the call."""
+
+    def __init__(self, max_rows: int, max_depth: int, stream=None):
+        self.lib = load_library()
+        s = None
+        if stream is not None:
+            s = (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) or _STREAM_LEGACY
+        handle = ctypes.c_void_p()
+        st = self.lib.rbf_ops_create(int(max_rows), int(max_depth), ctypes.c_void_p(s) if s else None,
+                                     ctypes.byref(handle))
+        if st != RBF_OK:
+            raise RbfError(st, "rbf_ops_create")
+        self._h = handle
+        self._stream_ref = stream
+
+    # -- lifetime
+    def close(self) -> None:
+        if getattr(self, "_h", None):
+            self.lib.rbf_ops_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def _check(self, st: int, where: str) -> None:
+        if st != RBF_OK:
+            raise RbfError(st, where, self.lib.rbf_ops_last_cuda_error(self._h))
+
+    # -- info
+    @property
+    def stream_handle(self) -> int:
+        return self.lib.rbf_ops_stream(self._h) or 0
+
+    @property
+    def last_launches(self) -> int:
+        """Kernels the most recent call enqueued."""
+        return self.lib.rbf_ops_last_launches(self._h)
+
+    def check_device_error(self) -> int:
+        """Wait for the stream; the status its kernels reported since the last check."""
+        return self.lib.rbf_ops_check_device_error(self._h)
+
+    def inject_host_fault(self, count: int) -> None:
+        self._check(self.lib.rbf_ops_inject_host_fault(self._h, int(count)), "rbf_ops_inject_host_fault")
+
+    # -- operators
+    def quantize_rows_i8_dev(self, d_x, d_q, d_scale) -> None:
+        """Rows of d_x [rows, cols] (float32, bfloat16 or float16) to int8 d_q with one scale a row in d_scale."""
+        x, ld_x = _matrix(d_x, "d_x")
+        q, ld_q = _i8(d_q, "d_q")
+        rows, cols = d_x.shape
+        _need(tuple(d_q.shape) == (rows, cols), f"d_q is {tuple(d_q.shape)}, d_x is {(rows, cols)}")
+        self._check(self.lib.quantize_rows_i8_dev(self._h, x, _dtype(d_x, "d_x"), ld_x, rows, cols, q, ld_q,
+                                                  _vector(d_scale, rows, "d_scale", optional=False)),
+                    "quantize_rows_i8_dev")
+
+    def matmul_i8_dev(self, d_a, d_a_scale, d_b, d_b_scale, d_out, bias=None) -> None:
+        """d_out [m, n] = d_a [m, k] times d_b [n, k] transposed, both int8, each row of either with its scale (None:
+        1), plus bias [n]. An int32 d_out takes the sums themselves, without scales or bias."""
+        a, ld_a = _i8(d_a, "d_a")
+        b, ld_b = _i8(d_b, "d_b")
+        out, ld_out = _matrix(d_out, "d_out")
+        (m, k), n = d_a.shape, d_b.shape[0]
+        _need(d_b.shape[1] == k, f"d_a has {k} columns, d_b {d_b.shape[1]}")
+        _need(tuple(d_out.shape) == (m, n), f"d_out is {tuple(d_out.shape)}, expected {(m, n)}")
+        self._check(self.lib.matmul_i8_dev(self._h, a, ld_a, _vector(d_a_scale, m, "d_a_scale"), b, ld_b,
+                                           _vector(d_b_scale, n, "d_b_scale"), _vector(bias, n, "bias"), out,
+                                           _dtype(d_out, "d_out", integers=True), ld_out, m, n, k), "matmul_i8_dev")
+
+    def linear_i8_dev(self, d_x, d_w, d_w_scale, d_out, bias=None) -> None:
+        """d_out [m, n] = d_x [m, k] (quantised by rows) times the int8 weights d_w [n, k] transposed, times the
+        weights' row scales d_w_scale (None: 1), plus bias [n]."""
+        x, ld_x = _matrix(d_x, "d_x")
+        w, ld_w = _i8(d_w, "d_w")
+        out, ld_out = _matrix(d_out, "d_out")
+        (m, k), n = d_x.shape, d_w.shape[0]
+        _need(d_w.shape[1] == k, f"d_x has {k} columns, d_w {d_w.shape[1]}")
+        _need(tuple(d_out.shape) == (m, n), f"d_out is {tuple(d_out.shape)}, expected {(m, n)}")
+        self._check(self.lib.linear_i8_dev(self._h, x, _dtype(d_x, "d_x"), ld_x, w, ld_w,
+                                           _vector(d_w_scale, n, "d_w_scale"), _vector(bias, n, "bias"), out,
+                                           _dtype(d_out, "d_out"), ld_out, m, n, k), "linear_i8_dev")
+
+    def sample_dev(self, d_logits, d_u, d_token, d_logprob=None, temperature=None, top_k=None, top_p=None,
+                   min_p=None) -> None:
+        """One index a row of d_logits [rows, vocab] into d_token (int32; -1 where every score is -infinity), and the
+        log of its share into d_logprob. d_u: one random number in [0, 1) a row; temperature, top_p and min_p (float32)
+        and top_k (int32): one entry a row, or None."""
+        x, ld = _matrix(d_logits, "d_logits")
+        rows, vocab = d_logits.shape
+        self._check(self.lib.sample_dev(self._h, x, _dtype(d_logits, "d_logits"), ld, rows, vocab,
+                                        _vector(d_u, rows, "d_u", optional=False),
+                                        _vector(temperature, rows, "temperature"),
+                                        _vector(top_k, rows, "top_k", "int32"), _vector(top_p, rows, "top_p"),
+                                        _vector(min_p, rows, "min_p"),
+                                        _vector(d_token, rows, "d_token", "int32", optional=False),
+                                        _vector(d_logprob, rows, "d_logprob")), "sample_dev")

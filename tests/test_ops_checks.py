@@ -1,0 +1,109 @@
+"""Refusals of the scoring-head operators, on the CPU: the binding refuses
+misshapen, mistyped and overlapping arguments before any pointer reaches the
+library, and the C entry points refuse bad sizes without a GPU call."""
+import ctypes
+
+import pytest
+import torch
+
+import resident_brute_force_gb300 as rbf
+from resident_brute_force_gb300 import ops as binding
+
+
+class _Cuda:
+    """A tensor's shape, type and strides with is_cuda set, for checks that come before any use of the data."""
+
+    def __init__(self, t):
+        self._t = t
+        self.is_cuda = True
+        self.shape, self.dtype = t.shape, t.dtype
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+class _NoLibrary:
+    def __getattr__(self, name):
+        def reached(*args):
+            raise AssertionError(f"{name} reached the library")
+        return reached
+
+
+@pytest.fixture
+def ops():
+    o = object.__new__(rbf.Ops)
+    o.lib, o._h = _NoLibrary(), None
+    return o
+
+
+def i8(*shape):
+    return _Cuda(torch.zeros(*shape, dtype=torch.int8))
+
+
+def f32(*shape):
+    return _Cuda(torch.zeros(*shape))
+
+
+def i32(*shape):
+    return _Cuda(torch.zeros(*shape, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("call", [
+    lambda o: o.quantize_rows_i8_dev(f32(3, 4), i8(3, 5), f32(3)),
+    lambda o: o.quantize_rows_i8_dev(f32(3, 4), i8(3, 4), f32(2)),
+    lambda o: o.quantize_rows_i8_dev(f32(12), i8(3, 4), f32(3)),
+    lambda o: o.quantize_rows_i8_dev(f32(3, 4), i8(3, 4), None),
+    lambda o: o.quantize_rows_i8_dev(_Cuda(torch.zeros(4, 3).t()), i8(3, 4), f32(3)),
+    lambda o: o.quantize_rows_i8_dev(_Cuda(torch.zeros(1, 4).expand(3, 4)), i8(3, 4), f32(3)),
+    lambda o: o.matmul_i8_dev(i8(2, 8), None, i8(3, 9), None, f32(2, 3)),
+    lambda o: o.matmul_i8_dev(i8(2, 8), None, i8(3, 8), None, f32(3, 2)),
+    lambda o: o.matmul_i8_dev(i8(2, 8), f32(3), i8(3, 8), None, f32(2, 3)),
+    lambda o: o.matmul_i8_dev(i8(2, 8), None, i8(3, 8), f32(2), f32(2, 3)),
+    lambda o: o.matmul_i8_dev(i8(2, 8), None, i8(3, 8), None, f32(2, 3), bias=f32(4)),
+    lambda o: o.linear_i8_dev(f32(2, 8), i8(3, 7), None, f32(2, 3)),
+    lambda o: o.linear_i8_dev(f32(2, 8), i8(3, 8), None, f32(2, 4)),
+    lambda o: o.sample_dev(f32(2, 8), f32(3), i32(2)),
+    lambda o: o.sample_dev(f32(2, 8), f32(2), i32(3)),
+    lambda o: o.sample_dev(f32(2, 8), None, i32(2)),
+    lambda o: o.sample_dev(f32(2, 8), f32(2), i32(2), f32(1)),
+    lambda o: o.sample_dev(f32(2, 8), f32(2), i32(2), top_k=i32(1)),
+    lambda o: o.sample_dev(f32(16), f32(2), i32(2)),
+])
+def test_shapes_are_refused(ops, call):
+    with pytest.raises(ValueError):
+        call(ops)
+
+
+@pytest.mark.parametrize("call", [
+    lambda o: o.quantize_rows_i8_dev(i8(3, 4), i8(3, 4), f32(3)),
+    lambda o: o.quantize_rows_i8_dev(f32(3, 4), f32(3, 4), f32(3)),
+    lambda o: o.quantize_rows_i8_dev(torch.zeros(3, 4), i8(3, 4), f32(3)),
+    lambda o: o.matmul_i8_dev(f32(2, 8), None, i8(3, 8), None, f32(2, 3)),
+    lambda o: o.matmul_i8_dev(i8(2, 8), None, f32(3, 8), None, f32(2, 3)),
+    lambda o: o.matmul_i8_dev(i8(2, 8), None, i8(3, 8), None, i8(2, 3)),
+    lambda o: o.linear_i8_dev(i8(2, 8), i8(3, 8), None, f32(2, 3)),
+    lambda o: o.linear_i8_dev(f32(2, 8), i8(3, 8), None, i32(2, 3)),
+    lambda o: o.sample_dev(i32(2, 8), f32(2), i32(2)),
+    lambda o: o.sample_dev(f32(2, 8), f32(2), f32(2)),
+    lambda o: o.sample_dev(f32(2, 8), f32(2), i32(2), top_k=f32(2)),
+])
+def test_types_are_refused(ops, call):
+    with pytest.raises(TypeError):
+        call(ops)
+
+
+def test_c_entry_points_refuse_without_a_handle():
+    from resident_brute_force_gb300 import _build
+    _build.build()
+    lib = rbf.load_library()
+    bad = rbf.RBF_ERR_INVALID_VALUE
+    assert lib.rbf_ops_create(1, 1, None, None) == bad
+    h = ctypes.c_void_p()
+    for rows, depth in ((0, 1), (1, 0), (-1, 5), ((1 << 20) + 1, 1), (1, binding.RBF_OPS_MAX_DEPTH + 1)):
+        assert lib.rbf_ops_create(rows, depth, None, ctypes.byref(h)) == bad and not h.value
+    assert lib.rbf_ops_destroy(None) == rbf.RBF_OK
+    assert lib.rbf_ops_check_device_error(None) == bad
+    assert lib.quantize_rows_i8_dev(None, 16, 0, 4, 1, 4, 16, 4, 16) == bad
+    assert lib.matmul_i8_dev(None, 16, 4, None, 16, 4, None, None, 16, 0, 4, 1, 4, 4) == bad
+    assert lib.linear_i8_dev(None, 16, 0, 4, 16, 4, None, None, 16, 0, 4, 1, 4, 4) == bad
+    assert lib.sample_dev(None, 16, 0, 4, 1, 4, 16, None, None, None, None, 16, None) == bad
