@@ -25,10 +25,12 @@ struct rbf_ops {
   int64_t max_rows = 0;
   int max_depth = 0;
 
-  int8_t* rows_i8 = nullptr;  // linear_i8_dev: the quantised rows, max_rows x row_pitch
-  float* row_scale = nullptr;
-  int64_t row_pitch = 0;
-  int* errw = nullptr;  // error bits of the kernels since the last check
+  void* rows_f16 = nullptr;      // the product's first operand in fp16, max_rows x matmul_i8_pitch(max_depth)
+  float* row_scale = nullptr;    // linear_i8_dev: the rows' scales
+  int* partial = nullptr;        // the product's partial sums of shared tiles
+  unsigned* arrived = nullptr;   // and their counters
+  int* errw = nullptr;           // error bits of the kernels since the last check
+  uint64_t timeout_ns = 2000000000ull;  // bound on every device-side wait
 
   int last_cuda_error = 0;
   int launches = 0;
@@ -55,8 +57,10 @@ rbf_status cuda_fail(rbf_ops* o, cudaError_t err) {
 
 void release(rbf_ops* o) {
   if (o->stream) cudaStreamSynchronize(o->stream);
-  cudaFree(o->rows_i8);
+  cudaFree(o->rows_f16);
   cudaFree(o->row_scale);
+  cudaFree(o->partial);
+  cudaFree(o->arrived);
   cudaFree(o->errw);
   if (o->own_stream && o->stream) cudaStreamDestroy(o->stream);
   delete o;
@@ -86,9 +90,15 @@ rbf_status check_matmul(const rbf_ops* o, const MatmulI8Launch& a) {
   return RBF_OK;
 }
 
-rbf_status run_matmul(rbf_ops* o, const MatmulI8Launch& a) {
-  OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
-  return RBF_OK;
+MatmulI8Workspace workspace(rbf_ops* o) {
+  MatmulI8Workspace w;
+  w.rows_f16 = o->rows_f16;
+  w.partial = o->partial;
+  w.arrived = o->arrived;
+  w.err = o->errw;
+  w.num_sms = o->num_sms;
+  w.timeout_ns = o->timeout_ns;
+  return w;
 }
 
 }  // namespace
@@ -109,7 +119,6 @@ rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream
   }
   o->max_rows = max_rows;
   o->max_depth = max_depth;
-  o->row_pitch = (int64_t(max_depth) + 15) / 16 * 16;
   if (cuda_stream) {
     o->stream = static_cast<cudaStream_t>(cuda_stream);
   } else {
@@ -119,7 +128,9 @@ rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream
     }
     o->own_stream = true;
   }
-  const bool ok = cudaMalloc(&o->rows_i8, static_cast<size_t>(max_rows) * o->row_pitch) == cudaSuccess &&
+  const bool ok = cudaMalloc(&o->rows_f16, static_cast<size_t>(max_rows) * matmul_i8_pitch(max_depth) * 2) == cudaSuccess &&
+                  cudaMalloc(&o->partial, matmul_i8_partial_bytes(o->num_sms)) == cudaSuccess &&
+                  cudaMalloc(&o->arrived, o->num_sms * sizeof(unsigned)) == cudaSuccess &&
                   cudaMalloc(&o->row_scale, static_cast<size_t>(max_rows) * sizeof(float)) == cudaSuccess &&
                   cudaMalloc(&o->errw, 4 * sizeof(int)) == cudaSuccess;
   if (!ok) {
@@ -128,6 +139,7 @@ rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream
     return RBF_ERR_OUT_OF_MEMORY;
   }
   if (cudaMemsetAsync(o->errw, 0, 4 * sizeof(int), o->stream) != cudaSuccess ||
+      cudaMemsetAsync(o->arrived, 0, o->num_sms * sizeof(unsigned), o->stream) != cudaSuccess ||
       cudaStreamSynchronize(o->stream) != cudaSuccess) {
     release(o);
     return RBF_ERR_CUDA;
@@ -150,7 +162,11 @@ rbf_status rbf_ops_check_device_error(rbf_ops* o) {
   int e = 0;
   cudaError_t st = cudaMemcpyAsync(&e, o->errw, sizeof(int), cudaMemcpyDeviceToHost, o->stream);
   if (st == cudaSuccess) st = cudaStreamSynchronize(o->stream);
-  if (st == cudaSuccess && e != 0) st = cudaMemsetAsync(o->errw, 0, 4 * sizeof(int), o->stream);
+  if (st == cudaSuccess && e != 0) {
+    st = cudaMemsetAsync(o->errw, 0, 4 * sizeof(int), o->stream);
+    // A launch that gave up may have left counters behind.
+    if (st == cudaSuccess) st = cudaMemsetAsync(o->arrived, 0, o->num_sms * sizeof(unsigned), o->stream);
+  }
   if (st != cudaSuccess) return cuda_fail(o, st);
   return e ? RBF_ERR_TIMEOUT : RBF_OK;
 }
@@ -205,7 +221,13 @@ rbf_status matmul_i8_dev(rbf_ops* o, const int8_t* d_a, int64_t ld_a, const floa
   if (!matrix_ok(d_a, 1, m, k, ld_a)) return RBF_ERR_INVALID_VALUE;
   if (out_dtype == RBF_DTYPE_I32 && (d_a_scale || d_b_scale || d_bias)) return RBF_ERR_INVALID_VALUE;
   if (m == 0 || n == 0) return RBF_OK;
-  return run_matmul(o, a);
+  if (!matmul_i8_tc_fits(a)) {
+    OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
+    return RBF_OK;
+  }
+  OPS_LAUNCH(o, launch_expand_rows(d_a, ld_a, m, k, o->rows_f16, o->num_sms, o->stream));
+  OPS_LAUNCH(o, launch_matmul_i8_tc(a, workspace(o), o->stream));
+  return RBF_OK;
 }
 
 rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t ld_x, const int8_t* d_w,
@@ -214,8 +236,8 @@ rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t
   if (!o || !float_dtype(x_dtype) || !float_dtype(out_dtype)) return RBF_ERR_INVALID_VALUE;
   o->launches = 0;
   MatmulI8Launch a;
-  a.a = o->rows_i8;
-  a.ld_a = o->row_pitch;
+  a.a = static_cast<const int8_t*>(o->rows_f16);
+  a.ld_a = matmul_i8_pitch(k);
   a.a_scale = o->row_scale;
   a.b = d_w;
   a.ld_b = ld_w;
@@ -236,11 +258,20 @@ rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t
   q.ld_x = ld_x;
   q.rows = m;
   q.cols = k;
-  q.q = o->rows_i8;
-  q.ld_q = o->row_pitch;
   q.scale = o->row_scale;
+  if (!matmul_i8_tc_fits(a)) {
+    // The workspace holds the rows as bytes here, in half of its room.
+    q.q = static_cast<int8_t*>(o->rows_f16);
+    q.ld_q = a.ld_a;
+    OPS_LAUNCH(o, launch_quantize_rows(q, o->stream));
+    OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
+    return RBF_OK;
+  }
+  q.f16 = o->rows_f16;
+  q.f16_pitch = matmul_i8_pitch(k);
   OPS_LAUNCH(o, launch_quantize_rows(q, o->stream));
-  return run_matmul(o, a);
+  OPS_LAUNCH(o, launch_matmul_i8_tc(a, workspace(o), o->stream));
+  return RBF_OK;
 }
 
 rbf_status sample_dev(rbf_ops* o, const void* d_logits, rbf_dtype dtype, int64_t ld, int64_t rows, int32_t vocab,

@@ -15,7 +15,8 @@ constexpr int kI32 = 3;
 
 inline int dtype_bytes(int dtype) { return dtype == kF32 || dtype == kI32 ? 4 : 2; }
 
-// Rows to 8-bit integers. The quantised row goes to `q` (int8, stride ld_q).
+// Rows to 8-bit integers. The quantised row goes to `q` (int8, stride ld_q) or,
+// as fp16 numbers, to `f16` (stride f16_pitch, zero past the row).
 struct QuantizeLaunch {
   const void* x = nullptr;
   int dtype = 0;
@@ -24,6 +25,8 @@ struct QuantizeLaunch {
   int cols = 0;
   int8_t* q = nullptr;
   int64_t ld_q = 0;
+  void* f16 = nullptr;
+  int f16_pitch = 0;
   float* scale = nullptr;
 };
 cudaError_t launch_quantize_rows(const QuantizeLaunch& a, cudaStream_t stream);
@@ -46,6 +49,24 @@ struct MatmulI8Launch {
 };
 // Any strides and alignments.
 cudaError_t launch_matmul_i8_any(const MatmulI8Launch& a, cudaStream_t stream);
+
+// The tensor-core product. Its first operand is the workspace's fp16 rows
+// (launch_expand_rows or launch_quantize_rows writes them, enqueued just
+// before); a.a and a.ld_a are not used.
+struct MatmulI8Workspace {
+  void* rows_f16 = nullptr;     // [m][matmul_i8_pitch(k)]
+  int* partial = nullptr;       // matmul_i8_partial_bytes
+  unsigned* arrived = nullptr;  // num_sms counters, zero between launches
+  int* err = nullptr;
+  int num_sms = 0;
+  uint64_t timeout_ns = 0;
+};
+int matmul_i8_pitch(int k);  // fp16 numbers per workspace row
+size_t matmul_i8_partial_bytes(int num_sms);
+bool matmul_i8_tc_fits(const MatmulI8Launch& a);
+cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, void* rows_f16, int num_sms,
+                               cudaStream_t stream);
+cudaError_t launch_matmul_i8_tc(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t stream);
 
 struct SampleLaunch {
   const void* logits = nullptr;

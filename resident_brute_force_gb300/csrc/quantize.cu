@@ -70,39 +70,158 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
   return whole;
 }
 
-// One CTA per row, any strides and alignments: two reads of the row, the
-// second from cache.
+// Where a row goes: bytes, or (f16 set) the fp16 rows of a product's
+// workspace, which are zero from the row's end to their pitch.
+struct Out {
+  int8_t* q;
+  int64_t ld_q;
+  __half* f16;
+  int pitch;
+  float* scale;
+};
+
+// One CTA per row, any strides, alignments and lengths: two reads of the row,
+// the second from cache.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_rows_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, int8_t* __restrict__ q,
-                         int64_t ld_q, float* __restrict__ scale) {
+    quantize_rows_any_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, const Out o) {
+  pdl_launch_dependents();  // a product may become resident now; it waits for these rows
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* row = x + r * ld_x;
     uint32_t top = 0;
     for (int j = threadIdx.x; j < cols; j += kQuantThreads)
       top = max(top, __float_as_uint(to_f32(row[j])) & 0x7FFFFFFFu);
     const RowScale s = row_scale(block_max(top));
-    for (int j = threadIdx.x; j < cols; j += kQuantThreads)
-      q[r * ld_q + j] = static_cast<int8_t>(quantize_one(to_f32(row[j]), s));
-    if (threadIdx.x == 0) scale[r] = s.scale;
+    if (o.f16) {
+      for (int j = threadIdx.x; j < o.pitch; j += kQuantThreads)
+        o.f16[r * o.pitch + j] = __float2half_rn(j < cols ? static_cast<float>(quantize_one(to_f32(row[j]), s)) : 0.0f);
+    } else {
+      for (int j = threadIdx.x; j < cols; j += kQuantThreads)
+        o.q[r * o.ld_q + j] = static_cast<int8_t>(quantize_one(to_f32(row[j]), s));
+    }
+    if (threadIdx.x == 0) o.scale[r] = s.scale;
     __syncthreads();  // block_max's shared words are used again
   }
 }
 
+// Eight values on a 16-byte boundary, zero from `live` on.
 template <typename T>
+__device__ __forceinline__ void load8(const T* p, int live, float (&x)[8]) {
+  if (live >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < live ? to_f32(p[i]) : 0.0f;
+  }
+}
+
+// THREADS threads a row (a warp up to 1,024 values, else the CTA up to 8,192),
+// which stays in registers: one read of it and one write, eight values a
+// thread at a time. Rows start on 16-byte boundaries, int8 rows on 8-byte ones.
+constexpr int kHeld = 4;  // groups of eight values a thread holds
+
+template <typename T, int THREADS, bool F16>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_rows_held_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, const Out o) {
+  pdl_launch_dependents();
+  constexpr int kRows = kQuantThreads / THREADS;
+  const int t = threadIdx.x % THREADS;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / THREADS;
+  if (kRows > 1 && r >= rows) return;  // whole warps
+  const T* row = x + r * ld_x;
+  float v[kHeld][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int g = 0; g < kHeld; ++g) {
+    const int c = (g * THREADS + t) * 8;
+    if (c < cols) load8(row + c, cols - c, v[g]);
+  }
+#pragma unroll
+  for (int g = 0; g < kHeld; ++g)
+    if ((g * THREADS + t) * 8 < cols)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[g][i]) & 0x7FFFFFFFu);
+  const RowScale s = row_scale(THREADS == 32 ? __reduce_max_sync(kFullMask, top) : block_max(top));
+  if (t == 0) o.scale[r] = s.scale;
+  const int end = F16 ? o.pitch : cols;
+#pragma unroll
+  for (int g = 0; g < kHeld; ++g) {
+    const int c = (g * THREADS + t) * 8;
+    if (c >= end) break;
+    // Rounded to whole numbers by adding and subtracting 1.5 * 2^23.
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i] = c < cols && s.inv != 0.0f ? __fadd_rn(__fmul_rn(__fmul_rn(v[g][i], s.pre), s.inv), 12582912.0f) : 12582912.0f;
+    if constexpr (F16) {
+      __half2 h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[i] = __floats2half2_rn(__fsub_rn(q[2 * i], 12582912.0f), __fsub_rn(q[2 * i + 1], 12582912.0f));
+      *reinterpret_cast<uint4*>(o.f16 + r * o.pitch + c) = *reinterpret_cast<const uint4*>(h);
+    } else {
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // the low byte of each sum is the number
+        const uint32_t lo = __byte_perm(__float_as_uint(q[4 * i]), __float_as_uint(q[4 * i + 1]), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(q[4 * i + 2]), __float_as_uint(q[4 * i + 3]), 0x0040);
+        w[i] = __byte_perm(lo, hi, 0x5410);
+      }
+      int8_t* dst = o.q + r * o.ld_q + c;
+      if (c + 8 <= cols) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) dst[i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
+      }
+    }
+  }
+}
+
+template <typename T, bool F16>
 cudaError_t launch_t(const QuantizeLaunch& a, cudaStream_t st) {
-  const int64_t grid = std::min<int64_t>(a.rows, int64_t(1) << 20);
-  quantize_rows_kernel<T><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(
-      static_cast<const T*>(a.x), a.ld_x, a.rows, a.cols, a.q, a.ld_q, a.scale);
+  Out o;
+  o.q = a.q;
+  o.ld_q = a.ld_q;
+  o.f16 = static_cast<__half*>(a.f16);
+  o.pitch = a.f16_pitch;
+  o.scale = a.scale;
+  const T* x = static_cast<const T*>(a.x);
+  const bool aligned = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.ld_x * sizeof(T)) % 16 == 0 &&
+                       (F16 || ((reinterpret_cast<uintptr_t>(a.q) & 7) == 0 && a.ld_q % 8 == 0));
+  const int width = F16 ? a.f16_pitch : a.cols;
+  if (aligned && width <= 32 * 8 * kHeld) {
+    const int64_t grid = (a.rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+    quantize_rows_held_kernel<T, 32, F16><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
+  } else if (aligned && width <= kQuantThreads * 8 * kHeld) {
+    quantize_rows_held_kernel<T, kQuantThreads, F16><<<static_cast<unsigned>(a.rows), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
+  } else {
+    const int64_t grid = std::min<int64_t>(a.rows, int64_t(1) << 20);
+    quantize_rows_any_kernel<T><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
+  }
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_to(const QuantizeLaunch& a, cudaStream_t st) {
+  return a.f16 ? launch_t<T, true>(a, st) : launch_t<T, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_rows(const QuantizeLaunch& a, cudaStream_t st) {
-  if (a.dtype == kF32) return launch_t<float>(a, st);
-  if (a.dtype == kBF16) return launch_t<__nv_bfloat16>(a, st);
-  return launch_t<__half>(a, st);
+  if (a.dtype == kF32) return launch_to<float>(a, st);
+  if (a.dtype == kBF16) return launch_to<__nv_bfloat16>(a, st);
+  return launch_to<__half>(a, st);
 }
 
 }  // namespace rbf
