@@ -32,8 +32,7 @@ __device__ __forceinline__ void store_out(const Epilogue& e, int64_t i, int64_t 
   }
   float v = __int2float_rn(sum);
   if (e.a_scale) v = __fmul_rn(v, e.a_scale[i]);
-  if (e.b_scale) v = __fmul_rn(v, e.b_scale[j]);
-  if (e.bias) v = __fadd_rn(v, e.bias[j]);
+  v = __fmaf_rn(v, e.b_scale ? e.b_scale[j] : 1.0f, e.bias ? e.bias[j] : 0.0f);
   if (e.out_dtype == kF32)
     static_cast<float*>(e.out)[at] = v;
   else if (e.out_dtype == kBF16)

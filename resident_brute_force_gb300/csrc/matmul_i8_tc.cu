@@ -24,15 +24,16 @@
 //   warp 0      loads the CTA's 128 channels x 128 bytes per stage (TMA, 128-
 //               byte swizzle, 16 KB) into a ring of its own, deep enough to
 //               cover HBM's latency at full rate;
-//   warps 2-9   two groups of four; a group takes every other stage. A thread
+//   warps 2-17  four groups of four; a group takes every fourth stage. A thread
 //               reads its channel's 128 bytes (conflict-free: the swizzle),
 //               turns four bytes into two fp16 pairs with two byte permutes
 //               (0x6400 | b is 1024 + b) and two subtractions, and stores them
-//               in its TMEM lane: 64 columns a stage, a ring of four;
-//   warp 10     loads the CTA's tokens (TMA) into a ring of four stages;
+//               in its TMEM lane: 64 columns a stage, a ring of 4 to 7 in
+//               the columns that the accumulator leaves;
+//   warp 18     loads the CTA's tokens (TMA) into a ring of as many stages;
 //   warp 1      one thread of the even CTA issues the pair's MMAs.
-// At the end of a tile (and every 1,024 values) warps 2-9 read the accumulator,
-// after they have converted the next four stages, so that the MMAs of the next
+// At the end of a tile (and every 1,024 values) warps 2-17 read the accumulator,
+// after they have converted the next ring of stages, so that the MMAs of the next
 // tile run while the last one's results are scaled and stored.
 //
 // Work is dealt out in tiles, or, where there are few tiles per pair, in equal
@@ -56,20 +57,23 @@ constexpr int kDepth = 128;          // values of depth a stage
 constexpr int kChannels = 128;       // channels per CTA and tile
 constexpr int kPairChannels = 256;
 constexpr int kWBytes = kChannels * kDepth;
-constexpr int kRing = 4;             // stages of the token ring and of the TMEM ring
 constexpr int kExactStages = 1024 / kDepth;
-constexpr int kWorkers = 8;          // warps 2-9
+constexpr int kGroups = 4;           // of worker warps: a group takes every fourth stage
+constexpr int kWorkers = 4 * kGroups;
+constexpr int kXWarp = 2 + kWorkers;
 constexpr int kThreads = (2 + kWorkers + 1) * 32;
-constexpr int kTmemCols = 512;       // accumulator: columns 0-255; converted channels: 256-511
-constexpr int kTmemRing = 256;
+constexpr int kTmemCols = 512;       // the accumulator first, then the ring of converted channels
 constexpr int kStageCols = kDepth / 2;
 constexpr int kRingBudget = 224 * 1024;
 
 template <int NT>
 struct Shape {
   static constexpr int kXBytes = NT * kDepth;  // NT / 2 tokens x 128 fp16
+  static constexpr int kRing = (kTmemCols - NT) / kStageCols;  // stages of the token ring and of the TMEM ring
+  static constexpr int kCols = NT / kGroups;   // accumulator columns of one worker thread
   static constexpr int kWStages = (kRingBudget - kRing * kXBytes) / kWBytes;
   static constexpr int kSmem = 1024 + kRing * kXBytes + kWStages * kWBytes + (2 * kWStages + 3 * kRing + 4) * 8 + 16;
+  static_assert(kRing >= kGroups && kWStages >= kGroups, "a group needs a slot of its own");
 };
 
 struct Params {
@@ -82,7 +86,7 @@ struct Params {
   int out_dtype;
   int stages;        // per tile
   int token_tiles;
-  int64_t tiles;
+  int tiles;         // tiles x stages < 2^31
   int split;         // 1: equal shares of all stages, 0: whole tiles
   int read_once;     // 1: the channels are read once (one token tile)
   int* partial;      // split: two tiles of partial sums per CTA
@@ -93,29 +97,25 @@ struct Params {
 
 // The pair's part of the work, one tile's stages [k0, k1) at a time.
 struct Walk {
-  int64_t at, end;
-  int stages, step;
+  int at, end, stages, step;
   bool split;
 
   __device__ __forceinline__ Walk(const Params& p, int pair, int pairs) : stages(p.stages), step(pairs), split(p.split) {
-    if (split) {
-      const int64_t total = p.tiles * stages;
-      at = total * pair / pairs;
-      end = total * (pair + 1) / pairs;
-    } else {
-      at = pair;
-      end = p.tiles;
-    }
+    at = split ? share_start(p, pair, pairs) : pair;
+    end = split ? share_start(p, pair + 1, pairs) : p.tiles;
   }
-  __device__ __forceinline__ int64_t total() const {
+  static __device__ __forceinline__ int share_start(const Params& p, int pair, int pairs) {
+    return static_cast<int>(static_cast<int64_t>(p.tiles) * p.stages * pair / pairs);
+  }
+  __device__ __forceinline__ int total() const {
     return split ? end - at : (at < end ? (end - at + step - 1) / step * stages : 0);
   }
-  __device__ __forceinline__ bool next(int64_t& tile, int& k0, int& k1) {
+  __device__ __forceinline__ bool next(int& tile, int& k0, int& k1) {
     if (at >= end) return false;
     if (split) {
       tile = at / stages;
-      k0 = static_cast<int>(at - tile * stages);
-      k1 = static_cast<int>(min(static_cast<int64_t>(stages), k0 + (end - at)));
+      k0 = at - tile * stages;
+      k1 = min(stages, k0 + (end - at));
       at += k1 - k0;
     } else {
       tile = at;
@@ -161,31 +161,15 @@ __device__ __forceinline__ void umma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
-// Arrive on the even CTA's barrier once this warp's stores to TMEM are done.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-// mbar_wait for a barrier that the other CTA's threads arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (global_timer_ns() - t0 > timeout_ns) return false;
-  }
+      : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
@@ -197,17 +181,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -225,13 +212,101 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// What a worker warp multiplies its part of a tile by, read ahead of the sums:
+// lane l has the scale and bias of channel ch0 + l, and the scales of tokens
+// col0 + l, col0 + 32 + l ...
 template <int NT>
+struct Scales {
+  static constexpr int kWords = (Shape<NT>::kCols + 31) / 32;
+  float sa[kWords];
+  float sb, add;
+  int64_t j0, i0;
+  int live;    // tokens of this part that exist
+  bool mine;   // this lane's channel exists
+
+  __device__ __forceinline__ void read(const Params& p, int tile, int ch0, int col0, int lane) {
+    j0 = static_cast<int64_t>(tile / p.token_tiles) * kPairChannels + ch0;
+    i0 = static_cast<int64_t>(tile % p.token_tiles) * NT + col0;
+    live = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(Shape<NT>::kCols), p.m - i0)));
+    mine = j0 + lane < p.n;
+    sb = p.b_scale && mine ? p.b_scale[j0 + lane] : 1.0f;
+    add = p.bias && mine ? p.bias[j0 + lane] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) sa[i] = p.a_scale && 32 * i + lane < live ? p.a_scale[i0 + 32 * i + lane] : 1.0f;
+  }
+};
+
+// Scale and store a worker warp's part of a tile, fp32 sums as they are. 16-bit
+// results are exchanged between neighbouring lanes, so that a lane holds two
+// channels of one token: one 4-byte store for two results.
+template <int NT, bool OUT16>
+__device__ __forceinline__ void store_tile(const Params& p, const Scales<NT>& s, const uint32_t (&acc)[Shape<NT>::kCols], int lane) {
+  constexpr int kCols = Shape<NT>::kCols;
+  constexpr int kSlab = kCols < 16 ? kCols : 16;
+  if (s.j0 >= p.n || s.live == 0) return;
+  const int odd = lane & 1;
+  const bool paired = OUT16 && s.j0 + 32 <= p.n && p.ld_out % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
+#pragma unroll
+  for (int c0 = 0; c0 < kCols; c0 += kSlab) {
+    if (c0 >= s.live) break;
+    float v[kSlab];
+#pragma unroll
+    for (int c = 0; c < kSlab; ++c)
+      v[c] = __fmaf_rn(__fmul_rn(__uint_as_float(acc[c0 + c]), __shfl_sync(kFullMask, s.sa[c0 / 32], (c0 + c) & 31)), s.sb, s.add);
+    if constexpr (!OUT16) {
+      float* o = static_cast<float*>(p.out) + (s.i0 + c0) * p.ld_out + s.j0 + lane;
+#pragma unroll
+      for (int c = 0; c < kSlab; ++c)
+        if (s.mine && c0 + c < s.live) o[c * p.ld_out] = v[c];
+    } else {
+      uint32_t two[kSlab / 2];  // tokens c and c + 1 of this lane's channel
+#pragma unroll
+      for (int c = 0; c < kSlab; c += 2) {
+        if (p.out_dtype == kBF16) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
+          two[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __half2 h = __floats2half2_rn(v[c], v[c + 1]);
+          two[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      if (paired) {
+        const uint32_t pick = odd ? 0x3276u : 0x5410u;
+        uint32_t* o = static_cast<uint32_t*>(p.out) + ((s.i0 + c0 + odd) * p.ld_out + s.j0 + lane - odd) / 2;
+#pragma unroll
+        for (int c = 0; c < kSlab; c += 2) {
+          const uint32_t other = __shfl_xor_sync(kFullMask, two[c / 2], 1);
+          if (c0 + c + odd < s.live) o[c / 2 * p.ld_out] = __byte_perm(two[c / 2], other, pick);
+        }
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(p.out) + (s.i0 + c0) * p.ld_out + s.j0 + lane;
+#pragma unroll
+        for (int c = 0; c < kSlab; ++c)
+          if (s.mine && c0 + c < s.live) o[c * p.ld_out] = static_cast<uint16_t>(two[c / 2] >> (16 * (c & 1)));
+      }
+    }
+  }
+}
+
+// The integer sums themselves.
+template <int NT>
+__device__ __forceinline__ void store_sums(const Params& p, const Scales<NT>& s, const uint32_t (&acc)[Shape<NT>::kCols], int lane) {
+  int* o = static_cast<int*>(p.out) + s.i0 * p.ld_out + s.j0 + lane;
+#pragma unroll
+  for (int c = 0; c < Shape<NT>::kCols; ++c)
+    if (s.mine && c < s.live) o[c * p.ld_out] = static_cast<int>(acc[c]);
+}
+
+// OUT: what is stored: 0 the sums (int32), 1 fp32, 2 a 16-bit type.
+template <int NT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                           const Params p) {
   using S = Shape<NT>;
-  constexpr int kCols = NT / 2;  // accumulator columns of one worker thread
-  constexpr int kDrain = kCols < 32 ? kCols : 32;  // of those, read at a time
+  constexpr int kCols = S::kCols;
+  constexpr int kDrain = kCols < 16 ? kCols : 16;  // columns read at a time
+  constexpr int kRing = S::kRing;
+  constexpr bool kSums = OUT == 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* xring = smem;
@@ -260,11 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     for (int s = 0; s < S::kWStages; ++s) {
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_empty[s], kWorkers / 2);
+      mbar_init(&w_empty[s], 4);
     }
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&x_full[s], 1);
-      mbar_init(&c_full[s], kWorkers);  // four warps of each CTA
+      mbar_init(&c_full[s], 8);  // four warps of each CTA
       mbar_init(&done[s], 1);
     }
     mbar_init(acc_full, 1);
@@ -291,8 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   Walk walk(p, pair, pairs);
-  int64_t tile;
-  int k0, k1;
+  int tile, k0, k1;
 
   if (warp == 0) {
     // ---------------------------------------------------- channels (bytes)
@@ -304,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int armed = 0;
       bool ok = true;
       while (ok && walk.next(tile, k0, k1)) {
-        const int row = static_cast<int>(tile / p.token_tiles * kPairChannels) + static_cast<int>(rank) * kChannels;
+        const int row = tile / p.token_tiles * kPairChannels + static_cast<int>(rank) * kChannels;
         for (int k = k0; k < k1; ++k) {
           if (!mbar_wait(&w_empty[s.i], s.phase ^ 1u, p.timeout_ns) || aborted()) {
             if (!aborted()) give_up(kErrProducerTimeout);
@@ -330,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == kXWarp) {
     // ------------------------------------------------------- tokens (fp16)
     if (lane == 0) {
       pdl_wait();  // the kernel before this one writes them
@@ -339,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int armed = 0;
       bool ok = true;
       while (ok && walk.next(tile, k0, k1)) {
-        const int row = static_cast<int>(tile % p.token_tiles) * NT + static_cast<int>(rank) * (NT / 2);
+        const int row = tile % p.token_tiles * NT + static_cast<int>(rank) * (NT / 2);
         for (int k = k0; k < k1; ++k) {
           if (!mbar_wait(&done[s.i], s.phase ^ 1u, p.timeout_ns) || aborted()) {
             if (!aborted()) give_up(kErrProducerTimeout);
@@ -369,44 +443,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      if (leader) {
-        constexpr uint32_t idesc = make_idesc(kPairChannels, NT, 0u);
-        Slot<kRing> s;
-        uint32_t acc_phase = 0;
-        bool ok = true;
-        while (ok && walk.next(tile, k0, k1)) {
-          for (int k = k0; k < k1 && ok; k += kExactStages) {
-            const int kend = min(k + kExactStages, k1);
-            if (!mbar_wait_cluster(acc_empty, acc_phase ^ 1u, p.timeout_ns) || aborted()) ok = false;
-            tc_fence_after();
-            for (int kk = k; kk < kend && ok; ++kk) {
-              if (!mbar_wait(&x_full[s.i], s.phase, p.timeout_ns) ||
-                  !mbar_wait_cluster(&c_full[s.i], s.phase, p.timeout_ns) || aborted()) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint64_t b0 = sw128_kmajor_desc(xring + s.i * S::kXBytes);
-              const uint64_t b1 = sw128_kmajor_desc(xring + s.i * S::kXBytes + S::kXBytes / 2);
-              const uint32_t c = tmem_base + kTmemRing + static_cast<uint32_t>(s.i * kStageCols);
-#pragma unroll
-              for (int i = 0; i < kDepth / 16; ++i)
-                umma_pair_ts(tmem_base, c + static_cast<uint32_t>(8 * i),
-                             (i < 4 ? b0 : b1) + static_cast<uint64_t>(2 * (i & 3)), idesc, (kk != k) | (i != 0));
-              umma_commit_pair(&done[s.i]);
-              s.advance();
+    // The whole warp walks and waits, so that addresses and descriptors stay
+    // in uniform registers, and one elected lane issues: 20 cycles an MMA of
+    // 32 tokens instead of 45 from a branch on the lane's number. An MMA of
+    // 256 tokens takes 130, and few are queued, so the next stage's barriers
+    // are looked at while the second half of this one's is still to be issued.
+    if (leader) {
+      constexpr uint32_t idesc = make_idesc(kPairChannels, NT, 0u);
+      Slot<kRing> s;
+      uint32_t acc_phase = 0;
+      bool ok = true, ready = false;
+      while (ok && walk.next(tile, k0, k1)) {
+        for (int k = k0; k < k1 && ok; k += kExactStages) {
+          const int kend = min(k + kExactStages, k1);
+          ok = __all_sync(kFullMask, mbar_wait(acc_empty, acc_phase ^ 1u, p.timeout_ns)) && !aborted();
+          tc_fence_after();
+          for (int kk = k; kk < kend && ok; ++kk) {
+            if (!ready) {
+              ok = __all_sync(kFullMask, mbar_wait(&x_full[s.i], s.phase, p.timeout_ns) &&
+                                             mbar_wait(&c_full[s.i], s.phase, p.timeout_ns));
+              if (!ok) break;
             }
-            if (ok) umma_commit_pair(acc_full);
-            acc_phase ^= 1u;
+            tc_fence_after();
+            const uint64_t b0 = sw128_kmajor_desc(xring + s.i * S::kXBytes);
+            const uint64_t b1 = sw128_kmajor_desc(xring + s.i * S::kXBytes + S::kXBytes / 2);
+            const uint32_t c = tmem_base + NT + static_cast<uint32_t>(s.i * kStageCols);
+            const bool one_lane = elect_one();
+            if (one_lane) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                umma_pair_ts(tmem_base, c + static_cast<uint32_t>(8 * i), b0 + static_cast<uint64_t>(2 * i), idesc,
+                             (kk != k) | (i != 0));
+            }
+            __syncwarp();
+            Slot<kRing> next = s;
+            next.advance();
+            ready = __all_sync(kFullMask, mbar_try_wait(&x_full[next.i], next.phase) &&
+                                              mbar_try_wait(&c_full[next.i], next.phase));
+            if (one_lane) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                umma_pair_ts(tmem_base, c + static_cast<uint32_t>(8 * (i + 4)), b1 + static_cast<uint64_t>(2 * i), idesc, 1u);
+              umma_commit_pair(&done[s.i]);
+            }
+            __syncwarp();
+            s = next;
           }
+          if (ok && elect_one()) umma_commit_pair(acc_full);
+          __syncwarp();
+          acc_phase ^= 1u;
         }
-        if (!ok && !aborted()) give_up(kErrConsumerTimeout);
-        // Every MMA (they read both CTAs' memories) is done before either exits.
-        umma_commit_pair(drain);
       }
-      if (!mbar_wait(drain, 0, p.timeout_ns)) atomicOr(p.err, kErrDrainTimeout);
+      if (!ok && lane == 0 && !aborted()) give_up(kErrConsumerTimeout);
+      // Every MMA (they read both CTAs' memories) is done before either exits.
+      if (elect_one()) umma_commit_pair(drain);
+      __syncwarp();
     }
+    if (!mbar_wait(drain, 0, p.timeout_ns)) atomicOr(p.err, kErrDrainTimeout);
     __syncwarp();
   } else {
     // -------------------------------------------------------------- workers
@@ -415,10 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = quad * 32 + lane;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t acc_empty_addr = cluster_addr(acc_empty, 0);
-    const int64_t total = walk.total();
+    const uint32_t c_full_addr = cluster_addr(c_full, 0);
+    const int total = walk.total();
     bool ok = true;
     // Warp-uniform: whether every lane's wait has ended in time.
-    auto fine = [&](bool in_time) { return __all_sync(kFullMask, in_time && !aborted()); };
+    auto fine = [&](bool in_time) { return __all_sync(kFullMask, in_time) != 0; };
     uint32_t meet_phase = 0;
     auto workers_meet = [&]() {
       __syncwarp();
@@ -429,57 +523,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // Convert this group's stages up to (not including) stage `until`.
-    int64_t stage = group;
+    int stage = group;
     Slot<S::kWStages> ws;
-    ws.advance(group);
-    uint32_t ring_slot = static_cast<uint32_t>(group);
-    uint32_t ring_phase = 0;
-    auto convert_until = [&](int64_t until) {
-      for (; ok && stage < until; stage += 2) {
+    ws.i = group;
+    Slot<kRing> rs;
+    rs.i = group;
+    auto convert_until = [&](int until) {
+      for (; ok && stage < until; stage += kGroups) {
         ok = fine(mbar_wait(&w_full[ws.i], ws.phase, p.timeout_ns));
         if (!ok) break;
         const uint8_t* row = wring + ws.i * kWBytes + ch * kDepth;
-        const uint32_t dst = lane_base + kTmemRing + ring_slot * kStageCols;
+        const uint32_t dst = lane_base + NT + rs.i * kStageCols;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 raw[4];
+        for (int h = 0; h < 4; ++h) {
+          uint4 raw[2];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) raw[c] = *reinterpret_cast<const uint4*>(row + (((4 * h + c) ^ (ch & 7)) << 4));
+          for (int c = 0; c < 2; ++c) raw[c] = *reinterpret_cast<const uint4*>(row + (((2 * h + c) ^ (ch & 7)) << 4));
           if (h == 0) {
-            ok = fine(mbar_wait(&done[ring_slot], ring_phase ^ 1u, p.timeout_ns));
+            ok = fine(mbar_wait(&done[rs.i], rs.phase ^ 1u, p.timeout_ns));
             if (!ok) break;
             tc_fence_after();
-          } else {
+          }
+          if (h == 3) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&w_empty[ws.i]);
           }
-          uint32_t f[32];
+          uint32_t f[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             bytes_to_f16(raw[c].x, f[8 * c + 0], f[8 * c + 1]);
             bytes_to_f16(raw[c].y, f[8 * c + 2], f[8 * c + 3]);
             bytes_to_f16(raw[c].z, f[8 * c + 4], f[8 * c + 5]);
             bytes_to_f16(raw[c].w, f[8 * c + 6], f[8 * c + 7]);
           }
-          tmem_st32(dst + 32 * h, f);
+          tmem_st16(dst + 16 * h, f);
         }
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(cluster_addr(&c_full[ring_slot], 0));
-        ws.advance(2);
-        ring_slot ^= 2u;
-        if (ring_slot == static_cast<uint32_t>(group)) ring_phase ^= 1u;
+        if (lane == 0) mbar_arrive_cluster(c_full_addr + rs.i * 8);  // orders TMEM only, as for acc_empty
+        ws.advance(kGroups);
+        rs.advance(kGroups);
       }
     };
 
-    int64_t finished = 0;  // stages whose accumulator has been read
+    int finished = 0;  // stages whose accumulator has been read
     uint32_t acc_phase = 0;
     bool waited = false;
     while (ok && walk.next(tile, k0, k1)) {
+      if (!waited) {  // the scales may come from the kernel before this one, which may also read `out`
+        pdl_wait();
+        waited = true;
+      }
+      Scales<NT> scales;
+      scales.read(p, tile, static_cast<int>(rank) * kChannels + quad * 32, group * kCols, lane);
       uint32_t acc[kCols];
-      const bool one = k1 - k0 <= kExactStages && k0 == 0 && k1 == p.stages;  // a whole sum that fp32 holds
+      // The whole sum is one accumulator's and fp32 holds it.
+      const bool one = k1 - k0 <= kExactStages && k0 == 0 && k1 == p.stages && !kSums;
       for (int k = k0; k < k1 && ok; k += kExactStages) {
         finished += min(kExactStages, k1 - k);
         convert_until(min(finished + kRing, total));
@@ -488,9 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         acc_phase ^= 1u;
         tc_fence_after();
+        auto ld = [&](int c, uint32_t* v) {
+          if constexpr (kDrain == 16)
+            tmem_ld16(lane_base + group * kCols + c, v);
+          else
+            tmem_ld8(lane_base + group * kCols + c, v);
+        };
         if (one) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 16) tmem_ld16(lane_base + group * kCols + c, acc + c);
+          for (int c = 0; c < kCols; c += kDrain) ld(c, acc + c);
           tmem_wait_ld();
         } else {
           if (k == k0) {
@@ -500,8 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kCols; c += kDrain) {
             uint32_t v[kDrain];
-#pragma unroll
-            for (int d = 0; d < kDrain; d += 16) tmem_ld16(lane_base + group * kCols + c + d, v + d);
+            ld(c, v);
             tmem_wait_ld();
 #pragma unroll
             for (int d = 0; d < kDrain; ++d) acc[c + d] += static_cast<uint32_t>(__float2int_rn(__uint_as_float(v[d])));
@@ -512,13 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(acc_empty_addr);
       }
       if (!ok) break;
-      if (!waited) {  // the scales may come from the kernel before this one, which may also read `out`
-        pdl_wait();
-        waited = true;
-      }
       if (k0 != 0 || k1 != p.stages) {
         // A shared tile: leave the partial sums, and finish it if all are there.
-        const int64_t all = p.tiles * p.stages, first_stage = tile * p.stages;
+        const int64_t all = static_cast<int64_t>(p.tiles) * p.stages, first_stage = static_cast<int64_t>(tile) * p.stages;
         const int first = static_cast<int>(((first_stage + 1) * pairs - 1) / all);
         const int last = static_cast<int>(((first_stage + p.stages) * pairs - 1) / all);
         auto slot_of = [&](int who) {
@@ -551,40 +653,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kCols; ++c) acc[c] += static_cast<uint32_t>(__ldcg(theirs + c * kChannels));
         }
       }
-      const int64_t j = tile / p.token_tiles * kPairChannels + static_cast<int>(rank) * kChannels + ch;
-      const int64_t i0 = tile % p.token_tiles * NT + group * kCols;
-      if (j < p.n && i0 < p.m) {
-        const int live = static_cast<int>(min(static_cast<int64_t>(kCols), p.m - i0));
-        const float sb = p.b_scale ? p.b_scale[j] : 1.0f;
-        const float add = p.bias ? p.bias[j] : 0.0f;
-        const float* sa = p.a_scale ? p.a_scale + i0 : nullptr;
-        auto value = [&](int c) {
-          float f = one ? __uint_as_float(acc[c]) : __int2float_rn(static_cast<int>(acc[c]));
-          if (sa) f = __fmul_rn(f, sa[c]);
-          return __fadd_rn(__fmul_rn(f, sb), add);
-        };
-        const int64_t at = i0 * p.ld_out + j;
-        if (p.out_dtype == kI32) {
-          int* o = static_cast<int*>(p.out) + at;
+      if constexpr (kSums) {
+        store_sums<NT>(p, scales, acc, lane);
+      } else {
+        if (!one) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c < live) o[c * p.ld_out] = one ? __float2int_rn(__uint_as_float(acc[c])) : static_cast<int>(acc[c]);
-        } else if (p.out_dtype == kF32) {
-          float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c < live) o[c * p.ld_out] = value(c);
-        } else if (p.out_dtype == kBF16) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c < live) o[c * p.ld_out] = __float2bfloat16_rn(value(c));
-        } else {
-          __half* o = static_cast<__half*>(p.out) + at;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c < live) o[c * p.ld_out] = __float2half_rn(value(c));
+          for (int c = 0; c < kCols; ++c) acc[c] = __float_as_uint(__int2float_rn(static_cast<int>(acc[c])));
         }
+        store_tile<NT, OUT == 2>(p, scales, acc, lane);
       }
     }
     if (!ok && lane == 0 && !aborted()) give_up(kErrConsumerTimeout);
@@ -638,7 +714,7 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT>
+template <int NT, int OUT>
 cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t st) {
   CUtensorMap mx, mw;
   const int pitch = matmul_i8_pitch(a.k);
@@ -656,20 +732,20 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   p.out_dtype = a.out_dtype;
   p.stages = pitch / kDepth;
   p.token_tiles = static_cast<int>((a.m + NT - 1) / NT);
-  p.tiles = (a.n + kPairChannels - 1) / kPairChannels * p.token_tiles;
+  p.tiles = static_cast<int>((a.n + kPairChannels - 1) / kPairChannels * p.token_tiles);
   p.read_once = p.token_tiles == 1;
   p.partial = w.partial;
   p.arrived = w.arrived;
   p.err = w.err;
   p.timeout_ns = w.timeout_ns;
   const int64_t max_pairs = w.num_sms / 2;
-  const int64_t total = p.tiles * p.stages;
+  const int64_t total = static_cast<int64_t>(p.tiles) * p.stages;
   // Whole tiles from four rounds on (the last round then costs a fifth at
   // most), or where they come out even.
   p.split = !(p.tiles >= 4 * max_pairs || p.tiles % max_pairs == 0);
-  const int64_t pairs = p.split ? std::min(max_pairs, total) : std::min(max_pairs, p.tiles);
+  const int64_t pairs = p.split ? std::min(max_pairs, total) : std::min<int64_t>(max_pairs, p.tiles);
 
-  auto fn = matmul_i8_pair_kernel<NT>;
+  auto fn = matmul_i8_pair_kernel<NT, OUT>;
   static PerDeviceOnce once;
   const cudaError_t limit = once.run(
       [fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NT>::kSmem); });
@@ -691,6 +767,13 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   return cudaLaunchKernelEx(&cfg, fn, mx, mw, p);
 }
 
+template <int NT>
+cudaError_t launch_out(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t st) {
+  if (a.out_dtype == kI32) return launch_t<NT, 0>(a, w, st);
+  if (a.out_dtype == kF32) return launch_t<NT, 1>(a, w, st);
+  return launch_t<NT, 2>(a, w, st);
+}
+
 }  // namespace
 
 int matmul_i8_pitch(int k) { return (k + kDepth - 1) / kDepth * kDepth; }
@@ -698,8 +781,10 @@ int matmul_i8_pitch(int k) { return (k + kDepth - 1) / kDepth * kDepth; }
 size_t matmul_i8_partial_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * kChannels * 256 * sizeof(int); }
 
 bool matmul_i8_tc_fits(const MatmulI8Launch& a) {
-  // The tensor map wants 16-byte boundaries; a row of the map's coordinates is 32 bits.
-  return a.k > 0 && (reinterpret_cast<uintptr_t>(a.b) & 15) == 0 && a.ld_b % 16 == 0 && a.n <= INT32_MAX - kPairChannels;
+  // The tensor map wants 16-byte boundaries and 32-bit coordinates; the kernel counts stages in 32 bits.
+  const double stages = (a.n / 256.0 + 1) * (a.m / (a.m <= 128 ? 32.0 : 256.0) + 1) * (a.k / 128.0 + 1);
+  return a.k > 0 && (reinterpret_cast<uintptr_t>(a.b) & 15) == 0 && a.ld_b % 16 == 0 && a.n <= INT32_MAX - kPairChannels &&
+         stages < 2.0e9;
 }
 
 cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, void* rows_f16, int num_sms,
@@ -711,10 +796,10 @@ cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, 
 }
 
 cudaError_t launch_matmul_i8_tc(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t st) {
-  if (a.m <= 32) return launch_t<32>(a, w, st);
-  if (a.m <= 64) return launch_t<64>(a, w, st);
-  if (a.m <= 128) return launch_t<128>(a, w, st);
-  return launch_t<256>(a, w, st);
+  if (a.m <= 32) return launch_out<32>(a, w, st);
+  if (a.m <= 64) return launch_out<64>(a, w, st);
+  if (a.m <= 128) return launch_out<128>(a, w, st);
+  return launch_out<256>(a, w, st);
 }
 
 }  // namespace rbf
