@@ -6,10 +6,12 @@
 // sm_103a has no 8-bit integer tensor instruction (tcgen05 kind::i8 does not
 // assemble for it), but fp16 holds every 8-bit integer, and the product of two
 // of them, up to 2^14, is exact in the fp32 accumulator as long as the running
-// sum stays within 2^24: for 1,024 products whatever their values. So the
-// kernel multiplies in fp16 (kind::f16, the full 16-bit rate), and where the
-// depth is larger it moves the accumulator into 32-bit integers in registers
-// every 1,024 values. The sums are exact for every input.
+// sum stays within 2^24: for 1,024 products whatever their values, and for as
+// many stages of 128 as the largest sum of |a| over one of them allows (it is
+// found while a is expanded; ordinary rows give 3,000 to 4,000 products). So
+// the kernel multiplies in fp16 (kind::f16, the full 16-bit rate), and where
+// the depth is larger than that it moves the accumulator into 32-bit integers
+// in registers in between. The sums are exact for every input.
 //
 // The large operand (b: corpus rows or output channels) is read from memory as
 // bytes and becomes fp16 on its way into the tensor memory, so it costs one
@@ -32,7 +34,7 @@
 //               the columns that the accumulator leaves;
 //   warp 18     loads the CTA's tokens (TMA) into a ring of as many stages;
 //   warp 1      one thread of the even CTA issues the pair's MMAs.
-// At the end of a tile (and every 1,024 values) warps 2-17 read the accumulator,
+// At the end of a tile (and of an exact sum) warps 2-17 read the accumulator,
 // after they have converted the next ring of stages, so that the MMAs of the next
 // tile run while the last one's results are scaled and stored.
 //
@@ -57,7 +59,7 @@ constexpr int kDepth = 128;          // values of depth a stage
 constexpr int kChannels = 128;       // channels per CTA and tile
 constexpr int kPairChannels = 256;
 constexpr int kWBytes = kChannels * kDepth;
-constexpr int kExactStages = 1024 / kDepth;
+constexpr int kExactStages = 1024 / kDepth;  // of any values
 constexpr int kGroups = 4;           // of worker warps: a group takes every fourth stage
 constexpr int kWorkers = 4 * kGroups;
 constexpr int kXWarp = 2 + kWorkers;
@@ -66,14 +68,21 @@ constexpr int kTmemCols = 512;       // the accumulator first, then the ring of 
 constexpr int kStageCols = kDepth / 2;
 constexpr int kRingBudget = 224 * 1024;
 
-template <int NT>
+// OUT: what is stored: 0 the sums (int32), 1 fp32, 2 a 16-bit type.
+template <int NT, int OUT>
 struct Shape {
-  static constexpr int kXBytes = NT * kDepth;  // NT / 2 tokens x 128 fp16
-  static constexpr int kRing = (kTmemCols - NT) / kStageCols;  // stages of the token ring and of the TMEM ring
-  static constexpr int kCols = NT / kGroups;   // accumulator columns of one worker thread
-  static constexpr int kWStages = (kRingBudget - kRing * kXBytes) / kWBytes;
-  static constexpr int kSmem = 1024 + kRing * kXBytes + kWStages * kWBytes + (2 * kWStages + 3 * kRing + 4) * 8 + 16;
+  static constexpr int kXBytes = NT * kDepth;          // NT / 2 tokens x 128 fp16
+  static constexpr int kAcc = NT <= 128 ? 2 : 1;       // accumulators
+  static constexpr int kRing = (kTmemCols - kAcc * NT) / kStageCols;  // stages of the token ring and of the TMEM ring
+  static constexpr int kCols = NT / kGroups;           // accumulator columns (tokens) of one worker warp
+  static constexpr int kSlab = kCols < 16 ? kCols : 16;  // tokens stored at a time
+  static constexpr int kStageOut = OUT == 2 ? kSlab * 64 : 0;  // a slab of 32 channels x 16 bits
+  static constexpr int kOutBytes = kWorkers * 2 * kStageOut;
+  static constexpr int kWStages = (kRingBudget - kRing * kXBytes - kOutBytes) / kWBytes;
+  static constexpr int kBars = 2 * kWStages + 3 * kRing + 2 * kAcc + 2;
+  static constexpr int kSmem = 1024 + kRing * kXBytes + kWStages * kWBytes + kOutBytes + kBars * 8 + 16;
   static_assert(kRing >= kGroups && kWStages >= kGroups, "a group needs a slot of its own");
+  static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
 };
 
 struct Params {
@@ -88,7 +97,10 @@ struct Params {
   int token_tiles;
   int tiles;         // tiles x stages < 2^31
   int split;         // 1: equal shares of all stages, 0: whole tiles
+  int tma_out;       // 1: 16-bit results may be stored by TMA
   int read_once;     // 1: the channels are read once (one token tile)
+  const unsigned* block_l1;  // the largest sum of |a| over a token's 128 values of a stage
+  unsigned* block_l1_next;   // the next launch's, to be zero for it
   int* partial;      // split: two tiles of partial sums per CTA
   unsigned* arrived; // split: one counter per CTA, zero between launches
   int* err;
@@ -161,6 +173,14 @@ __device__ __forceinline__ void umma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// Stages whose products one accumulator sums exactly: |b| <= 128 and
+// sum |a| <= block_l1 a stage, so that many stages stay within 2^24.
+// (block_l1 <= 128 * 128, which leaves kExactStages of them for any input.)
+__device__ __forceinline__ int exact_stages(const Params& p) {
+  const unsigned l1 = *reinterpret_cast<const volatile unsigned*>(p.block_l1);
+  return max(kExactStages, static_cast<int>(min((1u << 17) / max(l1, 1u), static_cast<unsigned>(p.stages))));
+}
+
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -188,7 +208,35 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 16 lanes x 8 (16) columns as 8 x 8 blocks: registers 0-1 lane / 4, 2-3 lane / 4 + 8, columns 2 (lane % 4) + {0, 1}.
+__device__ __forceinline__ void tmem_ld_blocks1(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_blocks2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+// Wait for this thread's loads; the registers pass through, so that nothing
+// that uses them can move ahead of the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+  if constexpr (N == 16)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+  else
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -212,113 +260,145 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// What a worker warp multiplies its part of a tile by, read ahead of the sums:
-// lane l has the scale and bias of channel ch0 + l, and the scales of tokens
-// col0 + l, col0 + 32 + l ...
-template <int NT>
-struct Scales {
-  static constexpr int kWords = (Shape<NT>::kCols + 31) / 32;
-  float sa[kWords];
-  float sb, add;
+// A worker warp's part of a tile: 32 channels from j0 on, tokens i0 .. of which
+// `live` exist. Its sums are in registers as the tensor memory gives them out:
+//   OUT 0, 1: lane = channel, register = token;
+//   OUT 2: as the 8 x 8 blocks of a 16-bit matrix store: per 16 tokens, and for
+//     each half of 16 channels, registers 4 j .. 4 j + 3 of a lane are tokens
+//     8 j + 2 (lane % 4) + {0, 1} of channels lane / 4 and lane / 4 + 8.
+// What they are multiplied by is read ahead of them.
+template <int NT, int OUT>
+struct Part {
+  using S = Shape<NT, OUT>;
+  static constexpr int kWords = (S::kCols + 31) / 32;
+  static constexpr int kChan = OUT == 2 ? 4 : 1;  // channels of a lane
   int64_t j0, i0;
-  int live;    // tokens of this part that exist
-  bool mine;   // this lane's channel exists
+  int live;
+  float sa[kWords];  // tokens lane, 32 + lane
+  float sb[kChan], add[kChan];
 
-  __device__ __forceinline__ void read(const Params& p, int tile, int ch0, int col0, int lane) {
+  __device__ __forceinline__ Part(const Params& p, int tile, int ch0, int col0, int lane) {
     j0 = static_cast<int64_t>(tile / p.token_tiles) * kPairChannels + ch0;
     i0 = static_cast<int64_t>(tile % p.token_tiles) * NT + col0;
-    live = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(Shape<NT>::kCols), p.m - i0)));
-    mine = j0 + lane < p.n;
-    sb = p.b_scale && mine ? p.b_scale[j0 + lane] : 1.0f;
-    add = p.bias && mine ? p.bias[j0 + lane] : 0.0f;
+    live = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(S::kCols), p.m - i0)));
+    if constexpr (OUT != 0) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) sa[i] = p.a_scale && 32 * i + lane < live ? p.a_scale[i0 + 32 * i + lane] : 1.0f;
+      for (int q = 0; q < kChan; ++q) {
+        const int64_t j = j0 + (OUT == 2 ? 8 * q + lane / 4 : lane);
+        sb[q] = p.b_scale && j < p.n ? p.b_scale[j] : 1.0f;
+        add[q] = p.bias && j < p.n ? p.bias[j] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) sa[i] = p.a_scale && 32 * i + lane < live ? p.a_scale[i0 + 32 * i + lane] : 1.0f;
+    }
   }
 };
 
-// Scale and store a worker warp's part of a tile, fp32 sums as they are. 16-bit
-// results are exchanged between neighbouring lanes, so that a lane holds two
-// channels of one token: one 4-byte store for two results.
-template <int NT, bool OUT16>
-__device__ __forceinline__ void store_tile(const Params& p, const Scales<NT>& s, const uint32_t (&acc)[Shape<NT>::kCols], int lane) {
-  constexpr int kCols = Shape<NT>::kCols;
-  constexpr int kSlab = kCols < 16 ? kCols : 16;
-  if (s.j0 >= p.n || s.live == 0) return;
-  const int odd = lane & 1;
-  const bool paired = OUT16 && s.j0 + 32 <= p.n && p.ld_out % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
+// 16-bit results go through shared memory, where 8 x 8 blocks are stored
+// transposed (stmatrix): rows of one token's 32 channels, 64 bytes, in the
+// 64-byte swizzle (16-byte piece q of row r at q ^ (r / 2 % 4)) that spreads a
+// block's rows over all banks. From there a tiled TMA store writes the slab of
+// 16 tokens and clips it at the matrix' edges; where the output's rows are not
+// on 16-byte boundaries, the warp's lanes store it. `buf`: the warp's two slabs.
+struct OutBuf {
+  uint8_t* buf;
+  int which;
+};
+
+// Scale and store tokens c0 .. c0 + kSlab - 1 of the part: r holds their sums,
+// integers for OUT 0 and fp32 numbers else.
+template <int NT, int OUT>
+__device__ __forceinline__ void store_slab(const Params& p, const CUtensorMap* map, const Part<NT, OUT>& t, int c0,
+                                           const uint32_t* r, OutBuf& ob, int lane) {
+  using S = Shape<NT, OUT>;
+  if (t.j0 >= p.n || c0 >= t.live) return;
+  if constexpr (OUT == 0) {
+    int* o = static_cast<int*>(p.out) + (t.i0 + c0) * p.ld_out + t.j0 + lane;
 #pragma unroll
-  for (int c0 = 0; c0 < kCols; c0 += kSlab) {
-    if (c0 >= s.live) break;
-    float v[kSlab];
+    for (int c = 0; c < S::kSlab; ++c)
+      if (t.j0 + lane < p.n && c0 + c < t.live) o[c * p.ld_out] = static_cast<int>(r[c]);
+  } else if constexpr (OUT == 1) {
+    float* o = static_cast<float*>(p.out) + (t.i0 + c0) * p.ld_out + t.j0 + lane;
+    const bool mine = t.j0 + lane < p.n;
 #pragma unroll
-    for (int c = 0; c < kSlab; ++c)
-      v[c] = __fmaf_rn(__fmul_rn(__uint_as_float(acc[c0 + c]), __shfl_sync(kFullMask, s.sa[c0 / 32], (c0 + c) & 31)), s.sb, s.add);
-    if constexpr (!OUT16) {
-      float* o = static_cast<float*>(p.out) + (s.i0 + c0) * p.ld_out + s.j0 + lane;
+    for (int c = 0; c < S::kSlab; ++c) {
+      const float v = __fmaf_rn(__fmul_rn(__uint_as_float(r[c]), __shfl_sync(kFullMask, t.sa[c0 / 32], (c0 + c) & 31)), t.sb[0], t.add[0]);
+      if (mine && c0 + c < t.live) o[c * p.ld_out] = v;
+    }
+  } else {
+    constexpr int kBlocks = S::kSlab / 8;
+    uint8_t* slab = ob.buf + ob.which * S::kStageOut;
+    ob.which ^= 1;
+    // The slab before last has been read.
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
 #pragma unroll
-      for (int c = 0; c < kSlab; ++c)
-        if (s.mine && c0 + c < s.live) o[c * p.ld_out] = v[c];
-    } else {
-      uint32_t two[kSlab / 2];  // tokens c and c + 1 of this lane's channel
+    for (int j = 0; j < kBlocks; ++j) {
+      const int tok = c0 + 8 * j + 2 * (lane & 3);
+      const float s0 = __shfl_sync(kFullMask, t.sa[c0 / 32], tok & 31);
+      const float s1 = __shfl_sync(kFullMask, t.sa[c0 / 32], (tok + 1) & 31);
+      uint32_t w[4];
 #pragma unroll
-      for (int c = 0; c < kSlab; c += 2) {
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t* e = r + ((q / 2) * kBlocks + j) * 4 + (q & 1) * 2;
+        const float v0 = __fmaf_rn(__fmul_rn(__uint_as_float(e[0]), s0), t.sb[q], t.add[q]);
+        const float v1 = __fmaf_rn(__fmul_rn(__uint_as_float(e[1]), s1), t.sb[q], t.add[q]);
         if (p.out_dtype == kBF16) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
-          two[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+          w[q] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
-          const __half2 h = __floats2half2_rn(v[c], v[c + 1]);
-          two[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          const __half2 h = __floats2half2_rn(v0, v1);
+          w[q] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
-      if (paired) {
-        const uint32_t pick = odd ? 0x3276u : 0x5410u;
-        uint32_t* o = static_cast<uint32_t*>(p.out) + ((s.i0 + c0 + odd) * p.ld_out + s.j0 + lane - odd) / 2;
+      const int row = 8 * j + (lane & 7);
+      const uint32_t at = smem_addr(slab) + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4);
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                   "r"(w[2]), "r"(w[3])
+                   : "memory");
+    }
+    if (p.tma_out) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                     "r"(static_cast<int>(t.j0)), "r"(static_cast<int>(t.i0) + c0), "r"(smem_addr(slab))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    } else {
+      __syncwarp();
+      uint16_t* o = static_cast<uint16_t*>(p.out) + (t.i0 + c0) * p.ld_out + t.j0 + lane;
 #pragma unroll
-        for (int c = 0; c < kSlab; c += 2) {
-          const uint32_t other = __shfl_xor_sync(kFullMask, two[c / 2], 1);
-          if (c0 + c + odd < s.live) o[c / 2 * p.ld_out] = __byte_perm(two[c / 2], other, pick);
-        }
-      } else {
-        uint16_t* o = static_cast<uint16_t*>(p.out) + (s.i0 + c0) * p.ld_out + s.j0 + lane;
-#pragma unroll
-        for (int c = 0; c < kSlab; ++c)
-          if (s.mine && c0 + c < s.live) o[c * p.ld_out] = static_cast<uint16_t>(two[c / 2] >> (16 * (c & 1)));
+      for (int i = 0; i < S::kSlab; ++i) {
+        const uint16_t v = *reinterpret_cast<const uint16_t*>(slab + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
+        if (t.j0 + lane < p.n && c0 + i < t.live) o[i * p.ld_out] = v;
       }
     }
   }
 }
 
-// The integer sums themselves.
-template <int NT>
-__device__ __forceinline__ void store_sums(const Params& p, const Scales<NT>& s, const uint32_t (&acc)[Shape<NT>::kCols], int lane) {
-  int* o = static_cast<int*>(p.out) + s.i0 * p.ld_out + s.j0 + lane;
-#pragma unroll
-  for (int c = 0; c < Shape<NT>::kCols; ++c)
-    if (s.mine && c < s.live) o[c * p.ld_out] = static_cast<int>(acc[c]);
-}
-
-// OUT: what is stored: 0 the sums (int32), 1 fp32, 2 a 16-bit type.
 template <int NT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
-                          const Params p) {
-  using S = Shape<NT>;
+                          const __grid_constant__ CUtensorMap tmap_out, const Params p) {
+  using S = Shape<NT, OUT>;
   constexpr int kCols = S::kCols;
-  constexpr int kDrain = kCols < 16 ? kCols : 16;  // columns read at a time
+  constexpr int kSlab = S::kSlab;
   constexpr int kRing = S::kRing;
-  constexpr bool kSums = OUT == 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* xring = smem;
   uint8_t* wring = smem + kRing * S::kXBytes;
-  uint64_t* w_full = reinterpret_cast<uint64_t*>(wring + S::kWStages * kWBytes);
+  uint8_t* outbuf = wring + S::kWStages * kWBytes;  // two slabs of results per worker warp
+  uint64_t* w_full = reinterpret_cast<uint64_t*>(outbuf + S::kOutBytes);
   uint64_t* w_empty = w_full + S::kWStages;
   uint64_t* x_full = w_empty + S::kWStages;  // the even CTA's are used: both CTAs' tokens
   uint64_t* c_full = x_full + kRing;         // the even CTA's are used: both CTAs' converted channels
   uint64_t* done = c_full + kRing;           // the MMAs of a stage have read both rings
   uint64_t* acc_full = done + kRing;
-  uint64_t* acc_empty = acc_full + 1;        // the even CTA's is used
-  uint64_t* drain = acc_empty + 1;
+  uint64_t* acc_empty = acc_full + S::kAcc;  // the even CTA's are used
+  uint64_t* drain = acc_empty + S::kAcc;
   uint64_t* meet = drain + 1;                // the workers of this CTA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
   __shared__ int abort_flag;
@@ -342,8 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c_full[s], 8);  // four warps of each CTA
       mbar_init(&done[s], 1);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 2 * kWorkers);
+    for (int b = 0; b < S::kAcc; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kWorkers);
+    }
     mbar_init(drain, 1);
     mbar_init(meet, kWorkers);
     fence_mbar_init();
@@ -358,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.block_l1_next = 0;
 
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&abort_flag) != 0; };
   auto give_up = [&](int bit) {
@@ -451,12 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader) {
       constexpr uint32_t idesc = make_idesc(kPairChannels, NT, 0u);
       Slot<kRing> s;
-      uint32_t acc_phase = 0;
+      Slot<S::kAcc> as;
+      pdl_wait();
+      const int exact = exact_stages(p);
       bool ok = true, ready = false;
       while (ok && walk.next(tile, k0, k1)) {
-        for (int k = k0; k < k1 && ok; k += kExactStages) {
-          const int kend = min(k + kExactStages, k1);
-          ok = __all_sync(kFullMask, mbar_wait(acc_empty, acc_phase ^ 1u, p.timeout_ns)) && !aborted();
+        for (int k = k0; k < k1 && ok; k += exact) {
+          const int kend = min(k + exact, k1);
+          ok = __all_sync(kFullMask, mbar_wait(&acc_empty[as.i], as.phase ^ 1u, p.timeout_ns)) && !aborted();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(as.i * NT);
           tc_fence_after();
           for (int kk = k; kk < kend && ok; ++kk) {
             if (!ready) {
@@ -467,12 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint64_t b0 = sw128_kmajor_desc(xring + s.i * S::kXBytes);
             const uint64_t b1 = sw128_kmajor_desc(xring + s.i * S::kXBytes + S::kXBytes / 2);
-            const uint32_t c = tmem_base + NT + static_cast<uint32_t>(s.i * kStageCols);
+            const uint32_t c = tmem_base + S::kAcc * NT + static_cast<uint32_t>(s.i * kStageCols);
             const bool one_lane = elect_one();
             if (one_lane) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                umma_pair_ts(tmem_base, c + static_cast<uint32_t>(8 * i), b0 + static_cast<uint64_t>(2 * i), idesc,
+                umma_pair_ts(d, c + static_cast<uint32_t>(8 * i), b0 + static_cast<uint64_t>(2 * i), idesc,
                              (kk != k) | (i != 0));
             }
             __syncwarp();
@@ -483,15 +569,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one_lane) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                umma_pair_ts(tmem_base, c + static_cast<uint32_t>(8 * (i + 4)), b1 + static_cast<uint64_t>(2 * i), idesc, 1u);
+                umma_pair_ts(d, c + static_cast<uint32_t>(8 * (i + 4)), b1 + static_cast<uint64_t>(2 * i), idesc, 1u);
               umma_commit_pair(&done[s.i]);
             }
             __syncwarp();
             s = next;
           }
-          if (ok && elect_one()) umma_commit_pair(acc_full);
+          if (ok && elect_one()) umma_commit_pair(&acc_full[as.i]);
           __syncwarp();
-          acc_phase ^= 1u;
+          as.advance();
         }
       }
       if (!ok && lane == 0 && !aborted()) give_up(kErrConsumerTimeout);
@@ -508,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = quad * 32 + lane;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t acc_empty_addr = cluster_addr(acc_empty, 0);
+    OutBuf ob{outbuf + (warp - 2) * 2 * S::kStageOut, 0};
     const uint32_t c_full_addr = cluster_addr(c_full, 0);
     const int total = walk.total();
     bool ok = true;
@@ -533,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = fine(mbar_wait(&w_full[ws.i], ws.phase, p.timeout_ns));
         if (!ok) break;
         const uint8_t* row = wring + ws.i * kWBytes + ch * kDepth;
-        const uint32_t dst = lane_base + NT + rs.i * kStageCols;
+        const uint32_t dst = lane_base + S::kAcc * NT + rs.i * kStageCols;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint4 raw[2];
@@ -569,53 +656,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     int finished = 0;  // stages whose accumulator has been read
-    uint32_t acc_phase = 0;
-    bool waited = false;
-    while (ok && walk.next(tile, k0, k1)) {
-      if (!waited) {  // the scales may come from the kernel before this one, which may also read `out`
-        pdl_wait();
-        waited = true;
+    Slot<S::kAcc> as;
+    // The next accumulator is complete; its address for this warp.
+    auto acc_ready = [&](uint32_t& from) {
+      ok = fine(mbar_wait(&acc_full[as.i], as.phase, p.timeout_ns));
+      tc_fence_after();
+      from = lane_base + static_cast<uint32_t>(as.i * NT + group * kCols);
+      return ok;
+    };
+    auto acc_release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_empty_addr + as.i * 8);
+      as.advance();
+    };
+    auto ld = [&](uint32_t at, uint32_t* v) {  // kSlab columns of the warp's 32 lanes
+      if constexpr (OUT == 2) {
+        constexpr uint32_t kHalf = 16u << 16;  // TMEM lanes 16-31 of the warp's
+        if constexpr (kSlab == 16) {
+          tmem_ld_blocks2(at, v);
+          tmem_ld_blocks2(at + kHalf, v + 8);
+        } else {
+          tmem_ld_blocks1(at, v);
+          tmem_ld_blocks1(at + kHalf, v + 4);
+        }
+      } else if constexpr (kSlab == 16) {
+        tmem_ld16(at, v);
+      } else {
+        tmem_ld8(at, v);
       }
-      Scales<NT> scales;
-      scales.read(p, tile, static_cast<int>(rank) * kChannels + quad * 32, group * kCols, lane);
-      uint32_t acc[kCols];
-      // The whole sum is one accumulator's and fp32 holds it.
-      const bool one = k1 - k0 <= kExactStages && k0 == 0 && k1 == p.stages && !kSums;
-      for (int k = k0; k < k1 && ok; k += kExactStages) {
-        finished += min(kExactStages, k1 - k);
+    };
+    convert_until(min(kRing, total));  // before anything that the kernel before this one writes is needed
+    pdl_wait();                        // it writes the scales, and may read `out`
+    const int exact = exact_stages(p);
+    while (ok && walk.next(tile, k0, k1)) {
+      const int ch0 = static_cast<int>(rank) * kChannels + quad * 32;
+      if (k0 == 0 && k1 == p.stages && p.stages <= exact) {
+        // The sums are one accumulator's: from tensor memory to the output, a
+        // slab at a time, the next one's load under way.
+        finished += k1;
         convert_until(min(finished + kRing, total));
         if (!ok) break;
-        ok = fine(mbar_wait(acc_full, acc_phase, p.timeout_ns));
-        if (!ok) break;
-        acc_phase ^= 1u;
-        tc_fence_after();
-        auto ld = [&](int c, uint32_t* v) {
-          if constexpr (kDrain == 16)
-            tmem_ld16(lane_base + group * kCols + c, v);
-          else
-            tmem_ld8(lane_base + group * kCols + c, v);
-        };
-        if (one) {
+        const Part<NT, OUT> part(p, tile, ch0, group * kCols, lane);
+        uint32_t from;
+        if (!acc_ready(from)) break;
+        // One accumulator: it is read at once and given back before its sums
+        // are stored. Two: the next slab is read while this one is stored.
+        constexpr int kAhead = S::kAcc == 1 ? kCols / kSlab : 2;
+        uint32_t v[kAhead][kSlab];
 #pragma unroll
-          for (int c = 0; c < kCols; c += kDrain) ld(c, acc + c);
-          tmem_wait_ld();
-        } else {
-          if (k == k0) {
+        for (int i = 0; i < kAhead - (S::kAcc == 2); ++i) ld(from + i * kSlab, v[i]);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) acc[c] = 0;
+        for (int i = 0; i < kCols / kSlab; ++i) {
+          uint32_t(&now)[kSlab] = v[i % kAhead];
+          tmem_wait_ld<kSlab>(now);
+          if (S::kAcc == 2 && i + 1 < kCols / kSlab) ld(from + (i + 1) * kSlab, v[(i + 1) % kAhead]);
+          if (i == (S::kAcc == 1 ? 0 : kCols / kSlab - 1)) acc_release();
+          if constexpr (OUT == 0) {
+#pragma unroll
+            for (int c = 0; c < kSlab; ++c) now[c] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(now[c])));
           }
-#pragma unroll
-          for (int c = 0; c < kCols; c += kDrain) {
-            uint32_t v[kDrain];
-            ld(c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int d = 0; d < kDrain; ++d) acc[c + d] += static_cast<uint32_t>(__float2int_rn(__uint_as_float(v[d])));
-          }
+          store_slab<NT, OUT>(p, &tmap_out, part, i * kSlab, now, ob, lane);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty_addr);
+        continue;
+      }
+      uint32_t acc[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = 0;
+      for (int k = k0; k < k1; k += exact) {
+        finished += min(exact, k1 - k);
+        convert_until(min(finished + kRing, total));
+        uint32_t from;
+        if (!ok || !acc_ready(from)) break;
+#pragma unroll
+        for (int c = 0; c < kCols; c += kSlab) {
+          uint32_t v[kSlab];
+          ld(from + c, v);
+          tmem_wait_ld<kSlab>(v);
+#pragma unroll
+          for (int i = 0; i < kSlab; ++i) acc[c + i] += static_cast<uint32_t>(__float2int_rn(__uint_as_float(v[i])));
+        }
+        acc_release();
       }
       if (!ok) break;
       if (k0 != 0 || k1 != p.stages) {
@@ -623,10 +744,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t all = static_cast<int64_t>(p.tiles) * p.stages, first_stage = static_cast<int64_t>(tile) * p.stages;
         const int first = static_cast<int>(((first_stage + 1) * pairs - 1) / all);
         const int last = static_cast<int>(((first_stage + p.stages) * pairs - 1) / all);
-        auto slot_of = [&](int who) {
-          return p.partial + (static_cast<int64_t>(who * 2 + static_cast<int>(rank)) * 2 + (who == first ? 1 : 0)) * (kChannels * NT);
+        auto slot_of = [&](int who) {  // a register's 32 lanes side by side
+          return p.partial + (static_cast<int64_t>(who * 2 + static_cast<int>(rank)) * 2 + (who == first ? 1 : 0)) * (kChannels * NT) +
+                 group * kCols * kChannels + ch;
         };
-        int* mine = slot_of(pair) + group * kCols * kChannels + ch;
+        int* mine = slot_of(pair);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) __stcg(mine + c * kChannels, static_cast<int>(acc[c]));
         __threadfence();
@@ -648,21 +770,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!fin) continue;
         for (int who = first; who <= last; ++who) {
           if (who == pair) continue;
-          const int* theirs = slot_of(who) + group * kCols * kChannels + ch;
+          const int* theirs = slot_of(who);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) acc[c] += static_cast<uint32_t>(__ldcg(theirs + c * kChannels));
         }
       }
-      if constexpr (kSums) {
-        store_sums<NT>(p, scales, acc, lane);
-      } else {
-        if (!one) {
+      const Part<NT, OUT> part(p, tile, ch0, group * kCols, lane);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) acc[c] = __float_as_uint(__int2float_rn(static_cast<int>(acc[c])));
+      for (int c = 0; c < kCols; c += kSlab) {
+        if constexpr (OUT != 0) {
+#pragma unroll
+          for (int i = 0; i < kSlab; ++i) acc[c + i] = __float_as_uint(__int2float_rn(static_cast<int>(acc[c + i])));
         }
-        store_tile<NT, OUT == 2>(p, scales, acc, lane);
+        store_slab<NT, OUT>(p, &tmap_out, part, c, acc + c, ob, lane);
       }
     }
+    if (OUT == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0 && !aborted()) give_up(kErrConsumerTimeout);
   }
 
@@ -673,36 +796,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
-// 8-bit rows to fp16, [m][pitch], zero past k: eight values a thread.
+// 8-bit rows to fp16, [m][pitch], zero past k: eight values a thread, and the
+// largest sum of magnitudes of 128 values (16 threads') into block_l1.
 __global__ void __launch_bounds__(256)
-    expand_rows_kernel(const int8_t* __restrict__ a, int64_t ld_a, int64_t m, int k, __half* __restrict__ x, int pitch) {
+    expand_rows_kernel(const int8_t* __restrict__ a, int64_t ld_a, int64_t m, int k, __half* __restrict__ x, int pitch,
+                       unsigned* __restrict__ block_l1) {
   pdl_launch_dependents();  // the product may become resident now; it waits for these rows
-  const int per = pitch / 8;
+  const int per = pitch / 8;  // a multiple of 16
   const bool wide = (reinterpret_cast<uintptr_t>(a) & 7) == 0 && ld_a % 8 == 0;
-  for (int64_t g = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; g < m * per;
+  unsigned top = 0;
+  const int64_t groups = m * per;
+  for (int64_t g = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; g < (groups + 31) / 32 * 32;
        g += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t i = g / per;
-    const int c = static_cast<int>(g - i * per) * 8;
-    const int8_t* src = a + i * ld_a + c;
     uint2 raw = make_uint2(0u, 0u);
-    if (wide && c + 8 <= k) {
-      raw = *reinterpret_cast<const uint2*>(src);
-    } else if (c < k) {
-      uint32_t w[2] = {0u, 0u};
+    if (g < groups) {
+      const int64_t i = g / per;
+      const int c = static_cast<int>(g - i * per) * 8;
+      const int8_t* src = a + i * ld_a + c;
+      if (wide && c + 8 <= k) {
+        raw = *reinterpret_cast<const uint2*>(src);
+      } else if (c < k) {
+        uint32_t w[2] = {0u, 0u};
 #pragma unroll
-      for (int b = 0; b < 8; ++b)
-        if (c + b < k) w[b >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[b])) << (8 * (b & 3));
-      raw = make_uint2(w[0], w[1]);
+        for (int b = 0; b < 8; ++b)
+          if (c + b < k) w[b >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[b])) << (8 * (b & 3));
+        raw = make_uint2(w[0], w[1]);
+      }
+      uint4 out;
+      bytes_to_f16(raw.x, out.x, out.y);
+      bytes_to_f16(raw.y, out.z, out.w);
+      *reinterpret_cast<uint4*>(x + i * pitch + c) = out;
     }
-    uint4 out;
-    bytes_to_f16(raw.x, out.x, out.y);
-    bytes_to_f16(raw.y, out.z, out.w);
-    *reinterpret_cast<uint4*>(x + i * pitch + c) = out;
+    unsigned l1 = __dp4a(__vabs4(raw.x), 0x01010101u, __dp4a(__vabs4(raw.y), 0x01010101u, 0u));
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) l1 += __shfl_xor_sync(kFullMask, l1, d);
+    top = max(top, l1);
+  }
+  __shared__ unsigned part[8];
+  top = __reduce_max_sync(kFullMask, top);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = max(top, part[w]);
+    atomicMax(block_l1, top);
   }
 }
 
 bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols, int64_t rows, int64_t pitch_bytes,
-              int box_cols, int box_rows) {
+              int box_cols, int box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -710,18 +852,22 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int6
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NT, int OUT>
 cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t st) {
-  CUtensorMap mx, mw;
+  CUtensorMap mx, mw, mo;
   const int pitch = matmul_i8_pitch(a.k);
   if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, w.rows_f16, pitch, a.m, int64_t(pitch) * 2, kDepth / 2, NT / 2) ||
       !make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.b, a.k, a.n, a.ld_b, kDepth, kChannels))
     return cudaErrorInvalidValue;
   Params p;
+  p.tma_out = OUT == 2 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.ld_out % 8 == 0 &&
+              make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.out, a.n, a.m, a.ld_out * 2, 32, Shape<NT, OUT>::kSlab,
+                       CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!p.tma_out) mo = mx;
   p.out = a.out;
   p.a_scale = a.a_scale;
   p.b_scale = a.b_scale;
@@ -734,6 +880,8 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   p.token_tiles = static_cast<int>((a.m + NT - 1) / NT);
   p.tiles = static_cast<int>((a.n + kPairChannels - 1) / kPairChannels * p.token_tiles);
   p.read_once = p.token_tiles == 1;
+  p.block_l1 = w.block_l1;
+  p.block_l1_next = w.block_l1_next;
   p.partial = w.partial;
   p.arrived = w.arrived;
   p.err = w.err;
@@ -748,12 +896,12 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   auto fn = matmul_i8_pair_kernel<NT, OUT>;
   static PerDeviceOnce once;
   const cudaError_t limit = once.run(
-      [fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NT>::kSmem); });
+      [fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NT, OUT>::kSmem); });
   if (limit != cudaSuccess) return limit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(Shape<NT>::kSmem);
+  cfg.dynamicSmemBytes = static_cast<size_t>(Shape<NT, OUT>::kSmem);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -764,7 +912,7 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fn, mx, mw, p);
+  return cudaLaunchKernelEx(&cfg, fn, mx, mw, mo, p);
 }
 
 template <int NT>
@@ -787,11 +935,12 @@ bool matmul_i8_tc_fits(const MatmulI8Launch& a) {
          stages < 2.0e9;
 }
 
-cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, void* rows_f16, int num_sms,
+cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, const MatmulI8Workspace& w,
                                cudaStream_t st) {
   const int pitch = matmul_i8_pitch(k);
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((m * (pitch / 8) + 255) / 256, int64_t(num_sms) * 16));
-  expand_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ld_a, m, k, static_cast<__half*>(rows_f16), pitch);
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((m * (pitch / 8) + 255) / 256, int64_t(w.num_sms) * 16));
+  expand_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ld_a, m, k, static_cast<__half*>(w.rows_f16), pitch,
+                                                                   w.block_l1);
   return cudaGetLastError();
 }
 

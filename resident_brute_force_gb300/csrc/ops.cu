@@ -29,6 +29,8 @@ struct rbf_ops {
   float* row_scale = nullptr;    // linear_i8_dev: the rows' scales
   int* partial = nullptr;        // the product's partial sums of shared tiles
   unsigned* arrived = nullptr;   // and their counters
+  unsigned* block_l1 = nullptr;  // two words, used by turns: a product clears the next one's
+  int turn = 0;
   int* errw = nullptr;           // error bits of the kernels since the last check
   uint64_t timeout_ns = 2000000000ull;  // bound on every device-side wait
 
@@ -61,6 +63,7 @@ void release(rbf_ops* o) {
   cudaFree(o->row_scale);
   cudaFree(o->partial);
   cudaFree(o->arrived);
+  cudaFree(o->block_l1);
   cudaFree(o->errw);
   if (o->own_stream && o->stream) cudaStreamDestroy(o->stream);
   delete o;
@@ -90,11 +93,15 @@ rbf_status check_matmul(const rbf_ops* o, const MatmulI8Launch& a) {
   return RBF_OK;
 }
 
-MatmulI8Workspace workspace(rbf_ops* o) {
+// The workspace of the next product.
+MatmulI8Workspace take_workspace(rbf_ops* o) {
   MatmulI8Workspace w;
   w.rows_f16 = o->rows_f16;
   w.partial = o->partial;
   w.arrived = o->arrived;
+  w.block_l1 = o->block_l1 + o->turn;
+  o->turn ^= 1;
+  w.block_l1_next = o->block_l1 + o->turn;
   w.err = o->errw;
   w.num_sms = o->num_sms;
   w.timeout_ns = o->timeout_ns;
@@ -132,6 +139,7 @@ rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream
                   cudaMalloc(&o->partial, matmul_i8_partial_bytes(o->num_sms)) == cudaSuccess &&
                   cudaMalloc(&o->arrived, o->num_sms * sizeof(unsigned)) == cudaSuccess &&
                   cudaMalloc(&o->row_scale, static_cast<size_t>(max_rows) * sizeof(float)) == cudaSuccess &&
+                  cudaMalloc(&o->block_l1, 2 * sizeof(unsigned)) == cudaSuccess &&
                   cudaMalloc(&o->errw, 4 * sizeof(int)) == cudaSuccess;
   if (!ok) {
     cudaGetLastError();
@@ -140,6 +148,7 @@ rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream
   }
   if (cudaMemsetAsync(o->errw, 0, 4 * sizeof(int), o->stream) != cudaSuccess ||
       cudaMemsetAsync(o->arrived, 0, o->num_sms * sizeof(unsigned), o->stream) != cudaSuccess ||
+      cudaMemsetAsync(o->block_l1, 0, 2 * sizeof(unsigned), o->stream) != cudaSuccess ||
       cudaStreamSynchronize(o->stream) != cudaSuccess) {
     release(o);
     return RBF_ERR_CUDA;
@@ -225,8 +234,9 @@ rbf_status matmul_i8_dev(rbf_ops* o, const int8_t* d_a, int64_t ld_a, const floa
     OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
     return RBF_OK;
   }
-  OPS_LAUNCH(o, launch_expand_rows(d_a, ld_a, m, k, o->rows_f16, o->num_sms, o->stream));
-  OPS_LAUNCH(o, launch_matmul_i8_tc(a, workspace(o), o->stream));
+  const MatmulI8Workspace w = take_workspace(o);
+  OPS_LAUNCH(o, launch_expand_rows(d_a, ld_a, m, k, w, o->stream));
+  OPS_LAUNCH(o, launch_matmul_i8_tc(a, w, o->stream));
   return RBF_OK;
 }
 
@@ -267,10 +277,12 @@ rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t
     OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
     return RBF_OK;
   }
-  q.f16 = o->rows_f16;
+  const MatmulI8Workspace w = take_workspace(o);
+  q.f16 = w.rows_f16;
   q.f16_pitch = matmul_i8_pitch(k);
+  q.block_l1 = w.block_l1;
   OPS_LAUNCH(o, launch_quantize_rows(q, o->stream));
-  OPS_LAUNCH(o, launch_matmul_i8_tc(a, workspace(o), o->stream));
+  OPS_LAUNCH(o, launch_matmul_i8_tc(a, w, o->stream));
   return RBF_OK;
 }
 

@@ -27,6 +27,7 @@ struct QuantizeLaunch {
   int64_t ld_q = 0;
   void* f16 = nullptr;
   int f16_pitch = 0;
+  unsigned* block_l1 = nullptr;  // with f16: the largest sum of |q| over 128 values of a row is put here (atomicMax)
   float* scale = nullptr;
 };
 cudaError_t launch_quantize_rows(const QuantizeLaunch& a, cudaStream_t stream);
@@ -57,6 +58,8 @@ struct MatmulI8Workspace {
   void* rows_f16 = nullptr;     // [m][matmul_i8_pitch(k)]
   int* partial = nullptr;       // matmul_i8_partial_bytes
   unsigned* arrived = nullptr;  // num_sms counters, zero between launches
+  unsigned* block_l1 = nullptr;       // largest sum of |a| over 128 values of a row; its writer found it zero
+  unsigned* block_l1_next = nullptr;  // the word of the next call, which the product clears
   int* err = nullptr;
   int num_sms = 0;
   uint64_t timeout_ns = 0;
@@ -64,7 +67,7 @@ struct MatmulI8Workspace {
 int matmul_i8_pitch(int k);  // fp16 numbers per workspace row
 size_t matmul_i8_partial_bytes(int num_sms);
 bool matmul_i8_tc_fits(const MatmulI8Launch& a);
-cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, void* rows_f16, int num_sms,
+cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, const MatmulI8Workspace& w,
                                cudaStream_t stream);
 cudaError_t launch_matmul_i8_tc(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t stream);
 

@@ -77,6 +77,7 @@ struct Out {
   int64_t ld_q;
   __half* f16;
   int pitch;
+  unsigned* block_l1;  // with f16: the largest sum of |q| over 128 values
   float* scale;
 };
 
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     if (o.f16) {
       for (int j = threadIdx.x; j < o.pitch; j += kQuantThreads)
         o.f16[r * o.pitch + j] = __float2half_rn(j < cols ? static_cast<float>(quantize_one(to_f32(row[j]), s)) : 0.0f);
+      if (threadIdx.x == 0) atomicMax(o.block_l1, 128u * 127u);  // the bound of any row: not worth a reduction here
     } else {
       for (int j = threadIdx.x; j < cols; j += kQuantThreads)
         o.q[r * o.ld_q + j] = static_cast<int8_t>(quantize_one(to_f32(row[j]), s));
@@ -152,10 +154,11 @@ __global__ void __launch_bounds__(kQuantThreads)
   const RowScale s = row_scale(THREADS == 32 ? __reduce_max_sync(kFullMask, top) : block_max(top));
   if (t == 0) o.scale[r] = s.scale;
   const int end = F16 ? o.pitch : cols;
+  float l1_top = 0.0f;
 #pragma unroll
   for (int g = 0; g < kHeld; ++g) {
     const int c = (g * THREADS + t) * 8;
-    if (c >= end) break;
+    if (c >= end) break;  // whole groups of 16 threads: the pitch is a multiple of 128
     // Rounded to whole numbers by adding and subtracting 1.5 * 2^23.
     float q[8];
 #pragma unroll
@@ -167,6 +170,14 @@ __global__ void __launch_bounds__(kQuantThreads)
       for (int i = 0; i < 4; ++i)
         h[i] = __floats2half2_rn(__fsub_rn(q[2 * i], 12582912.0f), __fsub_rn(q[2 * i + 1], 12582912.0f));
       *reinterpret_cast<uint4*>(o.f16 + r * o.pitch + c) = *reinterpret_cast<const uint4*>(h);
+      // 16 threads hold the 128 values of a stage.
+      float l1 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l1 += fabsf(q[i] - 12582912.0f);
+      const unsigned half = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) l1 += __shfl_xor_sync(half, l1, d);
+      l1_top = fmaxf(l1_top, l1);
     } else {
       uint32_t w[2];
 #pragma unroll
@@ -185,6 +196,11 @@ __global__ void __launch_bounds__(kQuantThreads)
       }
     }
   }
+  if constexpr (F16) {
+    const unsigned l1 = THREADS == 32 ? __reduce_max_sync(kFullMask, static_cast<unsigned>(l1_top))
+                                      : block_max(static_cast<unsigned>(l1_top));
+    if (t == 0) atomicMax(o.block_l1, l1);
+  }
 }
 
 template <typename T, bool F16>
@@ -194,6 +210,7 @@ cudaError_t launch_t(const QuantizeLaunch& a, cudaStream_t st) {
   o.ld_q = a.ld_q;
   o.f16 = static_cast<__half*>(a.f16);
   o.pitch = a.f16_pitch;
+  o.block_l1 = a.block_l1;
   o.scale = a.scale;
   const T* x = static_cast<const T*>(a.x);
   const bool aligned = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.ld_x * sizeof(T)) % 16 == 0 &&
