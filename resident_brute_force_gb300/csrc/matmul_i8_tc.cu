@@ -68,19 +68,20 @@ constexpr int kTmemCols = 512;       // the accumulator first, then the ring of 
 constexpr int kStageCols = kDepth / 2;
 constexpr int kRingBudget = 224 * 1024;
 
-// OUT: what is stored: 0 the sums (int32), 1 fp32, 2 a 16-bit type.
+// OUT: what is stored: 0 the sums (int32), 1 fp32, 2 bf16, 3 fp16.
 template <int NT, int OUT>
 struct Shape {
   static constexpr int kXBytes = NT * kDepth;          // NT / 2 tokens x 128 fp16
   static constexpr int kAcc = NT <= 128 ? 2 : 1;       // accumulators
-  static constexpr int kRing = (kTmemCols - kAcc * NT) / kStageCols;  // stages of the token ring and of the TMEM ring
+  static constexpr int kRing = (kTmemCols - kAcc * NT) / kStageCols;  // stages of the TMEM ring
+  static constexpr int kXRing = NT == 256 ? 3 : kRing;                 // stages of the token ring
   static constexpr int kCols = NT / kGroups;           // accumulator columns (tokens) of one worker warp
-  static constexpr int kSlab = kCols < 16 ? kCols : 16;  // tokens stored at a time
-  static constexpr int kStageOut = OUT == 2 ? kSlab * 64 : 0;  // a slab of 32 channels x 16 bits
-  static constexpr int kOutBytes = kWorkers * 2 * kStageOut;
-  static constexpr int kWStages = (kRingBudget - kRing * kXBytes - kOutBytes) / kWBytes;
-  static constexpr int kBars = 2 * kWStages + 3 * kRing + 2 * kAcc + 2;
-  static constexpr int kSmem = 1024 + kRing * kXBytes + kWStages * kWBytes + kOutBytes + kBars * 8 + 16;
+  static constexpr int kSlab = kCols < 16 ? kCols : 16;  // of those, read at a time
+  static constexpr int kStageOut = OUT >= 2 ? kCols * 64 : 0;  // a worker warp's results: 32 channels x 16 bits a token
+  static constexpr int kOutBytes = kWorkers * kStageOut;
+  static constexpr int kWStages = (kRingBudget - kXRing * kXBytes - kOutBytes) / kWBytes;
+  static constexpr int kBars = 2 * kWStages + kXRing + 2 * kRing + 2 * kAcc + 2;
+  static constexpr int kSmem = 1024 + kXRing * kXBytes + kWStages * kWBytes + kOutBytes + kBars * 8 + 16;
   static_assert(kRing >= kGroups && kWStages >= kGroups, "a group needs a slot of its own");
   static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
 };
@@ -92,7 +93,6 @@ struct Params {
   const float* bias;
   int64_t ld_out;
   int64_t m, n;
-  int out_dtype;
   int stages;        // per tile
   int token_tiles;
   int tiles;         // tiles x stages < 2^31
@@ -260,10 +260,29 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Two fp32 numbers in a register pair, one instruction for both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float low2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float high2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // A worker warp's part of a tile: 32 channels from j0 on, tokens i0 .. of which
 // `live` exist. Its sums are in registers as the tensor memory gives them out:
 //   OUT 0, 1: lane = channel, register = token;
-//   OUT 2: as the 8 x 8 blocks of a 16-bit matrix store: per 16 tokens, and for
+//   OUT 2, 3: as the 8 x 8 blocks of a 16-bit matrix store: per 16 tokens, and for
 //     each half of 16 channels, registers 4 j .. 4 j + 3 of a lane are tokens
 //     8 j + 2 (lane % 4) + {0, 1} of channels lane / 4 and lane / 4 + 8.
 // What they are multiplied by is read ahead of them.
@@ -271,7 +290,7 @@ template <int NT, int OUT>
 struct Part {
   using S = Shape<NT, OUT>;
   static constexpr int kWords = (S::kCols + 31) / 32;
-  static constexpr int kChan = OUT == 2 ? 4 : 1;  // channels of a lane
+  static constexpr int kChan = OUT >= 2 ? 4 : 1;  // channels of a lane
   int64_t j0, i0;
   int live;
   float sa[kWords];  // tokens lane, 32 + lane
@@ -284,7 +303,7 @@ struct Part {
     if constexpr (OUT != 0) {
 #pragma unroll
       for (int q = 0; q < kChan; ++q) {
-        const int64_t j = j0 + (OUT == 2 ? 8 * q + lane / 4 : lane);
+        const int64_t j = j0 + (OUT >= 2 ? 8 * q + lane / 4 : lane);
         sb[q] = p.b_scale && j < p.n ? p.b_scale[j] : 1.0f;
         add[q] = p.bias && j < p.n ? p.bias[j] : 0.0f;
       }
@@ -297,19 +316,52 @@ struct Part {
 // 16-bit results go through shared memory, where 8 x 8 blocks are stored
 // transposed (stmatrix): rows of one token's 32 channels, 64 bytes, in the
 // 64-byte swizzle (16-byte piece q of row r at q ^ (r / 2 % 4)) that spreads a
-// block's rows over all banks. From there a tiled TMA store writes the slab of
-// 16 tokens and clips it at the matrix' edges; where the output's rows are not
-// on 16-byte boundaries, the warp's lanes store it. `buf`: the warp's two slabs.
-struct OutBuf {
-  uint8_t* buf;
-  int which;
-};
+// block's rows over all banks. From there one tiled TMA store a warp and tile
+// writes them and clips them at the matrix' edges; where the output's rows are
+// not on 16-byte boundaries, the warp's lanes store them.
 
-// Scale and store tokens c0 .. c0 + kSlab - 1 of the part: r holds their sums,
-// integers for OUT 0 and fp32 numbers else.
+// The last tile's results have been read out of `buf`.
+template <int OUT>
+__device__ __forceinline__ void store_begin(int lane) {
+  if constexpr (OUT >= 2) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+  }
+}
+
 template <int NT, int OUT>
-__device__ __forceinline__ void store_slab(const Params& p, const CUtensorMap* map, const Part<NT, OUT>& t, int c0,
-                                           const uint32_t* r, OutBuf& ob, int lane) {
+__device__ __forceinline__ void store_end(const Params& p, const CUtensorMap* map, const Part<NT, OUT>& t, const uint8_t* buf,
+                                          int lane) {
+  if constexpr (OUT >= 2) {
+    if (t.j0 >= p.n || t.live == 0) return;
+    if (p.tma_out) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                     "r"(static_cast<int>(t.j0)), "r"(static_cast<int>(t.i0)), "r"(smem_addr(buf))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    } else {
+      __syncwarp();
+      uint16_t* o = static_cast<uint16_t*>(p.out) + t.i0 * p.ld_out + t.j0 + lane;
+      const bool mine = t.j0 + lane < p.n;
+#pragma unroll 8
+      for (int i = 0; i < t.live; ++i) {
+        const uint16_t v = *reinterpret_cast<const uint16_t*>(buf + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
+        if (mine) o[i * p.ld_out] = v;
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// Scale and store (16-bit types: put into `buf`) tokens c0 .. c0 + kSlab - 1 of
+// the part: r holds their sums, integers for OUT 0 and fp32 numbers else.
+template <int NT, int OUT>
+__device__ __forceinline__ void store_slab(const Params& p, const Part<NT, OUT>& t, int c0, const uint32_t* r, uint8_t* buf,
+                                           int lane) {
   using S = Shape<NT, OUT>;
   if (t.j0 >= p.n || c0 >= t.live) return;
   if constexpr (OUT == 0) {
@@ -327,53 +379,28 @@ __device__ __forceinline__ void store_slab(const Params& p, const CUtensorMap* m
     }
   } else {
     constexpr int kBlocks = S::kSlab / 8;
-    uint8_t* slab = ob.buf + ob.which * S::kStageOut;
-    ob.which ^= 1;
-    // The slab before last has been read.
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    __syncwarp();
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j) {
       const int tok = c0 + 8 * j + 2 * (lane & 3);
-      const float s0 = __shfl_sync(kFullMask, t.sa[c0 / 32], tok & 31);
-      const float s1 = __shfl_sync(kFullMask, t.sa[c0 / 32], (tok + 1) & 31);
+      const uint64_t sa2 = pack2(__shfl_sync(kFullMask, t.sa[c0 / 32], tok & 31), __shfl_sync(kFullMask, t.sa[c0 / 32], (tok + 1) & 31));
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t* e = r + ((q / 2) * kBlocks + j) * 4 + (q & 1) * 2;
-        const float v0 = __fmaf_rn(__fmul_rn(__uint_as_float(e[0]), s0), t.sb[q], t.add[q]);
-        const float v1 = __fmaf_rn(__fmul_rn(__uint_as_float(e[1]), s1), t.sb[q], t.add[q]);
-        if (p.out_dtype == kBF16) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+        const uint64_t v = fma2(mul2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])), sa2), pack2(t.sb[q], t.sb[q]), pack2(t.add[q], t.add[q]));
+        if constexpr (OUT == 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(low2(v), high2(v));
           w[q] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
-          const __half2 h = __floats2half2_rn(v0, v1);
+          const __half2 h = __floats2half2_rn(low2(v), high2(v));
           w[q] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
-      const int row = 8 * j + (lane & 7);
-      const uint32_t at = smem_addr(slab) + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4);
+      const int row = c0 + 8 * j + (lane & 7);
+      const uint32_t at = smem_addr(buf) + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4);
       asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
                    "r"(w[2]), "r"(w[3])
                    : "memory");
-    }
-    if (p.tma_out) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
-                     "r"(static_cast<int>(t.j0)), "r"(static_cast<int>(t.i0) + c0), "r"(smem_addr(slab))
-                     : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      }
-    } else {
-      __syncwarp();
-      uint16_t* o = static_cast<uint16_t*>(p.out) + (t.i0 + c0) * p.ld_out + t.j0 + lane;
-#pragma unroll
-      for (int i = 0; i < S::kSlab; ++i) {
-        const uint16_t v = *reinterpret_cast<const uint16_t*>(slab + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
-        if (t.j0 + lane < p.n && c0 + i < t.live) o[i * p.ld_out] = v;
-      }
     }
   }
 }
@@ -389,12 +416,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* xring = smem;
-  uint8_t* wring = smem + kRing * S::kXBytes;
-  uint8_t* outbuf = wring + S::kWStages * kWBytes;  // two slabs of results per worker warp
+  uint8_t* wring = smem + S::kXRing * S::kXBytes;
+  uint8_t* outbuf = wring + S::kWStages * kWBytes;  // 16-bit results of each worker warp
   uint64_t* w_full = reinterpret_cast<uint64_t*>(outbuf + S::kOutBytes);
   uint64_t* w_empty = w_full + S::kWStages;
   uint64_t* x_full = w_empty + S::kWStages;  // the even CTA's are used: both CTAs' tokens
-  uint64_t* c_full = x_full + kRing;         // the even CTA's are used: both CTAs' converted channels
+  uint64_t* c_full = x_full + S::kXRing;     // the even CTA's are used: both CTAs' converted channels
   uint64_t* done = c_full + kRing;           // the MMAs of a stage have read both rings
   uint64_t* acc_full = done + kRing;
   uint64_t* acc_empty = acc_full + S::kAcc;  // the even CTA's are used
@@ -417,9 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&w_full[s], 1);
       mbar_init(&w_empty[s], 4);
     }
+    for (int s = 0; s < S::kXRing; ++s) mbar_init(&x_full[s], 1);
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(&x_full[s], 1);
-      mbar_init(&c_full[s], 8);  // four warps of each CTA
+      mbar_init(&c_full[s], 8);  // four worker warps of each CTA
       mbar_init(&done[s], 1);
     }
     for (int b = 0; b < S::kAcc; ++b) {
@@ -492,16 +519,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       pdl_wait();  // the kernel before this one writes them
       const uint64_t policy = l2_policy_evict_last();
-      Slot<kRing> s;
-      int armed = 0;
+      Slot<S::kXRing> s;
+      Slot<kRing> over;  // the stage whose tokens this one's overwrite
+      int at = 0, armed = 0;
       bool ok = true;
       while (ok && walk.next(tile, k0, k1)) {
         const int row = tile % p.token_tiles * NT + static_cast<int>(rank) * (NT / 2);
-        for (int k = k0; k < k1; ++k) {
-          if (!mbar_wait(&done[s.i], s.phase ^ 1u, p.timeout_ns) || aborted()) {
-            if (!aborted()) give_up(kErrProducerTimeout);
-            ok = false;
-            break;
+        for (int k = k0; k < k1; ++k, ++at) {
+          if (at >= S::kXRing) {
+            if (!mbar_wait(&done[over.i], over.phase, p.timeout_ns) || aborted()) {
+              if (!aborted()) give_up(kErrProducerTimeout);
+              ok = false;
+              break;
+            }
+            over.advance();
           }
           if (leader) mbar_arrive_expect_tx(&x_full[s.i], 2 * S::kXBytes);
           const uint32_t bar = cluster_addr(&x_full[s.i], 0);
@@ -509,13 +540,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(dst, &tmap_x, k * kDepth, row, bar, policy);
           tma_load_2d_pair(dst + S::kXBytes / 2, &tmap_x, k * kDepth + kDepth / 2, row, bar, policy);
           s.advance();
-          if (armed < kRing) ++armed;
+          if (armed < S::kXRing) ++armed;
         }
       }
       if (!ok && leader) {
         for (; armed > 0; --armed) {
           if (s.i == 0) {
-            s.i = kRing;
+            s.i = S::kXRing;
             s.phase ^= 1u;
           }
           --s.i;
@@ -529,11 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp walks and waits, so that addresses and descriptors stay
     // in uniform registers, and one elected lane issues: 20 cycles an MMA of
     // 32 tokens instead of 45 from a branch on the lane's number. An MMA of
-    // 256 tokens takes 130, and few are queued, so the next stage's barriers
-    // are looked at while the second half of this one's is still to be issued.
+    // 256 tokens takes 130, and few are queued, so from 128 tokens on the next
+    // stage's barrier is looked at before the second half of this one is issued.
     if (leader) {
       constexpr uint32_t idesc = make_idesc(kPairChannels, NT, 0u);
+      constexpr bool kPeek = NT >= 128;
+      const bool even = (lane & 1) == 0;  // even lanes wait for the channels while odd ones wait for the tokens
       Slot<kRing> s;
+      Slot<S::kXRing> xs;
       Slot<S::kAcc> as;
       pdl_wait();
       const int exact = exact_stages(p);
@@ -541,18 +575,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && walk.next(tile, k0, k1)) {
         for (int k = k0; k < k1 && ok; k += exact) {
           const int kend = min(k + exact, k1);
-          ok = __all_sync(kFullMask, mbar_wait(&acc_empty[as.i], as.phase ^ 1u, p.timeout_ns)) && !aborted();
+          ok = __all_sync(kFullMask, mbar_wait(&acc_empty[as.i], as.phase ^ 1u, p.timeout_ns));
           const uint32_t d = tmem_base + static_cast<uint32_t>(as.i * NT);
           tc_fence_after();
           for (int kk = k; kk < kend && ok; ++kk) {
-            if (!ready) {
-              ok = __all_sync(kFullMask, mbar_wait(&x_full[s.i], s.phase, p.timeout_ns) &&
-                                             mbar_wait(&c_full[s.i], s.phase, p.timeout_ns));
+            if (!kPeek || !ready) {
+              ok = __all_sync(kFullMask, mbar_wait(even ? &c_full[s.i] : &x_full[xs.i], even ? s.phase : xs.phase, p.timeout_ns));
               if (!ok) break;
             }
             tc_fence_after();
-            const uint64_t b0 = sw128_kmajor_desc(xring + s.i * S::kXBytes);
-            const uint64_t b1 = sw128_kmajor_desc(xring + s.i * S::kXBytes + S::kXBytes / 2);
+            const uint64_t b0 = sw128_kmajor_desc(xring + xs.i * S::kXBytes);
+            const uint64_t b1 = sw128_kmajor_desc(xring + xs.i * S::kXBytes + S::kXBytes / 2);
             const uint32_t c = tmem_base + S::kAcc * NT + static_cast<uint32_t>(s.i * kStageCols);
             const bool one_lane = elect_one();
             if (one_lane) {
@@ -564,8 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             Slot<kRing> next = s;
             next.advance();
-            ready = __all_sync(kFullMask, mbar_try_wait(&x_full[next.i], next.phase) &&
-                                              mbar_try_wait(&c_full[next.i], next.phase));
+            xs.advance();
+            if (kPeek)
+              ready = __all_sync(kFullMask, mbar_try_wait(even ? &c_full[next.i] : &x_full[xs.i], even ? next.phase : xs.phase));
             if (one_lane) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -594,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = quad * 32 + lane;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t acc_empty_addr = cluster_addr(acc_empty, 0);
-    OutBuf ob{outbuf + (warp - 2) * 2 * S::kStageOut, 0};
+    uint8_t* outs = outbuf + (warp - 2) * S::kStageOut;
     const uint32_t c_full_addr = cluster_addr(c_full, 0);
     const int total = walk.total();
     bool ok = true;
@@ -621,16 +655,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const uint8_t* row = wring + ws.i * kWBytes + ch * kDepth;
         const uint32_t dst = lane_base + S::kAcc * NT + rs.i * kStageCols;
+        uint4 raw[2][2];  // 32 bytes, and the next 32
+        auto fetch = [&](int h) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) raw[h & 1][c] = *reinterpret_cast<const uint4*>(row + (((2 * h + c) ^ (ch & 7)) << 4));
+        };
+        fetch(0);
+        ok = fine(mbar_wait(&done[rs.i], rs.phase ^ 1u, p.timeout_ns));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          uint4 raw[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) raw[c] = *reinterpret_cast<const uint4*>(row + (((2 * h + c) ^ (ch & 7)) << 4));
-          if (h == 0) {
-            ok = fine(mbar_wait(&done[rs.i], rs.phase ^ 1u, p.timeout_ns));
-            if (!ok) break;
-            tc_fence_after();
-          }
+          if (h < 3) fetch(h + 1);
           if (h == 3) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&w_empty[ws.i]);
@@ -638,14 +674,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t f[16];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            bytes_to_f16(raw[c].x, f[8 * c + 0], f[8 * c + 1]);
-            bytes_to_f16(raw[c].y, f[8 * c + 2], f[8 * c + 3]);
-            bytes_to_f16(raw[c].z, f[8 * c + 4], f[8 * c + 5]);
-            bytes_to_f16(raw[c].w, f[8 * c + 6], f[8 * c + 7]);
+            const uint4 v = raw[h & 1][c];
+            bytes_to_f16(v.x, f[8 * c + 0], f[8 * c + 1]);
+            bytes_to_f16(v.y, f[8 * c + 2], f[8 * c + 3]);
+            bytes_to_f16(v.z, f[8 * c + 4], f[8 * c + 5]);
+            bytes_to_f16(v.w, f[8 * c + 6], f[8 * c + 7]);
           }
           tmem_st16(dst + 16 * h, f);
         }
-        if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -671,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       as.advance();
     };
     auto ld = [&](uint32_t at, uint32_t* v) {  // kSlab columns of the warp's 32 lanes
-      if constexpr (OUT == 2) {
+      if constexpr (OUT >= 2) {
         constexpr uint32_t kHalf = 16u << 16;  // TMEM lanes 16-31 of the warp's
         if constexpr (kSlab == 16) {
           tmem_ld_blocks2(at, v);
@@ -704,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // are stored. Two: the next slab is read while this one is stored.
         constexpr int kAhead = S::kAcc == 1 ? kCols / kSlab : 2;
         uint32_t v[kAhead][kSlab];
+        store_begin<OUT>(lane);
 #pragma unroll
         for (int i = 0; i < kAhead - (S::kAcc == 2); ++i) ld(from + i * kSlab, v[i]);
 #pragma unroll
@@ -716,8 +753,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kSlab; ++c) now[c] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(now[c])));
           }
-          store_slab<NT, OUT>(p, &tmap_out, part, i * kSlab, now, ob, lane);
+          store_slab<NT, OUT>(p, part, i * kSlab, now, outs, lane);
         }
+        store_end<NT, OUT>(p, &tmap_out, part, outs, lane);
         continue;
       }
       uint32_t acc[kCols];
@@ -776,16 +814,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const Part<NT, OUT> part(p, tile, ch0, group * kCols, lane);
+      store_begin<OUT>(lane);
 #pragma unroll
       for (int c = 0; c < kCols; c += kSlab) {
         if constexpr (OUT != 0) {
 #pragma unroll
           for (int i = 0; i < kSlab; ++i) acc[c + i] = __float_as_uint(__int2float_rn(static_cast<int>(acc[c + i])));
         }
-        store_slab<NT, OUT>(p, &tmap_out, part, c, acc + c, ob, lane);
+        store_slab<NT, OUT>(p, part, c, acc + c, outs, lane);
       }
+      store_end<NT, OUT>(p, &tmap_out, part, outs, lane);
     }
-    if (OUT == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (OUT >= 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0 && !aborted()) give_up(kErrConsumerTimeout);
   }
 
@@ -864,8 +904,8 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
       !make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.b, a.k, a.n, a.ld_b, kDepth, kChannels))
     return cudaErrorInvalidValue;
   Params p;
-  p.tma_out = OUT == 2 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.ld_out % 8 == 0 &&
-              make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.out, a.n, a.m, a.ld_out * 2, 32, Shape<NT, OUT>::kSlab,
+  p.tma_out = OUT >= 2 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.ld_out % 8 == 0 &&
+              make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.out, a.n, a.m, a.ld_out * 2, 32, Shape<NT, OUT>::kCols,
                        CU_TENSOR_MAP_SWIZZLE_64B);
   if (!p.tma_out) mo = mx;
   p.out = a.out;
@@ -875,7 +915,6 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   p.ld_out = a.ld_out;
   p.m = a.m;
   p.n = a.n;
-  p.out_dtype = a.out_dtype;
   p.stages = pitch / kDepth;
   p.token_tiles = static_cast<int>((a.m + NT - 1) / NT);
   p.tiles = static_cast<int>((a.n + kPairChannels - 1) / kPairChannels * p.token_tiles);
@@ -919,7 +958,8 @@ template <int NT>
 cudaError_t launch_out(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t st) {
   if (a.out_dtype == kI32) return launch_t<NT, 0>(a, w, st);
   if (a.out_dtype == kF32) return launch_t<NT, 1>(a, w, st);
-  return launch_t<NT, 2>(a, w, st);
+  if (a.out_dtype == kBF16) return launch_t<NT, 2>(a, w, st);
+  return launch_t<NT, 3>(a, w, st);
 }
 
 }  // namespace
