@@ -23,20 +23,21 @@
 // warp owns a contiguous part of that.
 //   1. One read from memory finds the largest score.
 //   2. Without top_k and top_p a second pass sums the weights, per warp.
-//   3. Else the second pass counts the scores in bins of 2^(1/64) in weight.
-//      The counts give the bin in which top_k ends, and bounds on the sum of
-//      weights above each bin edge that leave two or three bins in which top_p
-//      can end; if these hold more than a list, they are divided again.
-//      a. If all indices down to there fit a list (kListCap), they are
-//         gathered and one CTA finishes the row in it: sorted by key it knows
-//         the kept prefix, sorted again by index the choice.
-//      b. Else a third pass sums the weights above those bins, per warp, and
-//         gathers the scores in them; sorted, they give the key K.
-//   4. The warps' kept sums say which warp's part holds r; that part is divided
+//   3. top_k: of the threads' largest scores (distinct scores of the row), the
+//      k-th largest bounds the row's k-th from below, so one pass gathers
+//      little more than the k best into a list. top_p: a pass counts the
+//      scores in bins of 2^(1/64) in weight and sums the weights; the counts
+//      bound the sums above each bin edge, which leaves two or three bins in
+//      which the prefix can end.
+//   4. Few candidates (kSmall): one CTA finishes the row, every thread finding
+//      the rank and the running weight of its candidate by looking at all.
+//      Else the scores of those bins are gathered in a list, where K is found
+//      by halving, while the weights above them are summed, per warp.
+//   5. The warps' kept sums say which warp's part holds r; that part is divided
 //      among the warps again until one warp has it in its lanes.
-// Rows whose scores coincide so often that no bins divide them (thousands of
-// equal ones around the end of the prefix) find K by halving the interval of
-// keys, one pass over the row a step.
+// Where a list does not hold the bins' scores they are divided into finer
+// bins; scores that coincide by the thousand (no bins divide them) leave K to
+// be found by halving the interval of keys, one pass over the row a step.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,6 +59,9 @@ constexpr int kBinsPerOctave = 64;
 constexpr int kBins = 37 * kBinsPerOctave + 1;  // z = 0 .. -37, rounded
 constexpr int kBinsPerThread = (kBins + kThreads - 1) / kThreads;
 constexpr int kListCap = 2048;
+constexpr int kMaxHeld = 192 * 1024;  // of a row's scores in one CTA's shared memory
+constexpr int kMaxSmem = kMaxHeld + kListCap * 8;
+constexpr int kSmall = kThreads;  // candidates of a row that one CTA finishes
 
 using u64 = unsigned long long;
 
@@ -66,6 +70,7 @@ struct Vec;  // 16 bytes of scores
 template <>
 struct Vec<float> {
   static constexpr int kLen = 4;
+  static constexpr int kSame = 0;  // low bits of a score's code that its type leaves equal
   static constexpr uint32_t kNone = 0xFF800000u;  // -infinity
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x);
@@ -81,6 +86,7 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kLen = 8;
+  static constexpr int kSame = 16;
   static constexpr uint32_t kNone = 0xFF80FF80u;
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -98,6 +104,7 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<__half> {
   static constexpr int kLen = 8;
+  static constexpr int kSame = 13;
   static constexpr uint32_t kNone = 0xFC00FC00u;
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -225,10 +232,10 @@ struct Scale {
     ntop2 = pack2(-top, -top);
     rate2 = pack2(rate, rate);
   }
-  __device__ __forceinline__ float shift(float x) const { return inf ? (x == INFINITY ? 0.0f : -INFINITY) : x; }
-  // z of two scores.
-  __device__ __forceinline__ u64 z2(float a, float b) const { return mul2(add2(pack2(shift(a), shift(b)), ntop2), rate2); }
-  __device__ __forceinline__ float z(float x) const { return __fmul_rn(__fsub_rn(shift(x), top), rate); }
+  static __device__ __forceinline__ float shift(float x) { return x == INFINITY ? 0.0f : -INFINITY; }
+  // z of two scores that have been shifted where that is due.
+  __device__ __forceinline__ u64 z2(float a, float b) const { return mul2(add2(pack2(a, b), ntop2), rate2); }
+  __device__ __forceinline__ float z(float x) const { return __fmul_rn(__fsub_rn(inf ? shift(x) : x, top), rate); }
 };
 
 __device__ __forceinline__ u64 fixed(float e) { return static_cast<u64>(__float2ll_rn(__fmul_rn(e, kOne))); }
@@ -287,20 +294,16 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
 __device__ __forceinline__ void remote_store(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
-__device__ __forceinline__ u64 remote_load(uint32_t a) {
-  u64 v;
-  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void remote_add(uint32_t a, unsigned v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
 
 struct Shared {
   u64 part[kWarps];
   u64 slot[2][kMaxCluster];  // one word per CTA, written by all of them; two turns
   u64 kept[kWarps];          // the warps' kept sums
   u64 say[8];                // what CTA 0 has decided
+  u64 words[3][kMaxCluster]; // words that every CTA has sent to every other
+  u64 small_key[kSmall];     // candidates, and what they keep
+  u64 small_w[kSmall];
+  unsigned add_lo[kWarps], add_hi[kWarps];
   u64 scan[3][kWarps];
   int lo, hi;                // the vectors that still may hold the choice
   u64 before;                // kept sum ahead of them
@@ -347,30 +350,6 @@ struct Cta {
   }
 };
 
-// Descending bitonic sort of n (a power of two) words in shared memory.
-__device__ __forceinline__ void block_sort_desc(u64* list, int n) {
-  for (int k = 2; k <= n; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-        const u64 a = list[lo], b = list[hi];
-        if (((lo & k) == 0) == (a < b)) {
-          list[lo] = b;
-          list[hi] = a;
-        }
-      }
-    }
-  }
-  __syncthreads();
-}
-
-__device__ __forceinline__ int pow2_at_least(int n) {
-  int p = 32;
-  while (p < n) p <<= 1;
-  return p;
-}
-
 __device__ __forceinline__ float log_share(u64 w, u64 total) {
   return 2 * w < total ? logf(__fdiv_rn(__ull2float_rn(w), __ull2float_rn(total)))
                        : log1pf(-__fdiv_rn(__ull2float_rn(total - w), __ull2float_rn(total)));
@@ -384,28 +363,40 @@ struct Bracket {
   float origin = 0.0f, scale = 0.0f;
   int from = 0, to = kBins - 1;
 
+  // A bin is the rounding of -64 z to a whole number, which adding 2^23 leaves in the low bits of the fp32 pattern.
+  static constexpr uint32_t kPattern = 0x4B000000u;
+  static __device__ __forceinline__ u64 pattern2(u64 z2) {
+    constexpr float k = -static_cast<float>(kBinsPerOctave);
+    return fma2(z2, pack2(k, k), pack2(8388608.0f, 8388608.0f));
+  }
+  // The bin of a pattern; kBins or more for z under -37 (infinities have larger patterns).
+  static __device__ __forceinline__ uint32_t bin(float y) { return __float_as_uint(y) - kPattern; }
   // The position of a score (its order never decreases as z falls): below 0
   // for one above the finer bins, kBins or more for one that is past all.
-  __device__ __forceinline__ int at(float z) const {
-    const float y = __fmaf_rn(z, -static_cast<float>(kBinsPerOctave), 8388608.0f);
-    if (!(y < 8388608.0f + kBins)) return kBins;
-    const int v = static_cast<int>(__float_as_uint(y) - 0x4B000000u);
-    if (!fine) return v;
-    if (v < v0) return -1;
-    if (v > v1) return kBins;
+  __device__ __forceinline__ int at(float z, float y) const {
+    const uint32_t v = bin(y);
+    if (v >= static_cast<uint32_t>(kBins)) return kBins;
+    if (!fine) return static_cast<int>(v);
+    if (static_cast<int>(v) < v0) return -1;
+    if (static_cast<int>(v) > v1) return kBins;
     return min(max(static_cast<int>((-z - origin) * scale), 0), kBins - 1);
   }
-  // Bounds on the weight at a position of a bin that is not fine.
-  static __device__ __forceinline__ void bounds(int v, unsigned count, bool fine, const Bracket& b, u64& lower, u64& upper) {
-    const float zl = fine ? -(b.origin + static_cast<float>(v + 1) / b.scale) : -(v + 0.5f) / kBinsPerOctave;
-    const float zu = fine ? -(b.origin + static_cast<float>(v) / b.scale) : -(v - 0.5f) / kBinsPerOctave;
-    // 2^-14 covers the rounding of z and of the bins' edges, one unit the weight's own.
-    const float l = exp2f(zl) * kOne * (1.0f - 0x1p-14f), u = exp2f(zu) * kOne * (1.0f + 0x1p-14f);
-    const u64 lu = static_cast<u64>(l);
-    lower = lu > 0 ? (lu - 1) * count : 0;
-    upper = (static_cast<u64>(u) + 2) * count;
+  // z at the lower-weight edge of position p, and the step to the next one.
+  __device__ __forceinline__ float edge(int p) const {
+    return fine ? -(origin + static_cast<float>(p + 1) / scale) : -(static_cast<float>(p) + 0.5f) / kBinsPerOctave;
   }
+  __device__ __forceinline__ float step() const { return fine ? -1.0f / scale : -1.0f / kBinsPerOctave; }
 };
+// Bounds on the sum of `count` weights in a bin whose edges have the weights
+// `low` and `high`: 2^-14 covers the rounding of z and of the edges, one unit
+// the weight's own.
+__device__ __forceinline__ u64 lower_sum(float low, unsigned count) {
+  const u64 w = static_cast<u64>(low * (kOne * (1.0f - 0x1p-14f)));
+  return w > 0 ? (w - 1) * count : 0;
+}
+__device__ __forceinline__ u64 upper_sum(float high, unsigned count) {
+  return (static_cast<u64>(high * (kOne * (1.0f + 0x1p-14f))) + 2) * count;
+}
 
 template <typename T, bool HELD>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch a) {
@@ -460,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     }
     for (int e = lane; e < 2; e += 32) {
       const int w = e == 0 ? v0 : v1 - 1;
-      if (w < v0 || w >= v1 || (w >= f0 && w < f1)) continue;
+      if (v0 >= v1 || (e == 1 && w == v0) || (w >= f0 && w < f1)) continue;
       const uint4 raw = row.load(w);
       if constexpr (HELD) held[w - c0] = raw;
       best = vec_max<T>(best, raw);
@@ -498,25 +489,83 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     return;
   }
 
-  // f(z pair, vector, first of the two) for this warp's scores; after every
-  // kFlush vectors, g().
-  auto each_pair = [&](int from, int to, auto&& f, auto&& g) {
-    int since = 0;
-    for (int v = from + lane; v < to; v += 32) {
+  // f(scores, z pairs, vector) for this warp's vectors, four loads under way
+  // a lane; after at most kFlush vectors, g().
+  auto each = [&](auto&& f, auto&& g) {
+    auto one = [&](const uint4& raw, int v) {
       float x[E];
-      Vec<T>::unpack(get(v), x);
+      u64 z[E / 2];
+      Vec<T>::unpack(raw, x);
+      if (sc.inf) {
 #pragma unroll
-      for (int i = 0; i < E; i += 2) f(sc.z2(x[i], x[i + 1]), v, i, x[i], x[i + 1]);
-      if (++since == kFlush) {
+        for (int i = 0; i < E; ++i) x[i] = Scale::shift(x[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) z[i] = sc.z2(x[2 * i], x[2 * i + 1]);
+      f(x, z, v);
+    };
+    constexpr int kBatch = HELD ? 2 : 4;
+    int v = v0 + lane, since = 0;
+    for (; v + 32 * (kBatch - 1) < v1; v += 32 * kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) raw[i] = get(v + 32 * i);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) one(raw[i], v + 32 * i);
+      if ((since += kBatch) == kFlush) {
         g();
         since = 0;
       }
     }
     g();
+    for (; v < v1; v += 32) one(get(v), v);
+    g();
+  };
+  // The key of a score that `each` hands out.
+  auto key_of = [&](float x, int v, int i) {
+    return make_key(sc.inf && x == 0.0f ? INFINITY : x, static_cast<uint32_t>(index_of(v, i)));
+  };
+  // Put the scores of a vector that `mask` names into this CTA's list.
+  auto append = [&](unsigned mask, const float (&x)[E], int v) {
+    if (mask == 0) return;
+    unsigned at = atomicAdd(&s.list_len, static_cast<unsigned>(__popc(mask)));
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (mask >> i & 1u) {
+        if (at < kListCap) list[at] = key_of(x[i], v, i);
+        ++at;
+      }
+  };
+  // Clear the bits of the scores whose keys are under `cut`.
+  auto only_kept = [&](unsigned mask, const float (&x)[E], int v, u64 cut) {
+    if (cut != 0 && mask != 0) {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if ((mask >> i & 1u) && key_of(x[i], v, i) < cut) mask &= ~(1u << i);
+    }
+    return mask;
+  };
+  // Sum over CTA 0's threads of a value each, for all of them; `t` names one of three words a warp.
+  auto block_sum = [&](u64 v, int t) {
+    v = warp_sum(v);
+    if (lane == 0) s.scan[t][cta.warp] = v;
+    __syncthreads();
+    u64 r = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) r += s.scan[t][w];
+    return r;
+  };
+  // CTA 0's words [i0, i1) to the others.
+  auto tell = [&](int i0, int i1) {
+    __syncthreads();
+    if (cta.rank == 0 && threadIdx.x >= 1 && threadIdx.x < cta.size)
+      for (int i = i0; i < i1; ++i) remote_store(remote(&s.say[i], threadIdx.x), s.say[i]);
+    cta.sync();
   };
 
   const bool by_k = q.k < a.vocab, by_p = q.part_p < kAll;
-  u64 cut = 0;         // keys from here on are kept
+  u64 cut = 0;           // keys from here on are kept
+  bool summed = false;   // s.kept has the warps' kept sums
 
   // Kept weight of a score, once the cut is known.
   auto kept = [&](float x, int index) -> u64 {
@@ -524,335 +573,459 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     return e >= q.min_p && make_key(x, static_cast<uint32_t>(index)) >= cut ? fixed(e) : 0ull;
   };
 
-  if (by_k || by_p) {
-    // ---------------------------------------------------- 3. count by bins
-    Bracket br;
-    u64 above = 0;        // cluster-wide sum of weights ahead of the bracket
-    u64 count_above = 0;  // and number of scores
-    u64 sum_all = 0;      // sum of what top_k kept, once known
-    bool know_sum = !by_k;
-    bool for_k = by_k;    // which of the two ends is looked for
-    u64 kcut = 0;
-    u64 last_key = 0;     // the key at which the end that is looked for lies
-    for (;;) {
-      // Positions of all scores that may be kept: counts of the ones in the
-      // bracket's range, sum of the weights ahead of it.
-      for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
-      if (threadIdx.x == 0) s.list_len = 0;
-      cta.sync();
-      const bool sum_it = by_p && !for_k && (br.fine || !know_sum || sum_all == 0);
-      Mass m;
-      each_pair(
-          v0, v1,
-          [&](u64 z2, int v, int i, float xa, float xb) {
-            const float za = low2(z2), zb = high2(z2);
-            const int pa = br.at(za), pb = br.at(zb);
-            const bool ka = kcut == 0 || make_key(xa, index_of(v, i)) >= kcut;
-            const bool kb = kcut == 0 || make_key(xb, index_of(v, i + 1)) >= kcut;
-            if (ka && pa >= 0 && pa < kBins) atomicAdd(&hist[pa], 1u);
-            if (kb && pb >= 0 && pb < kBins) atomicAdd(&hist[pb], 1u);
-            if (sum_it) m.add(pack2(ka && (!br.fine || pa < 0) ? ex2(za) : 0.0f, kb && (!br.fine || pb < 0) ? ex2(zb) : 0.0f));
-          },
-          [&] { m.flush(); });
-      const u64 sum = sum_it ? cta.reduce<false>(m.total) : 0;  // of all, or of the ones ahead of the finer bins
-      if (sum_it && !br.fine) sum_all = sum;
-      if (sum_it && br.fine) above = sum;
-      // CTA 0 collects the counts.
-      __syncthreads();
-      if (cta.size > 1) {
-        if (cta.rank != 0)
-          for (int i = threadIdx.x; i < kBins; i += kThreads)
-            if (hist[i]) remote_add(remote(&hist[i], 0), hist[i]);
-        cta.sync();
-      }
-      const u64 target = for_k ? static_cast<u64>(q.k) : share(sum_all, q.part_p);
-      if (cta.rank == 0) {
-        // Running counts and bounds: a thread has kBinsPerThread bins.
-        u64 n = 0, lower = 0, upper = 0;
-        unsigned c[kBinsPerThread];
+  // Counts of the scores by position, and where a prefix ends that has `target`
+  // scores (for_k) or weight: say[0], say[1] the first and last position, say[2]
+  // scores ahead of the first, say[3] scores down to the last one, say[4] all.
+  // Each CTA adds up the cluster's counts for an equal part of the positions.
+  auto clear_counts = [&]() {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+    if (threadIdx.x == 0) s.list_len = 0;
+    cta.sync();
+  };
+  auto decide = [&](const Bracket& br, bool for_k, u64 target, u64 above, u64 count_above) {
+    cta.sync();  // all counts are there
+    const int per = (kBins + static_cast<int>(cta.size) * kThreads - 1) / (static_cast<int>(cta.size) * kThreads);  // a thread's
+    const int b0 = (static_cast<int>(cta.rank) * kThreads + static_cast<int>(threadIdx.x)) * per;
+    unsigned c[kBinsPerThread];
+    u64 n = 0, lower = 0, upper = 0;
+    const float step = br.step(), ratio = exp2f(step);
+    float low = exp2f(br.edge(b0)), high = exp2f(br.edge(b0) - step);
 #pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
-          const int b = threadIdx.x * kBinsPerThread + i;
-          c[i] = b < kBins ? hist[b] : 0u;
-          n += c[i];
-          if (!for_k && c[i]) {
-            u64 l, u;
-            Bracket::bounds(b, c[i], br.fine, br, l, u);
-            lower += l;
-            upper += u;
-          }
-        }
-        const u64 sn = warp_scan(n, lane), sl = warp_scan(lower, lane), su = warp_scan(upper, lane);
-        if (lane == 31) {
-          s.scan[0][cta.warp] = sn;
-          s.scan[1][cta.warp] = sl;
-          s.scan[2][cta.warp] = su;
-        }
-        if (threadIdx.x == 0) {
-          s.say[0] = kBins - 1;  // first position at which the end may lie
-          s.say[1] = kBins - 1;  // last one
-        }
-        __syncthreads();
-        u64 bn = count_above, bl = above, bu = above;
-        u64 all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < cta.warp) {
-            bn += s.scan[0][w];
-            bl += s.scan[1][w];
-            bu += s.scan[2][w];
-          }
-          all += s.scan[0][w];
-        }
-        bn += sn - n;
-        bl += sl - lower;
-        bu += su - upper;
-        // The thread in whose bins a running value passes the target.
-        u64 fn = bn, fl = bl, fu = bu;
-        for (int i = 0; i < kBinsPerThread; ++i) {
-          const int b = threadIdx.x * kBinsPerThread + i;
-          if (b >= kBins) break;
-          u64 l = 0, u = 0;
-          if (!for_k && c[i]) Bracket::bounds(b, c[i], br.fine, br, l, u);
-          if (for_k) {
-            if (fn < target && fn + c[i] >= target) s.say[0] = s.say[1] = b;
-          } else {
-            if (fu < target && fu + u >= target) s.say[0] = b;
-            if (fl < target && fl + l >= target) s.say[1] = b;
-          }
-          fn += c[i];
+    for (int i = 0; i < kBinsPerThread; ++i) c[i] = 0;
+    for (uint32_t o = 0; o < cta.size; ++o) {
+      const uint32_t from = remote(hist, o);
+#pragma unroll
+      for (int i = 0; i < kBinsPerThread; ++i) {
+        if (i >= per || b0 + i >= kBins) break;
+        unsigned got;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(got) : "r"(from + (b0 + i) * 4) : "memory");
+        c[i] += got;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBinsPerThread; ++i) {
+      if (i >= per) break;
+      n += c[i];
+      if (!for_k) {
+        lower += lower_sum(low, c[i]);
+        upper += upper_sum(high, c[i]);
+        high = low;
+        low *= ratio;
+      }
+    }
+    const u64 sn = warp_scan(n, lane), sl = warp_scan(lower, lane), su = warp_scan(upper, lane);
+    if (lane == 31) {
+      s.scan[0][cta.warp] = sn;
+      s.scan[1][cta.warp] = sl;
+      s.scan[2][cta.warp] = su;
+    }
+    if (threadIdx.x == 0) s.say[0] = s.say[1] = kBins - 1;
+    __syncthreads();
+    u64 fn = sn - n, fl = sl - lower, fu = su - upper, all_n = 0, all_l = 0, all_u = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < cta.warp) {
+        fn += s.scan[0][w];
+        fl += s.scan[1][w];
+        fu += s.scan[2][w];
+      }
+      all_n += s.scan[0][w];
+      all_l += s.scan[1][w];
+      all_u += s.scan[2][w];
+    }
+    // The CTAs' totals, and with them the values ahead of this one's part.
+    if (threadIdx.x < cta.size) {
+      remote_store(remote(&s.words[0][cta.rank], threadIdx.x), all_n);
+      remote_store(remote(&s.words[1][cta.rank], threadIdx.x), all_l);
+      remote_store(remote(&s.words[2][cta.rank], threadIdx.x), all_u);
+    }
+    cta.sync();
+    fn += count_above;
+    fl += above;
+    fu += above;
+    u64 all = count_above;
+    for (uint32_t o = 0; o < cta.size; ++o) {
+      if (o < cta.rank) {
+        fn += s.words[0][o];
+        fl += s.words[1][o];
+        fu += s.words[2][o];
+      }
+      all += s.words[0][o];
+    }
+    if (threadIdx.x == 0) {
+      s.say[2] = s.say[3] = all;
+      s.say[4] = all;
+    }
+    __syncthreads();
+    // The thread in whose bins a running value reaches the target tells all.
+    auto say = [&](int word, u64 v) {
+      for (uint32_t o = 0; o < cta.size; ++o) remote_store(remote(&s.say[word], o), v);
+    };
+    cta.sync();  // the words of say that are told have their defaults everywhere
+    if (for_k ? fn < target && fn + n >= target : (fl < target && fl + lower >= target) || (fu < target && fu + upper >= target)) {
+      low = exp2f(br.edge(b0));
+      high = exp2f(br.edge(b0) - step);
+#pragma unroll
+      for (int i = 0; i < kBinsPerThread; ++i) {
+        if (i >= per) break;
+        bool first = false, last = false;
+        if (for_k) {
+          first = last = fn < target && fn + c[i] >= target;
+        } else {
+          const u64 l = lower_sum(low, c[i]), u = upper_sum(high, c[i]);
+          first = fu < target && fu + u >= target;
+          last = fl < target && fl + l >= target;
           fl += l;
           fu += u;
+          high = low;
+          low *= ratio;
         }
-        __syncthreads();
-        // Counts ahead of the bracket, and in it.
-        const int from = static_cast<int>(s.say[0]), to = static_cast<int>(s.say[1]);
-        u64 ahead = 0, in = 0;
-#pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
-          const int b = threadIdx.x * kBinsPerThread + i;
-          if (b < from) ahead += c[i];
-          if (b >= from && b <= to) in += c[i];
+        if (first) {
+          say(0, static_cast<u64>(b0 + i));
+          say(2, fn);
         }
-        ahead = warp_sum(ahead);
-        in = warp_sum(in);
-        __syncthreads();
-        if (lane == 0) {
-          s.scan[0][cta.warp] = ahead;
-          s.scan[1][cta.warp] = in;
+        fn += c[i];
+        if (last) {
+          say(1, static_cast<u64>(b0 + i));
+          say(3, fn);
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          ahead = count_above;
-          in = 0;
-          for (int w = 0; w < kWarps; ++w) {
-            ahead += s.scan[0][w];
-            in += s.scan[1][w];
-          }
-          s.say[2] = ahead;
-          s.say[3] = in;
-          s.say[4] = count_above + all;  // scores down to the last position
-        }
-        __syncthreads();
-        if (cta.size > 1 && threadIdx.x >= 1 && threadIdx.x < cta.size)
-          for (int i = 0; i < 5; ++i) remote_store(remote(&s.say[i], threadIdx.x), s.say[i]);
       }
-      cta.sync();
+    }
+    cta.sync();
+  };
+
+  // All CTAs' lists behind CTA 0's; the number of keys (more than kListCap:
+  // they are not all there).
+  auto merge_lists = [&]() -> u64 {
+    __syncthreads();
+    if (cta.size == 1) return s.list_len;
+    const unsigned mine = s.list_len;
+    if (threadIdx.x < cta.size) remote_store(remote(&s.words[0][cta.rank], threadIdx.x), mine);
+    cta.sync();
+    u64 all = 0, at = 0;
+    for (uint32_t o = 0; o < cta.size; ++o) {
+      if (o < cta.rank) at += s.words[0][o];
+      all += s.words[0][o];
+    }
+    if (cta.rank != 0 && all <= kListCap)
+      for (unsigned i = threadIdx.x; i < mine; i += kThreads) remote_store(remote(&list[at + i], 0), list[i]);
+    cta.sync();
+    return all;
+  };
+
+  // The row's end in CTA 0: its n <= kSmall candidates are all that may be
+  // kept. Every thread takes one and looks at all of them. sum_all: what top_p
+  // is a share of (0: the sum of the q.k best of the candidates).
+  auto finish_small = [&](int n, u64 sum_all) {
+    const int t = threadIdx.x;
+    const u64 key = t < n ? list[t] : 0ull;
+    const float e = t < n ? ex2(sc.z(key_score(key))) : 0.0f;
+    const u64 w = fixed(e);
+    s.small_key[t] = key;
+    s.small_w[t] = w;
+    __syncthreads();
+    int rank = 0;
+    u64 ahead = 0;  // weight of the better candidates
+    for (int j = 0; j < n; ++j) {
+      const bool better = s.small_key[j] > key;
+      rank += better;
+      ahead += better ? s.small_w[j] : 0ull;
+    }
+    bool keep = t < n && rank < q.k;
+    if (by_p) {
+      const u64 sum = sum_all ? sum_all : block_sum(keep ? w : 0ull, 0);
+      keep = keep && ahead < share(sum, q.part_p);
+    }
+    keep = t < n && (rank == 0 || (keep && e >= q.min_p));
+    const u64 all = block_sum(keep ? w : 0ull, 1);  // also: everyone has read small_w
+    s.small_w[t] = keep ? w : 0ull;
+    __syncthreads();
+    const uint32_t low = static_cast<uint32_t>(key);  // falls as the index rises
+    u64 before = 0;
+    for (int j = 0; j < n; ++j) before += static_cast<uint32_t>(s.small_key[j]) > low ? s.small_w[j] : 0ull;
+    const u64 aim = share(all, q.part_u);
+    if (keep && before <= aim && aim < before + w) {
+      a.token[r] = static_cast<int32_t>(key_index(key));
+      if (a.logprob) a.logprob[r] = log_share(w, all);
+    }
+  };
+
+  // In CTA 0: the largest key K of the list for which `base` plus the number
+  // (for_k) or weight of its keys from K on reaches the target. Keys without
+  // the bits that are the same for all are divided into as many buckets as
+  // there are threads, then the keys of the bucket in which the target is
+  // reached again, until a bucket is one key.
+  auto list_cut = [&](int len, bool for_k, u64 base, u64 target) -> u64 {
+    constexpr int kSame = Vec<T>::kSame;
+    const int index_bits = 32 - __clz(a.vocab);
+    const u64 index_mask = (u64(1) << index_bits) - 1;
+    auto short_key = [&](u64 key) { return (key >> (32 + kSame)) << index_bits | (key & index_mask); };
+    u64 lo = ~0ull, hi = 0;
+    for (int j = threadIdx.x; j < len; j += kThreads) {
+      const u64 k = short_key(list[j]);
+      lo = umin64(lo, k);
+      hi = umax64(hi, k);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      lo = umin64(lo, __shfl_xor_sync(kFullMask, lo, m));
+      hi = umax64(hi, __shfl_xor_sync(kFullMask, hi, m));
+    }
+    if (lane == 0) {
+      s.scan[0][cta.warp] = lo;
+      s.scan[1][cta.warp] = hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      lo = umin64(lo, s.scan[0][w]);
+      hi = umax64(hi, s.scan[1][w]);
+    }
+    for (;;) {  // the target is reached within [lo, hi]
+      const int width = 64 - __clzll(static_cast<long long>(hi - lo));
+      const int shift = max(0, width - 8);  // kThreads = 2^8 buckets
+      s.small_w[threadIdx.x] = 0;
+      __syncthreads();
+      for (int j = threadIdx.x; j < len; j += kThreads) {
+        const u64 key = list[j], k = short_key(key);
+        if (k >= lo && k <= hi) atomicAdd(&s.small_w[(k - lo) >> shift], for_k ? 1ull : weight(key_score(key), sc));
+      }
+      __syncthreads();
+      // From the last bucket down: a thread has one.
+      const int bucket = kThreads - 1 - static_cast<int>(threadIdx.x);
+      const u64 w = s.small_w[bucket];
+      const u64 incl = warp_scan(w, lane);
+      if (lane == 31) s.scan[2][cta.warp] = incl;
+      __syncthreads();
+      u64 ahead = base + incl - w;
+#pragma unroll
+      for (int o = 0; o < kWarps; ++o)
+        if (o < cta.warp) ahead += s.scan[2][o];
+      if (ahead < target && ahead + w >= target) {
+        s.small_key[0] = static_cast<u64>(bucket);
+        s.small_key[1] = ahead;
+      }
+      __syncthreads();
+      lo += s.small_key[0] << shift;
+      base = s.small_key[1];
+      hi = umin64(hi, lo + ((u64(1) << shift) - 1));
+      if (shift == 0) break;
+    }
+    for (int j = threadIdx.x; j < len; j += kThreads)
+      if (short_key(list[j]) == lo) s.small_key[2] = list[j];
+    __syncthreads();
+    return s.small_key[2];
+  };
+
+  if (by_k) {
+    // ----------------------------------------------- 3. the k best, in a list
+    u64 n = kListCap + 1;
+    if (static_cast<u64>(q.k) <= static_cast<u64>(cta.size) * kThreads / 2) {
+      Bracket br;
+      clear_counts();
+      const float z = sc.z(x0[0]), y = __fmaf_rn(z, -static_cast<float>(kBinsPerOctave), 8388608.0f);
+      const int at = br.at(z, y);
+      if (at < kBins) atomicAdd(&hist[at], 1u);
+      decide(br, true, static_cast<u64>(q.k), 0, 0);
+      if (s.say[4] >= static_cast<u64>(q.k)) {
+        // Every score down to the bin of the k-th largest of the threads' largest.
+        const uint32_t last = static_cast<uint32_t>(s.say[1]) + Bracket::kPattern;
+        each(
+            [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
+              unsigned mask = 0;
+#pragma unroll
+              for (int i = 0; i < E / 2; ++i) {
+                const u64 y2 = Bracket::pattern2(z[i]);
+                mask |= (static_cast<uint32_t>(y2) <= last ? 1u : 0u) << (2 * i) | (static_cast<uint32_t>(y2 >> 32) <= last ? 2u : 0u) << (2 * i);
+              }
+              append(mask, x, v);
+            },
+            [&] {});
+        n = merge_lists();
+      }
+    }
+    if (n <= kSmall) {
+      if (cta.rank == 0) finish_small(static_cast<int>(n), 0);
+      return;
+    }
+    if (n <= kListCap) {
+      if (cta.rank == 0) {
+        const u64 key = list_cut(static_cast<int>(n), true, 0, static_cast<u64>(q.k));
+        if (threadIdx.x == 0) s.say[6] = key;
+      }
+      tell(6, 7);
+      cut = s.say[6];
+    }
+  }
+  if (by_p || (by_k && cut == 0)) {
+    // -------------------------------------- bins, for a large top_k, then top_p
+    Bracket br;
+    u64 above = 0;                      // sum of weights ahead of the finer bins
+    u64 count_above = 0;                // and number of scores
+    u64 sum_all = 0;                    // sum of what top_k kept
+    bool for_k = by_k && cut == 0;      // which of the two ends is looked for
+    for (;;) {
+      clear_counts();
+      const bool sum_it = !for_k;
+      Mass m;
+      if (!br.fine && cut == 0) {
+        each(
+            [&](const float (&)[E], const u64 (&z)[E / 2], int) {
+#pragma unroll
+              for (int i = 0; i < E / 2; ++i) {
+                const u64 y2 = Bracket::pattern2(z[i]);
+                const uint32_t ba = Bracket::bin(low2(y2)), bb = Bracket::bin(high2(y2));
+                if (ba < static_cast<uint32_t>(kBins)) atomicAdd(&hist[ba], 1u);
+                if (bb < static_cast<uint32_t>(kBins)) atomicAdd(&hist[bb], 1u);
+                if (sum_it) m.add(pack2(ex2(low2(z[i])), ex2(high2(z[i]))));
+              }
+            },
+            [&] { m.flush(); });
+      } else {
+        each(
+            [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
+              const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
+#pragma unroll
+              for (int i = 0; i < E / 2; ++i) {
+                const u64 y2 = Bracket::pattern2(z[i]);
+                const float za = low2(z[i]), zb = high2(z[i]);
+                const int pa = br.at(za, low2(y2)), pb = br.at(zb, high2(y2));
+                const bool ka = in >> (2 * i) & 1u, kb = in >> (2 * i + 1) & 1u;
+                if (ka && pa >= 0 && pa < kBins) atomicAdd(&hist[pa], 1u);
+                if (kb && pb >= 0 && pb < kBins) atomicAdd(&hist[pb], 1u);
+                if (sum_it) m.add(pack2(ka && (!br.fine || pa < 0) ? ex2(za) : 0.0f, kb && (!br.fine || pb < 0) ? ex2(zb) : 0.0f));
+              }
+            },
+            [&] { m.flush(); });
+      }
+      if (sum_it) {
+        const u64 sum = cta.reduce<false>(m.total);  // of all, or of the ones ahead of the finer bins
+        if (br.fine)
+          above = sum;
+        else
+          sum_all = sum;
+      }
+      const u64 target = for_k ? static_cast<u64>(q.k) : share(sum_all, q.part_p);
+      decide(br, for_k, target, above, count_above);
       br.from = static_cast<int>(s.say[0]);
       br.to = static_cast<int>(s.say[1]);
-      const u64 ahead = s.say[2], in = s.say[3], reach = s.say[4];
+      const u64 ahead = s.say[2], in = s.say[3] - s.say[2], reach = s.say[4];
+      u64 last_key;
       if (for_k && !br.fine && reach <= target) {
-        // Everything that has a weight is among the top_k.
-        for_k = false;
-        if (!by_p) break;  // nothing is cut
-        br = Bracket();
-        cta.sync();
-        continue;
-      }
-      const bool whole = ahead + in <= kListCap && !br.fine;  // all down to the bracket's end
-      if (!whole && in > kListCap && !br.fine) {
-        // Divide the bracket's bins again.
-        Bracket f;
-        f.fine = true;
-        f.v0 = br.from;
-        f.v1 = br.to;
-        f.origin = (br.from - 0.5f) / kBinsPerOctave;
-        f.scale = static_cast<float>(kBins) * kBinsPerOctave / static_cast<float>(br.to - br.from + 1);
-        br = f;
-        count_above = ahead;
-        cta.sync();  // CTA 0's words have been read
-        continue;
-      }
-      if (in <= kListCap || whole) {
-        // ------------------------------------------------------- gather
-        cta.sync();  // the counts are no longer needed
-        const int from = whole ? 0 : br.from;
-        Mass m2;
-        each_pair(
-            v0, v1,
-            [&](u64 z2, int v, int i, float xa, float xb) {
-              const float za = low2(z2), zb = high2(z2);
-              const int pa = br.at(za), pb = br.at(zb);
-              const u64 key_a = make_key(xa, index_of(v, i)), key_b = make_key(xb, index_of(v, i + 1));
-              if (pa >= from && pa <= br.to && key_a >= kcut) {
-                const unsigned n = atomicAdd(&s.list_len, 1u);
-                if (n < kListCap) list[n] = key_a;
-              }
-              if (pb >= from && pb <= br.to && key_b >= kcut) {
-                const unsigned n = atomicAdd(&s.list_len, 1u);
-                if (n < kListCap) list[n] = key_b;
-              }
-              if (!whole && by_p) m2.add(pack2(pa < from ? ex2(za) : 0.0f, pb < from ? ex2(zb) : 0.0f));
-            },
-            [&] { m2.flush(); });
-        if (!whole && by_p) above = cta.reduce<false>(m2.total);
-        cta.sync();
-        if (cta.rank == 0) {
-          // Append the other CTAs' keys.
-          int len = static_cast<int>(s.list_len);
-          for (uint32_t c = 1; c < cta.size; ++c) {
-            unsigned n;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n) : "r"(remote(&s.list_len, c)) : "memory");
-            for (unsigned i = threadIdx.x; i < n; i += kThreads)
-              if (len + static_cast<int>(i) < kListCap) list[len + i] = remote_load(remote(&list[i], c));
-            len += static_cast<int>(n);
-          }
-          len = min(len, kListCap);
-          const int size = pow2_at_least(len);
-          for (int i = len + threadIdx.x; i < size; i += kThreads) list[i] = 0;
-          block_sort_desc(list, size);
-          // Running weights in the order of the search: a thread has `per` keys.
-          const int per = (size + kThreads - 1) / kThreads;
-          u64 sum_here = 0;
-          for (int i = 0; i < per; ++i) {
-            const int j = threadIdx.x * per + i;
-            if (j < len) sum_here += weight(key_score(list[j]), sc);
-          }
-          const u64 incl = warp_scan(sum_here, lane);
-          if (lane == 31) s.scan[0][cta.warp] = incl;
-          __syncthreads();
-          u64 run = incl - sum_here;
-          for (int w = 0; w < cta.warp; ++w) run += s.scan[0][w];
-          if (whole) {
-            // Finish the row here. top_k's sum, then the kept prefix.
-            const int nk = for_k ? min(q.k, len) : len;
-            if (threadIdx.x == 0) {
-              s.say[5] = 0;
-              s.say[6] = 0;
-              s.say[7] = 1;
-            }
-            __syncthreads();
-            if (by_p && for_k) {
-              u64 t = run;
-              for (int i = 0; i < per; ++i) {
-                const int j = threadIdx.x * per + i;
-                if (j < len) t += weight(key_score(list[j]), sc);
-                if (j == nk - 1) s.say[5] = t;
-              }
-              __syncthreads();
-            }
-            const u64 goal = by_p ? share(for_k ? s.say[5] : sum_all, q.part_p) : ~0ull;
-            {
-              u64 t = run;
-              int mine = 0;
-              for (int i = 0; i < per; ++i) {
-                const int j = threadIdx.x * per + i;
-                if (j >= nk) break;
-                const float e = ex2(sc.z(key_score(list[j])));
-                if (j == 0 || (t < goal && e >= q.min_p)) ++mine;
-                t += fixed(e);
-              }
-              mine = __reduce_add_sync(kFullMask, mine);
-              if (lane == 0) atomicAdd(reinterpret_cast<unsigned*>(&s.say[6]), static_cast<unsigned>(mine));
-            }
-            __syncthreads();
-            const int nkeep = static_cast<int>(s.say[6]);
-            // In index order: the key's low word falls as the index rises.
-            const int size2 = pow2_at_least(nkeep);
-            for (int i = threadIdx.x; i < size2; i += kThreads) {
-              const u64 key = i < nkeep ? list[i] : 0ull;
-              list[i] = (key << 32) | (key >> 32);
-            }
-            block_sort_desc(list, size2);
-            const int per2 = (size2 + kThreads - 1) / kThreads;
-            u64 here = 0;
-            for (int i = 0; i < per2; ++i) {
-              const int j = threadIdx.x * per2 + i;
-              if (j < nkeep) here += weight(score_from_code(static_cast<uint32_t>(list[j])), sc);
-            }
-            const u64 in2 = warp_scan(here, lane);
-            __syncthreads();
-            if (lane == 31) s.scan[0][cta.warp] = in2;
-            __syncthreads();
-            u64 t = in2 - here, w_all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-              if (w < cta.warp) t += s.scan[0][w];
-              w_all += s.scan[0][w];
-            }
-            const u64 aim = share(w_all, q.part_u);
-            for (int i = 0; i < per2; ++i) {
-              const int j = threadIdx.x * per2 + i;
-              if (j >= nkeep) break;
-              const u64 w = weight(score_from_code(static_cast<uint32_t>(list[j])), sc);
-              if (t <= aim && aim < t + w) {
-                a.token[r] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(list[j] >> 32));
-                if (a.logprob) a.logprob[r] = log_share(w, w_all);
-              }
-              t += w;
-            }
-          } else {
-            // The key at which the prefix ends.
-            if (threadIdx.x == 0) s.say[5] = list[len > 0 ? len - 1 : 0];
-            __syncthreads();
-            u64 t = above + run;
-            for (int i = 0; i < per; ++i) {
-              const int j = threadIdx.x * per + i;
-              if (j >= len) break;
-              const u64 w = weight(key_score(list[j]), sc);
-              if (for_k ? ahead + j + 1 == target : (t < target && t + w >= target)) {
-                s.say[5] = list[j];
-                s.say[6] = t + w;
-              }
-              t += w;
-            }
-            __syncthreads();
-            if (threadIdx.x >= 1 && threadIdx.x < cta.size)
-              for (int i = 5; i < 7; ++i) remote_store(remote(&s.say[i], threadIdx.x), s.say[i]);
-          }
-        }
-        cta.sync();
-        if (whole) return;  // CTA 0 has finished the row, and nobody reads another's memory any more
-        last_key = s.say[5];
+        last_key = 0;  // everything that has a weight is among the top_k
       } else {
-        // Equal scores by the thousand: halve the interval of keys.
-        u64 lo = kcut, hi = make_key(top, 0) + 1;
-        while (hi - lo > 1) {
-          const u64 mid = lo + (hi - lo) / 2;
-          u64 c = 0;
-          for (int v = v0 + lane; v < v1; v += 32) {
-            float x[E];
-            Vec<T>::unpack(get(v), x);
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-              if (make_key(x[i], index_of(v, i)) >= mid) c += for_k ? 1ull : weight(x[i], sc);
-          }
-          if (cta.reduce<false>(c) >= target)
-            lo = mid;
-          else
-            hi = mid;
+        const bool small = !for_k && !br.fine && ahead + in <= kSmall;  // all that may be kept
+        if (!small && in > kListCap && !br.fine) {
+          // Divide the bins again.
+          Bracket f;
+          f.fine = true;
+          f.v0 = br.from;
+          f.v1 = br.to;
+          f.origin = (br.from - 0.5f) / kBinsPerOctave;
+          f.scale = static_cast<float>(kBins) * kBinsPerOctave / static_cast<float>(br.to - br.from + 1);
+          br = f;
+          count_above = ahead;
+          cta.sync();  // what CTA 0 said has been read
+          continue;
         }
-        last_key = lo;
-        cta.sync();
+        if (small || in <= kListCap) {
+          // ------------------------------------------------- 4. gather
+          const int from = small ? 0 : br.from;
+          Mass m2;
+          if (!br.fine) {
+            const uint32_t first = static_cast<uint32_t>(from) + Bracket::kPattern, width = static_cast<uint32_t>(br.to - from);
+            const float edge = __uint_as_float(first);
+            const bool weigh = !for_k && !small;
+            each(
+                [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
+                  unsigned mask = 0;
+#pragma unroll
+                  for (int i = 0; i < E / 2; ++i) {
+                    const u64 y2 = Bracket::pattern2(z[i]);
+                    mask |= (static_cast<uint32_t>(y2) - first <= width ? 1u : 0u) << (2 * i) |
+                            (static_cast<uint32_t>(y2 >> 32) - first <= width ? 2u : 0u) << (2 * i);
+                    if (weigh) m2.add(pack2(low2(y2) < edge ? ex2(low2(z[i])) : 0.0f, high2(y2) < edge ? ex2(high2(z[i])) : 0.0f));
+                  }
+                  append(only_kept(mask, x, v, cut), x, v);
+                },
+                [&] { m2.flush(); });
+          } else {
+            each(
+                [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
+                  unsigned mask = 0;
+#pragma unroll
+                  for (int i = 0; i < E / 2; ++i) {
+                    const u64 y2 = Bracket::pattern2(z[i]);
+                    const int pa = br.at(low2(z[i]), low2(y2)), pb = br.at(high2(z[i]), high2(y2));
+                    mask |= (pa >= from && pa <= br.to ? 1u : 0u) << (2 * i) | (pb >= from && pb <= br.to ? 2u : 0u) << (2 * i);
+                    if (!for_k) m2.add(pack2(pa < from ? ex2(low2(z[i])) : 0.0f, pb < from ? ex2(high2(z[i])) : 0.0f));
+                  }
+                  append(only_kept(mask, x, v, cut), x, v);
+                },
+                [&] { m2.flush(); });
+          }
+          if (!for_k && !small) {
+            above = cta.reduce<false>(m2.total);
+            const u64 own = warp_sum(m2.total);
+            if (lane == 0) s.kept[cta.warp] = own;
+          }
+          const int len = static_cast<int>(merge_lists());
+          if (small) {
+            if (cta.rank == 0) finish_small(len, sum_all);
+            return;
+          }
+          if (cta.rank == 0) {
+            const u64 key = list_cut(len, for_k, for_k ? ahead : above, target);
+            if (threadIdx.x == 0) s.say[6] = key;
+          }
+          tell(6, 7);
+          last_key = s.say[6];
+          if (!for_k && q.min_p == 0.0f) {
+            // The warps' kept sums: the weights ahead of the bins, and this
+            // CTA's keys of the list (its first ones, in CTA 0's too).
+            summed = true;
+            const int own_len = static_cast<int>(s.list_len);
+            if (threadIdx.x < kWarps) s.add_lo[threadIdx.x] = s.add_hi[threadIdx.x] = 0;
+            __syncthreads();
+            for (int j = threadIdx.x; j < own_len; j += kThreads) {
+              const u64 key = list[j];
+              if (key < last_key) continue;
+              const u64 w = weight(key_score(key), sc);
+              const int v = (static_cast<int>(key_index(key)) + row.lead) / E;
+              int o = static_cast<int>(int64_t(v - c0) * kWarps / (c1 - c0));
+              while (v >= part_of(c0, c1, o + 1)) ++o;  // the division may round down across a part's start
+              atomicAdd(&s.add_lo[o], static_cast<unsigned>(w & 0xFFFFFu));  // at most 2^11 of them
+              atomicAdd(&s.add_hi[o], static_cast<unsigned>(w >> 20));
+            }
+            __syncthreads();
+            if (threadIdx.x < kWarps)
+              s.kept[threadIdx.x] += (static_cast<u64>(s.add_hi[threadIdx.x]) << 20) + s.add_lo[threadIdx.x];
+          }
+        } else {
+          // Equal scores by the thousand: halve the interval of keys.
+          u64 lo = cut, hi = make_key(top, 0) + 1;
+          while (hi - lo > 1) {
+            const u64 mid = lo + (hi - lo) / 2;
+            u64 c = 0;
+            for (int v = v0 + lane; v < v1; v += 32) {
+              float x[E];
+              Vec<T>::unpack(get(v), x);
+#pragma unroll
+              for (int i = 0; i < E; ++i)
+                if (make_key(x[i], static_cast<uint32_t>(index_of(v, i))) >= mid) c += for_k ? 1ull : weight(x[i], sc);
+            }
+            if (cta.reduce<false>(c) >= target)
+              lo = mid;
+            else
+              hi = mid;
+          }
+          last_key = lo;
+        }
       }
-      if (!for_k) {
-        cut = last_key;
-        break;
-      }
-      kcut = cut = last_key;
-      for_k = false;
-      if (!by_p) break;
+      cut = last_key;
+      if (!for_k || !by_p) break;
       // Now top_p, among what top_k kept.
-      know_sum = false;
-      sum_all = 0;
+      for_k = false;
       above = 0;
       count_above = 0;
       br = Bracket();
@@ -861,19 +1034,23 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
   }
 
   // ------------------------------------------------- the warps' kept sums
-  Mass m;
-  each_pair(
-      v0, v1,
-      [&](u64 z2, int v, int i, float xa, float xb) {
-        float ea = ex2(low2(z2)), eb = ex2(high2(z2));
-        if (ea < q.min_p || (cut != 0 && make_key(xa, index_of(v, i)) < cut)) ea = 0.0f;
-        if (eb < q.min_p || (cut != 0 && make_key(xb, index_of(v, i + 1)) < cut)) eb = 0.0f;
-        m.add(pack2(ea, eb));
-      },
-      [&] { m.flush(); });
-  const u64 total = cta.reduce<false>(m.total);
-  const u64 own = warp_sum(m.total);
-  if (lane == 0) s.kept[cta.warp] = own;
+  if (!summed) {
+    Mass m;
+    each(
+        [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
+          const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            const float ea = ex2(low2(z[i])), eb = ex2(high2(z[i]));
+            m.add(pack2((in >> (2 * i) & 1u) && ea >= q.min_p ? ea : 0.0f, (in >> (2 * i + 1) & 1u) && eb >= q.min_p ? eb : 0.0f));
+          }
+        },
+        [&] { m.flush(); });
+    const u64 own = warp_sum(m.total);
+    if (lane == 0) s.kept[cta.warp] = own;
+  }
+  __syncthreads();
+  const u64 total = cta.reduce<false>(lane == 0 ? s.kept[cta.warp] : 0ull);
   const u64 aim = share(total, q.part_u);
   u64 before = 0;
   u64 mine_all = total;
@@ -949,7 +1126,7 @@ cudaError_t launch_t(const SampleLaunch& a, int cluster, int held_bytes, cudaStr
   auto fn = sample_kernel<T, HELD>;
   static PerDeviceOnce once;
   const cudaError_t ready = once.run([fn] {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, max_dynamic_smem() - 2048);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (ready != cudaSuccess) return ready;
@@ -976,7 +1153,7 @@ cudaError_t launch_rows(const SampleLaunch& a, cudaStream_t st) {
   int cluster = 1;
   while (cluster < kMaxCluster && bytes / cluster > 32 * 1024) cluster *= 2;
   const int64_t held = (bytes + cluster - 1) / cluster / 16 * 16 + 32;
-  if (held <= 64 * 1024) return launch_t<T, true>(a, cluster, static_cast<int>(held), st);
+  if (held <= kMaxHeld) return launch_t<T, true>(a, cluster, static_cast<int>(held), st);
   return launch_t<T, false>(a, cluster, 0, st);
 }
 
