@@ -26,7 +26,7 @@
 //   3. top_k: of the threads' largest scores (distinct scores of the row), the
 //      k-th largest bounds the row's k-th from below, so one pass gathers
 //      little more than the k best into a list. top_p: a pass counts the
-//      scores in bins of 2^(1/64) in weight and sums the weights; the counts
+//      scores in bins of 2^(1/128) in weight and sums the weights; the counts
 //      bound the sums above each bin edge, which leaves two or three bins in
 //      which the prefix can end.
 //   4. Few candidates (kSmall): one CTA finishes the row, every thread finding
@@ -55,10 +55,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kOne = 68719476736.0f;  // 2^36: the largest weight
-constexpr int kBinsPerOctave = 64;
+constexpr int kBinsPerOctave = 128;
 constexpr int kBins = 37 * kBinsPerOctave + 1;  // z = 0 .. -37, rounded
-constexpr int kBinsPerThread = (kBins + kThreads - 1) / kThreads;
-constexpr int kListCap = 2048;
+constexpr int kQuads = (kBins + 3) / 4;  // the counts are read four at a time
+constexpr int kListCap = kQuads * 2;     // as many 8-byte keys as the counts of all bins take
 constexpr int kMaxHeld = 192 * 1024;  // of a row's scores in one CTA's shared memory
 constexpr int kMaxSmem = kMaxHeld + kListCap * 8;
 constexpr int kSmall = kThreads;  // candidates of a row that one CTA finishes
@@ -363,7 +363,7 @@ struct Bracket {
   float origin = 0.0f, scale = 0.0f;
   int from = 0, to = kBins - 1;
 
-  // A bin is the rounding of -64 z to a whole number, which adding 2^23 leaves in the low bits of the fp32 pattern.
+  // A bin is the rounding of -128 z to a whole number, which adding 2^23 leaves in the low bits of the fp32 pattern.
   static constexpr uint32_t kPattern = 0x4B000000u;
   static __device__ __forceinline__ u64 pattern2(u64 z2) {
     constexpr float k = -static_cast<float>(kBinsPerOctave);
@@ -578,39 +578,56 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
   // scores ahead of the first, say[3] scores down to the last one, say[4] all.
   // Each CTA adds up the cluster's counts for an equal part of the positions.
   auto clear_counts = [&]() {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < kQuads; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x == 0) s.list_len = 0;
     cta.sync();
   };
   auto decide = [&](const Bracket& br, bool for_k, u64 target, u64 above, u64 count_above) {
     cta.sync();  // all counts are there
-    const int per = (kBins + static_cast<int>(cta.size) * kThreads - 1) / (static_cast<int>(cta.size) * kThreads);  // a thread's
-    const int b0 = (static_cast<int>(cta.rank) * kThreads + static_cast<int>(threadIdx.x)) * per;
-    unsigned c[kBinsPerThread];
+    const int per = (kQuads + static_cast<int>(cta.size) * kThreads - 1) / (static_cast<int>(cta.size) * kThreads);  // a thread's
+    const int q0 = (static_cast<int>(cta.rank) * kThreads + static_cast<int>(threadIdx.x)) * per;
+    const int q1 = min(q0 + per, kQuads), b0 = 4 * q0;
+    // The cluster's counts of four positions, eight CTAs' loads under way at once.
+    auto count = [&](int quad) {
+      uint4 c = make_uint4(0u, 0u, 0u, 0u);
+      for (uint32_t o0 = 0; o0 < cta.size; o0 += 8) {
+        uint4 got[8];
+#pragma unroll
+        for (uint32_t o = 0; o < 8; ++o) {
+          got[o] = make_uint4(0u, 0u, 0u, 0u);
+          if (o0 + o < cta.size)
+            asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(got[o].x), "=r"(got[o].y), "=r"(got[o].z), "=r"(got[o].w)
+                         : "r"(remote(hist + 4 * quad, o0 + o))
+                         : "memory");
+        }
+#pragma unroll
+        for (uint32_t o = 0; o < 8; ++o) {
+          c.x += got[o].x;
+          c.y += got[o].y;
+          c.z += got[o].z;
+          c.w += got[o].w;
+        }
+      }
+      return c;
+    };
     u64 n = 0, lower = 0, upper = 0;
     const float step = br.step(), ratio = exp2f(step);
     float low = exp2f(br.edge(b0)), high = exp2f(br.edge(b0) - step);
+    for (int quad = q0; quad < q1; ++quad) {
+      const uint4 c4 = count(quad);
+      const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-    for (int i = 0; i < kBinsPerThread; ++i) c[i] = 0;
-    for (uint32_t o = 0; o < cta.size; ++o) {
-      const uint32_t from = remote(hist, o);
-#pragma unroll
-      for (int i = 0; i < kBinsPerThread; ++i) {
-        if (i >= per || b0 + i >= kBins) break;
-        unsigned got;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(got) : "r"(from + (b0 + i) * 4) : "memory");
-        c[i] += got;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBinsPerThread; ++i) {
-      if (i >= per) break;
-      n += c[i];
-      if (!for_k) {
-        lower += lower_sum(low, c[i]);
-        upper += upper_sum(high, c[i]);
-        high = low;
-        low *= ratio;
+      for (int i = 0; i < 4; ++i) {
+        n += c[i];
+        if (!for_k) {
+          if (c[i]) {
+            lower += lower_sum(low, c[i]);
+            upper += upper_sum(high, c[i]);
+          }
+          high = low;
+          low *= ratio;
+        }
       }
     }
     const u64 sn = warp_scan(n, lane), sl = warp_scan(lower, lane), su = warp_scan(upper, lane);
@@ -665,29 +682,33 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     if (for_k ? fn < target && fn + n >= target : (fl < target && fl + lower >= target) || (fu < target && fu + upper >= target)) {
       low = exp2f(br.edge(b0));
       high = exp2f(br.edge(b0) - step);
+      for (int quad = q0; quad < q1; ++quad) {
+        const uint4 c4 = count(quad);
+        const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-      for (int i = 0; i < kBinsPerThread; ++i) {
-        if (i >= per) break;
-        bool first = false, last = false;
-        if (for_k) {
-          first = last = fn < target && fn + c[i] >= target;
-        } else {
-          const u64 l = lower_sum(low, c[i]), u = upper_sum(high, c[i]);
-          first = fu < target && fu + u >= target;
-          last = fl < target && fl + l >= target;
-          fl += l;
-          fu += u;
-          high = low;
-          low *= ratio;
-        }
-        if (first) {
-          say(0, static_cast<u64>(b0 + i));
-          say(2, fn);
-        }
-        fn += c[i];
-        if (last) {
-          say(1, static_cast<u64>(b0 + i));
-          say(3, fn);
+        for (int i = 0; i < 4; ++i) {
+          const u64 b = static_cast<u64>(4 * quad + i);
+          bool first = false, last = false;
+          if (for_k) {
+            first = last = fn < target && fn + c[i] >= target;
+          } else {
+            const u64 l = c[i] ? lower_sum(low, c[i]) : 0, u = c[i] ? upper_sum(high, c[i]) : 0;
+            first = fu < target && fu + u >= target;
+            last = fl < target && fl + l >= target;
+            fl += l;
+            fu += u;
+            high = low;
+            low *= ratio;
+          }
+          if (first) {
+            say(0, b);
+            say(2, fn);
+          }
+          fn += c[i];
+          if (last) {
+            say(1, b);
+            say(3, fn);
+          }
         }
       }
     }
@@ -832,13 +853,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
         const uint32_t last = static_cast<uint32_t>(s.say[1]) + Bracket::kPattern;
         each(
             [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
-              unsigned mask = 0;
+              uint32_t near = 0xFFFFFFFFu;
+              u64 y2[E / 2];
 #pragma unroll
               for (int i = 0; i < E / 2; ++i) {
-                const u64 y2 = Bracket::pattern2(z[i]);
-                mask |= (static_cast<uint32_t>(y2) <= last ? 1u : 0u) << (2 * i) | (static_cast<uint32_t>(y2 >> 32) <= last ? 2u : 0u) << (2 * i);
+                y2[i] = Bracket::pattern2(z[i]);
+                near = min(near, min(static_cast<uint32_t>(y2[i]), static_cast<uint32_t>(y2[i] >> 32)));
               }
-              append(mask, x, v);
+              if (near <= last) {  // few vectors hold any
+                unsigned mask = 0;
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i)
+                  mask |= (static_cast<uint32_t>(y2[i]) <= last ? 1u : 0u) << (2 * i) | (static_cast<uint32_t>(y2[i] >> 32) <= last ? 2u : 0u) << (2 * i);
+                append(mask, x, v);
+              }
             },
             [&] {});
         n = merge_lists();
@@ -938,15 +966,22 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
             const bool weigh = !for_k && !small;
             each(
                 [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
-                  unsigned mask = 0;
+                  uint32_t near = 0xFFFFFFFFu;
+                  u64 y2[E / 2];
 #pragma unroll
                   for (int i = 0; i < E / 2; ++i) {
-                    const u64 y2 = Bracket::pattern2(z[i]);
-                    mask |= (static_cast<uint32_t>(y2) - first <= width ? 1u : 0u) << (2 * i) |
-                            (static_cast<uint32_t>(y2 >> 32) - first <= width ? 2u : 0u) << (2 * i);
-                    if (weigh) m2.add(pack2(low2(y2) < edge ? ex2(low2(z[i])) : 0.0f, high2(y2) < edge ? ex2(high2(z[i])) : 0.0f));
+                    y2[i] = Bracket::pattern2(z[i]);
+                    near = min(near, min(static_cast<uint32_t>(y2[i]) - first, static_cast<uint32_t>(y2[i] >> 32) - first));
+                    if (weigh) m2.add(pack2(low2(y2[i]) < edge ? ex2(low2(z[i])) : 0.0f, high2(y2[i]) < edge ? ex2(high2(z[i])) : 0.0f));
                   }
-                  append(only_kept(mask, x, v, cut), x, v);
+                  if (near <= width) {  // few vectors hold any
+                    unsigned mask = 0;
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i)
+                      mask |= (static_cast<uint32_t>(y2[i]) - first <= width ? 1u : 0u) << (2 * i) |
+                              (static_cast<uint32_t>(y2[i] >> 32) - first <= width ? 2u : 0u) << (2 * i);
+                    append(only_kept(mask, x, v, cut), x, v);
+                  }
                 },
                 [&] { m2.flush(); });
           } else {
@@ -994,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
               const int v = (static_cast<int>(key_index(key)) + row.lead) / E;
               int o = static_cast<int>(int64_t(v - c0) * kWarps / (c1 - c0));
               while (v >= part_of(c0, c1, o + 1)) ++o;  // the division may round down across a part's start
-              atomicAdd(&s.add_lo[o], static_cast<unsigned>(w & 0xFFFFFu));  // at most 2^11 of them
+              atomicAdd(&s.add_lo[o], static_cast<unsigned>(w & 0xFFFFFu));  // kListCap of them stay under 2^32
               atomicAdd(&s.add_hi[o], static_cast<unsigned>(w >> 20));
             }
             __syncthreads();
@@ -1038,11 +1073,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     Mass m;
     each(
         [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
-          const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
+          if (cut == 0) {
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            const float ea = ex2(low2(z[i])), eb = ex2(high2(z[i]));
-            m.add(pack2((in >> (2 * i) & 1u) && ea >= q.min_p ? ea : 0.0f, (in >> (2 * i + 1) & 1u) && eb >= q.min_p ? eb : 0.0f));
+            for (int i = 0; i < E / 2; ++i) {
+              const float ea = ex2(low2(z[i])), eb = ex2(high2(z[i]));
+              m.add(q.min_p == 0.0f ? pack2(ea, eb) : pack2(ea >= q.min_p ? ea : 0.0f, eb >= q.min_p ? eb : 0.0f));
+            }
+          } else {
+            const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+              const float ea = ex2(low2(z[i])), eb = ex2(high2(z[i]));
+              m.add(pack2((in >> (2 * i) & 1u) && ea >= q.min_p ? ea : 0.0f, (in >> (2 * i + 1) & 1u) && eb >= q.min_p ? eb : 0.0f));
+            }
           }
         },
         [&] { m.flush(); });
