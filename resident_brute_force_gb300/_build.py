@@ -23,7 +23,8 @@ CHECKS_BUILD_DIR = os.path.join(HERE, "_build_checks")
 CHECKS_LIB_PATH = os.path.join(HERE, "librbf_checks.so")
 
 SOURCES = ["engine.cu", "score_select.cu", "merge.cu", "topk_i32.cu", "noalloc.cu", "gemm_select.cu", "normalize.cu",
-           "ops.cu", "quantize.cu", "matmul_i8.cu", "matmul_i8_tc.cu", "sample.cu"]
+           "ops.cu", "quantize.cu", "matmul_i8.cu", "matmul_i8_tc.cu", "matmul_i8_few.cu",
+           "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -230,6 +230,10 @@ rbf_status matmul_i8_dev(rbf_ops* o, const int8_t* d_a, int64_t ld_a, const floa
   if (!matrix_ok(d_a, 1, m, k, ld_a)) return RBF_ERR_INVALID_VALUE;
   if (out_dtype == RBF_DTYPE_I32 && (d_a_scale || d_b_scale || d_bias)) return RBF_ERR_INVALID_VALUE;
   if (m == 0 || n == 0) return RBF_OK;
+  if (matmul_i8_few_fits(a)) {
+    OPS_LAUNCH(o, launch_matmul_i8_few(a, d_a, ld_a, kI8, o->num_sms, o->stream));
+    return RBF_OK;
+  }
   if (!matmul_i8_tc_fits(a)) {
     OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
     return RBF_OK;
@@ -262,6 +266,10 @@ rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t
   if (rbf_status st = check_matmul(o, a)) return st;
   if (!matrix_ok(d_x, dtype_bytes(x_dtype), m, k, ld_x)) return RBF_ERR_INVALID_VALUE;
   if (m == 0 || n == 0) return RBF_OK;
+  if (matmul_i8_few_fits(a)) {
+    OPS_LAUNCH(o, launch_matmul_i8_few(a, d_x, ld_x, x_dtype, o->num_sms, o->stream));
+    return RBF_OK;
+  }
   QuantizeLaunch q;
   q.x = d_x;
   q.dtype = x_dtype;

@@ -12,6 +12,7 @@ constexpr int kF32 = 0;
 constexpr int kBF16 = 1;
 constexpr int kF16 = 2;
 constexpr int kI32 = 3;
+constexpr int kI8 = 4;  // internal: the tokens of matmul_i8_dev
 
 inline int dtype_bytes(int dtype) { return dtype == kF32 || dtype == kI32 ? 4 : 2; }
 
@@ -50,6 +51,14 @@ struct MatmulI8Launch {
 };
 // Any strides and alignments.
 cudaError_t launch_matmul_i8_any(const MatmulI8Launch& a, cudaStream_t stream);
+
+// Up to four tokens, in one launch: 8-bit ones (dtype kI8), or floating-point
+// ones that it quantises. a.a and a.ld_a are not used, nor a.a_scale with the
+// latter.
+constexpr int kFewMaxTokenBytes = 96 * 1024;  // of the 8-bit tokens in shared memory
+bool matmul_i8_few_fits(const MatmulI8Launch& a);
+cudaError_t launch_matmul_i8_few(const MatmulI8Launch& a, const void* tokens, int64_t ld, int dtype, int num_sms,
+                                 cudaStream_t stream);
 
 // The tensor-core product. Its first operand is the workspace's fp16 rows
 // (launch_expand_rows or launch_quantize_rows writes them, enqueued just

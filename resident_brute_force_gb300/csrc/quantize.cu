@@ -1,60 +1,16 @@
 // quantize.cu -- rows of floating-point numbers to 8-bit integers with one
 // scale a row (include/rbf_ops.h, quantize_rows_i8_dev).
-//
-// With t = max_j |x_j|: scale = t * (1 / 127), q_j = x_j * ((1 / t) * 127)
-// rounded to nearest even, all in fp32 (one division a row, one product a
-// value, each rounded as IEEE says, so that the integers are the same wherever
-// they are computed). |q| <= 127: x_j times the factor is at most
-// 127 (1 + 2^-22), which rounds to 127.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+// The arithmetic is quantize.cuh's.
 #include <algorithm>
 
 #include "ops_internal.h"
+#include "quantize.cuh"
 #include "rbf_device.cuh"
 
 namespace rbf {
 namespace {
 
 constexpr int kQuantThreads = 256;
-
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-
-// What a row's values are multiplied by: first by `pre` (a power of two: 1,
-// or 2^100 for a row so small that 1 / t could overflow), then by `inv`.
-struct RowScale {
-  float scale, pre, inv;
-};
-
-// `code`: the largest |x| of the row as its fp32 pattern, which orders
-// magnitudes as unsigned integers with the infinities and the NaNs on top.
-__device__ __forceinline__ RowScale row_scale(uint32_t code) {
-  RowScale r;
-  if (code >= 0x7F800000u) {  // a NaN or an infinity: zeros, and a scale that makes every product NaN
-    r.scale = __uint_as_float(0x7FC00000u);
-    r.pre = 0.0f;
-    r.inv = 0.0f;
-    return r;
-  }
-  const float t = __uint_as_float(code);
-  r.scale = __fmul_rn(t, 1.0f / 127.0f);
-  r.pre = t < 0x1p-100f ? 0x1p100f : 1.0f;
-  r.inv = t > 0.0f ? __fmul_rn(__fdiv_rn(1.0f, __fmul_rn(t, r.pre)), 127.0f) : 0.0f;
-  return r;
-}
-
-__device__ __forceinline__ int quantize_one(float x, const RowScale& r) {
-  if (r.inv == 0.0f) return 0;  // also keeps 0 * infinity out
-  return __float2int_rn(__fmul_rn(__fmul_rn(x, r.pre), r.inv));
-}
 
 __device__ __forceinline__ uint32_t block_max(uint32_t v) {
   __shared__ uint32_t part[kQuantThreads / 32];
@@ -95,33 +51,14 @@ __global__ void __launch_bounds__(kQuantThreads)
     const RowScale s = row_scale(block_max(top));
     if (o.f16) {
       for (int j = threadIdx.x; j < o.pitch; j += kQuantThreads)
-        o.f16[r * o.pitch + j] = __float2half_rn(j < cols ? static_cast<float>(quantize_one(to_f32(row[j]), s)) : 0.0f);
+        o.f16[r * o.pitch + j] = __float2half_rn(j < cols ? quantize_sum(to_f32(row[j]), s) - kRounder : 0.0f);
       if (threadIdx.x == 0) atomicMax(o.block_l1, 128u * 127u);  // the bound of any row: not worth a reduction here
     } else {
       for (int j = threadIdx.x; j < cols; j += kQuantThreads)
-        o.q[r * o.ld_q + j] = static_cast<int8_t>(quantize_one(to_f32(row[j]), s));
+        o.q[r * o.ld_q + j] = static_cast<int8_t>(__float_as_uint(quantize_sum(to_f32(row[j]), s)));
     }
     if (threadIdx.x == 0) o.scale[r] = s.scale;
     __syncthreads();  // block_max's shared words are used again
-  }
-}
-
-// Eight values on a 16-byte boundary, zero from `live` on.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int live, float (&x)[8]) {
-  if (live >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < live ? to_f32(p[i]) : 0.0f;
   }
 }
 
@@ -159,33 +96,25 @@ __global__ void __launch_bounds__(kQuantThreads)
   for (int g = 0; g < kHeld; ++g) {
     const int c = (g * THREADS + t) * 8;
     if (c >= end) break;  // whole groups of 16 threads: the pitch is a multiple of 128
-    // Rounded to whole numbers by adding and subtracting 1.5 * 2^23.
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      q[i] = c < cols && s.inv != 0.0f ? __fadd_rn(__fmul_rn(__fmul_rn(v[g][i], s.pre), s.inv), 12582912.0f) : 12582912.0f;
+    for (int i = 0; i < 8; ++i) q[i] = c < cols ? quantize_sum(v[g][i], s) : kRounder;
     if constexpr (F16) {
       __half2 h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        h[i] = __floats2half2_rn(__fsub_rn(q[2 * i], 12582912.0f), __fsub_rn(q[2 * i + 1], 12582912.0f));
+        h[i] = __floats2half2_rn(__fsub_rn(q[2 * i], kRounder), __fsub_rn(q[2 * i + 1], kRounder));
       *reinterpret_cast<uint4*>(o.f16 + r * o.pitch + c) = *reinterpret_cast<const uint4*>(h);
       // 16 threads hold the 128 values of a stage.
       float l1 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) l1 += fabsf(q[i] - 12582912.0f);
+      for (int i = 0; i < 8; ++i) l1 += fabsf(q[i] - kRounder);
       const unsigned half = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) l1 += __shfl_xor_sync(half, l1, d);
       l1_top = fmaxf(l1_top, l1);
     } else {
-      uint32_t w[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {  // the low byte of each sum is the number
-        const uint32_t lo = __byte_perm(__float_as_uint(q[4 * i]), __float_as_uint(q[4 * i + 1]), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(q[4 * i + 2]), __float_as_uint(q[4 * i + 3]), 0x0040);
-        w[i] = __byte_perm(lo, hi, 0x5410);
-      }
+      const uint32_t w[2] = {pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7])};
       int8_t* dst = o.q + r * o.ld_q + c;
       if (c + 8 <= cols) {
         *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);

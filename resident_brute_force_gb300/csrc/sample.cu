@@ -737,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
   // The row's end in CTA 0: its n <= kSmall candidates are all that may be
   // kept. Every thread takes one and looks at all of them. sum_all: what top_p
   // is a share of (0: the sum of the q.k best of the candidates).
-  auto finish_small = [&](int n, u64 sum_all) {
+  auto finish_small = [&](int candidates, u64 sum_all) {
+    const int n = min(candidates, kSmall);
     const int t = threadIdx.x;
     const u64 key = t < n ? list[t] : 0ull;
     const float e = t < n ? ex2(sc.z(key_score(key))) : 0.0f;

@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _binding
-from ._binding import RBF_OK, RbfError, _dev_ptr, _need, load_library
+from ._binding import RBF_OK, RbfError, _dev_ptr, load_library
 
 RBF_DTYPE_F32 = 0
 RBF_DTYPE_BF16 = 1
@@ -39,43 +39,60 @@ _STREAM_LEGACY = 1  # cudaStreamLegacy: the default stream, named explicitly
 _DTYPES: dict = {}
 
 
-def _dtype(t, what: str, integers: bool = False) -> int:
+def _dtypes() -> dict:
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.float32: RBF_DTYPE_F32, torch.bfloat16: RBF_DTYPE_BF16, torch.float16: RBF_DTYPE_F16,
-                        torch.int32: RBF_DTYPE_I32})
-    code = _DTYPES.get(t.dtype)
-    if code is None or (code == RBF_DTYPE_I32 and not integers):
-        raise TypeError(f"{what} is {t.dtype}: expected float32, bfloat16 or float16"
-                        + (" or int32" if integers else ""))
-    return code
+                        torch.int32: RBF_DTYPE_I32, torch.int8: -1})
+    return _DTYPES
 
 
-def _matrix(t, what: str) -> tuple[int, int]:
-    """Device pointer and row stride of a 2-D CUDA tensor with contiguous rows."""
-    _need(t.dim() == 2, f"{what} is a 2-D tensor")
-    if not t.is_cuda:
-        raise TypeError(f"{what}: expected a CUDA tensor")
-    rows, cols = t.shape
-    _need(cols <= 1 or t.stride(1) == 1, f"{what}: the values of a row must be contiguous")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    _need(ld >= cols, f"{what}: rows overlap")
-    return t.data_ptr(), ld
+# The checks below run before every launch: messages are put together only when one fails.
+
+def _float_matrix(t, what: str, integers: bool = False):
+    """Device pointer, row stride, rows, columns and dtype code of a 2-D CUDA tensor with contiguous rows."""
+    code = _dtypes().get(t.dtype)
+    if code is None or code < 0 or (code == RBF_DTYPE_I32 and not integers):
+        raise TypeError(f"{what} is {t.dtype}: expected float32, bfloat16 or float16" + (" or int32" if integers else ""))
+    return *_matrix(t, what), code
 
 
-def _i8(t, what: str):
-    import torch
-    if t.dtype != torch.int8:
+def _i8_matrix(t, what: str):
+    if _dtypes().get(t.dtype) != -1:
         raise TypeError(f"{what} is {t.dtype}: expected int8")
     return _matrix(t, what)
 
 
+def _matrix(t, what: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} is a 2-D tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    rows, cols = shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{what}: the values of a row must be contiguous")
+    if rows <= 1:
+        ld = max(ld, cols, 1)  # one row: any stride
+    elif ld < cols:
+        raise ValueError(f"{what}: rows overlap")
+    return t.data_ptr(), ld, rows, cols
+
+
 def _vector(t, count: int, what: str, dtype: str = "float32", optional: bool = True):
     if t is None:
-        _need(optional, f"{what} is required")
+        if not optional:
+            raise ValueError(f"{what} is required")
         return None
-    _need(t.numel() == count, f"{what} has {t.numel()} entries, expected {count}")
+    if t.numel() != count:
+        raise ValueError(f"{what} has {t.numel()} entries, expected {count}")
     return _dev_ptr(t, dtype)
+
+
+def _same(got, want, what: str) -> None:
+    if got != want:
+        raise ValueError(f"{what} is {got}, expected {want}")
 
 
 class Ops:
@@ -141,48 +158,43 @@ class Ops:
     # -- operators
     def quantize_rows_i8_dev(self, d_x, d_q, d_scale) -> None:
         """Rows of d_x [rows, cols] (float32, bfloat16 or float16) to int8 d_q with one scale a row in d_scale."""
-        x, ld_x = _matrix(d_x, "d_x")
-        q, ld_q = _i8(d_q, "d_q")
-        rows, cols = d_x.shape
-        _need(tuple(d_q.shape) == (rows, cols), f"d_q is {tuple(d_q.shape)}, d_x is {(rows, cols)}")
-        self._check(self.lib.quantize_rows_i8_dev(self._h, x, _dtype(d_x, "d_x"), ld_x, rows, cols, q, ld_q,
+        x, ld_x, rows, cols, dtype = _float_matrix(d_x, "d_x")
+        q, ld_q, q_rows, q_cols = _i8_matrix(d_q, "d_q")
+        _same((q_rows, q_cols), (rows, cols), "the shape of d_q")
+        self._check(self.lib.quantize_rows_i8_dev(self._h, x, dtype, ld_x, rows, cols, q, ld_q,
                                                   _vector(d_scale, rows, "d_scale", optional=False)),
                     "quantize_rows_i8_dev")
 
     def matmul_i8_dev(self, d_a, d_a_scale, d_b, d_b_scale, d_out, bias=None) -> None:
         """d_out [m, n] = d_a [m, k] times d_b [n, k] transposed, both int8, each row of either with its scale (None:
         1), plus bias [n]. An int32 d_out takes the sums themselves, without scales or bias."""
-        a, ld_a = _i8(d_a, "d_a")
-        b, ld_b = _i8(d_b, "d_b")
-        out, ld_out = _matrix(d_out, "d_out")
-        (m, k), n = d_a.shape, d_b.shape[0]
-        _need(d_b.shape[1] == k, f"d_a has {k} columns, d_b {d_b.shape[1]}")
-        _need(tuple(d_out.shape) == (m, n), f"d_out is {tuple(d_out.shape)}, expected {(m, n)}")
+        a, ld_a, m, k = _i8_matrix(d_a, "d_a")
+        b, ld_b, n, b_cols = _i8_matrix(d_b, "d_b")
+        out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", integers=True)
+        _same(b_cols, k, "the depth of d_b")
+        _same((out_rows, out_cols), (m, n), "the shape of d_out")
         self._check(self.lib.matmul_i8_dev(self._h, a, ld_a, _vector(d_a_scale, m, "d_a_scale"), b, ld_b,
-                                           _vector(d_b_scale, n, "d_b_scale"), _vector(bias, n, "bias"), out,
-                                           _dtype(d_out, "d_out", integers=True), ld_out, m, n, k), "matmul_i8_dev")
+                                           _vector(d_b_scale, n, "d_b_scale"), _vector(bias, n, "bias"), out, dtype,
+                                           ld_out, m, n, k), "matmul_i8_dev")
 
     def linear_i8_dev(self, d_x, d_w, d_w_scale, d_out, bias=None) -> None:
         """d_out [m, n] = d_x [m, k] (quantised by rows) times the int8 weights d_w [n, k] transposed, times the
         weights' row scales d_w_scale (None: 1), plus bias [n]."""
-        x, ld_x = _matrix(d_x, "d_x")
-        w, ld_w = _i8(d_w, "d_w")
-        out, ld_out = _matrix(d_out, "d_out")
-        (m, k), n = d_x.shape, d_w.shape[0]
-        _need(d_w.shape[1] == k, f"d_x has {k} columns, d_w {d_w.shape[1]}")
-        _need(tuple(d_out.shape) == (m, n), f"d_out is {tuple(d_out.shape)}, expected {(m, n)}")
-        self._check(self.lib.linear_i8_dev(self._h, x, _dtype(d_x, "d_x"), ld_x, w, ld_w,
-                                           _vector(d_w_scale, n, "d_w_scale"), _vector(bias, n, "bias"), out,
-                                           _dtype(d_out, "d_out"), ld_out, m, n, k), "linear_i8_dev")
+        x, ld_x, m, k, x_dtype = _float_matrix(d_x, "d_x")
+        w, ld_w, n, w_cols = _i8_matrix(d_w, "d_w")
+        out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out")
+        _same(w_cols, k, "the depth of d_w")
+        _same((out_rows, out_cols), (m, n), "the shape of d_out")
+        self._check(self.lib.linear_i8_dev(self._h, x, x_dtype, ld_x, w, ld_w, _vector(d_w_scale, n, "d_w_scale"),
+                                           _vector(bias, n, "bias"), out, dtype, ld_out, m, n, k), "linear_i8_dev")
 
     def sample_dev(self, d_logits, d_u, d_token, d_logprob=None, temperature=None, top_k=None, top_p=None,
                    min_p=None) -> None:
         """One index a row of d_logits [rows, vocab] into d_token (int32; -1 where every score is -infinity), and the
         log of its share into d_logprob. d_u: one random number in [0, 1) a row; temperature, top_p and min_p (float32)
         and top_k (int32): one entry a row, or None."""
-        x, ld = _matrix(d_logits, "d_logits")
-        rows, vocab = d_logits.shape
-        self._check(self.lib.sample_dev(self._h, x, _dtype(d_logits, "d_logits"), ld, rows, vocab,
+        x, ld, rows, vocab, dtype = _float_matrix(d_logits, "d_logits")
+        self._check(self.lib.sample_dev(self._h, x, dtype, ld, rows, vocab,
                                         _vector(d_u, rows, "d_u", optional=False),
                                         _vector(temperature, rows, "temperature"),
                                         _vector(top_k, rows, "top_k", "int32"), _vector(top_p, rows, "top_p"),
