@@ -78,6 +78,7 @@ struct Vec<float> {
     x[2] = __uint_as_float(v.z);
     x[3] = __uint_as_float(v.w);
   }
+  static __device__ __forceinline__ float one(float e) { return e; }
   // Elementwise maximum; a NaN loses to any number.
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
@@ -96,6 +97,7 @@ struct Vec<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
+  static __device__ __forceinline__ float one(__nv_bfloat16 e) { return __bfloat162float(e); }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
@@ -115,6 +117,7 @@ struct Vec<__half> {
       x[2 * i + 1] = f.y;
     }
   }
+  static __device__ __forceinline__ float one(__half e) { return __half2float(e); }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
@@ -210,11 +213,6 @@ __device__ __forceinline__ u64 mul2(u64 a, u64 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float ex2(float z) {  // exp2f where the result is not subnormal, 0 there
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
@@ -242,24 +240,25 @@ __device__ __forceinline__ u64 fixed(float e) { return static_cast<u64>(__float2
 __device__ __forceinline__ u64 weight(float x, const Scale& s) { return fixed(ex2(s.z(x))); }
 
 // A sum of weights. e is divided into a multiple of 2^-18 and a rest that is
-// rounded to a multiple of 2^-36 (adding and subtracting 1.5 * 2^23 units
-// rounds to units, halves to even); both parts are summed in fp32, exactly, for
-// up to 64 weights a lane of the pair, then moved into the integer.
+// rounded to a multiple of 2^-36: adding 1.5 * 2^23 units rounds to units
+// (halves to even) and leaves their number, plus that of the constant, in the
+// low bits of the fp32 pattern. The patterns are summed as integers, modulo
+// 2^32, and the constants' share is taken out at the end: exact for up to 2^13
+// weights a thread, then moved into 64 bits.
 struct Mass {
-  u64 hi, lo, total;
-  __device__ __forceinline__ Mass() : hi(0), lo(0), total(0) {}
-  __device__ __forceinline__ void add(u64 e2) {
-    const u64 c1 = pack2(0x1.8p5f, 0x1.8p5f), n1 = pack2(-0x1.8p5f, -0x1.8p5f);
-    const u64 c2 = pack2(0x1.8p-13f, 0x1.8p-13f), n2 = pack2(-0x1.8p-13f, -0x1.8p-13f);
-    const u64 minus = pack2(-1.0f, -1.0f);
-    const u64 h = add2(add2(e2, c1), n1);
-    const u64 l = add2(add2(fma2(h, minus, e2), c2), n2);
-    hi = add2(hi, h);
-    lo = add2(lo, l);
+  unsigned hi = 0, lo = 0;
+  u64 total = 0;
+  static constexpr float kHi = 0x1.8p5f, kLo = 0x1.8p-13f;
+  __device__ __forceinline__ void add(float a, float b) {
+    const float ta = __fadd_rn(a, kHi), tb = __fadd_rn(b, kHi);
+    hi += __float_as_uint(ta) + __float_as_uint(tb);
+    const float la = __fadd_rn(a, __fsub_rn(kHi, ta)), lb = __fadd_rn(b, __fsub_rn(kHi, tb));
+    lo += __float_as_uint(__fadd_rn(la, kLo)) + __float_as_uint(__fadd_rn(lb, kLo));
   }
-  __device__ __forceinline__ void flush() {
-    total += static_cast<u64>(__float2int_rn(low2(hi) * 0x1p18f) + __float2int_rn(high2(hi) * 0x1p18f)) << 18;
-    total += static_cast<u64>(static_cast<long long>(__float2int_rn(low2(lo) * 0x1p36f) + __float2int_rn(high2(lo) * 0x1p36f)));
+  // `n`: weights added since the last flush.
+  __device__ __forceinline__ void flush(unsigned n) {
+    total += static_cast<u64>(hi - n * 0x42400000u) << 18;
+    total += static_cast<u64>(static_cast<long long>(static_cast<int>(lo - n * 0x39400000u)));
     hi = 0;
     lo = 0;
   }
@@ -267,20 +266,24 @@ struct Mass {
 
 // ------------------------------------------------------ warps and clusters
 
+// Sum over the warp, in three parts of 26 bits: 32 of each stay under 2^31.
 __device__ __forceinline__ u64 warp_sum(u64 v) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(kFullMask, v, m);
-  return v;
+  constexpr u64 kPart = (u64(1) << 26) - 1;
+  const u64 a = __reduce_add_sync(kFullMask, static_cast<unsigned>(v & kPart));
+  const u64 b = __reduce_add_sync(kFullMask, static_cast<unsigned>(v >> 26 & kPart));
+  const u64 c = __reduce_add_sync(kFullMask, static_cast<unsigned>(v >> 52));
+  return a + (b << 26) + (c << 52);
 }
 __device__ __forceinline__ u64 warp_max(u64 v) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v = umax64(v, __shfl_xor_sync(kFullMask, v, m));
-  return v;
+  const unsigned hi = __reduce_max_sync(kFullMask, static_cast<unsigned>(v >> 32));
+  const unsigned lo = __reduce_max_sync(kFullMask, static_cast<unsigned>(v >> 32) == hi ? static_cast<unsigned>(v) : 0u);
+  return static_cast<u64>(hi) << 32 | lo;
 }
-__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
+template <typename V>
+__device__ __forceinline__ V warp_scan(V v, int lane) {  // inclusive
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const u64 o = __shfl_up_sync(kFullMask, v, d);
+    const V o = __shfl_up_sync(kFullMask, v, d);
     if (lane >= d) v += o;
   }
   return v;
@@ -337,16 +340,14 @@ struct Cta {
     __syncthreads();  // the words of the last reduction have been read
     if (lane == 0) s.part[warp] = v;
     __syncthreads();
-    u64 r = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) r = MAX ? umax64(r, s.part[w]) : r + s.part[w];
+    u64 r = lane < kWarps ? s.part[lane] : 0ull;
+    r = MAX ? warp_max(r) : warp_sum(r);
     if (size == 1) return r;
     if (threadIdx.x < size) remote_store(remote(&s.slot[turn][rank], threadIdx.x), r);
     sync();
-    r = 0;
-    for (uint32_t c = 0; c < size; ++c) r = MAX ? umax64(r, s.slot[turn][c]) : r + s.slot[turn][c];
+    r = lane < static_cast<int>(size) ? s.slot[turn][lane] : 0ull;
     turn ^= 1;
-    return r;
+    return MAX ? warp_max(r) : warp_sum(r);
   }
 };
 
@@ -365,10 +366,7 @@ struct Bracket {
 
   // A bin is the rounding of -128 z to a whole number, which adding 2^23 leaves in the low bits of the fp32 pattern.
   static constexpr uint32_t kPattern = 0x4B000000u;
-  static __device__ __forceinline__ u64 pattern2(u64 z2) {
-    constexpr float k = -static_cast<float>(kBinsPerOctave);
-    return fma2(z2, pack2(k, k), pack2(8388608.0f, 8388608.0f));
-  }
+  static __device__ __forceinline__ float pattern(float z) { return __fmaf_rn(z, -static_cast<float>(kBinsPerOctave), 8388608.0f); }
   // The bin of a pattern; kBins or more for z under -37 (infinities have larger patterns).
   static __device__ __forceinline__ uint32_t bin(float y) { return __float_as_uint(y) - kPattern; }
   // The position of a score (its order never decreases as z falls): below 0
@@ -387,21 +385,16 @@ struct Bracket {
   }
   __device__ __forceinline__ float step() const { return fine ? -1.0f / scale : -1.0f / kBinsPerOctave; }
 };
-// Bounds on the sum of `count` weights in a bin whose edges have the weights
-// `low` and `high`: 2^-14 covers the rounding of z and of the edges, one unit
-// the weight's own.
-__device__ __forceinline__ u64 lower_sum(float low, unsigned count) {
-  const u64 w = static_cast<u64>(low * (kOne * (1.0f - 0x1p-14f)));
-  return w > 0 ? (w - 1) * count : 0;
-}
-__device__ __forceinline__ u64 upper_sum(float high, unsigned count) {
-  return (static_cast<u64>(high * (kOne * (1.0f + 0x1p-14f))) + 2) * count;
-}
+// Sums of counts times the weights at the bins' edges bound the sums of weights;
+// they are made in fp32, in units of the largest weight: 2^-9 covers the
+// rounding of z, of the edges and of a few thousand additions, 2^-36 a score
+// the weights' own.
+constexpr float kBelow = 1.0f - 0x1p-9f, kAbove = 1.0f + 0x1p-9f;
 
 template <typename T, bool HELD>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch a) {
   constexpr int E = Vec<T>::kLen;
-  constexpr int kFlush = 64 / (E / 2);  // vectors that Mass sums before a flush
+  constexpr int kFlush = 8192 / E;  // vectors that Mass sums before a flush
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared s;
   unsigned* hist = reinterpret_cast<unsigned*>(dyn);  // kBins counts, or
@@ -489,19 +482,22 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     return;
   }
 
-  // f(scores, z pairs, vector) for this warp's vectors, four loads under way
-  // a lane; after at most kFlush vectors, g().
+  // f(scores, their z, vector) for this warp's vectors, some loads under way a
+  // lane; after at most kFlush vectors g(number of scores since the last one).
   auto each = [&](auto&& f, auto&& g) {
     auto one = [&](const uint4& raw, int v) {
-      float x[E];
-      u64 z[E / 2];
+      float x[E], z[E];
       Vec<T>::unpack(raw, x);
       if (sc.inf) {
 #pragma unroll
         for (int i = 0; i < E; ++i) x[i] = Scale::shift(x[i]);
       }
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) z[i] = sc.z2(x[2 * i], x[2 * i + 1]);
+      for (int i = 0; i < E; i += 2) {
+        const u64 z2 = sc.z2(x[i], x[i + 1]);
+        z[i] = low2(z2);
+        z[i + 1] = high2(z2);
+      }
       f(x, z, v);
     };
     constexpr int kBatch = HELD ? 2 : 4;
@@ -513,28 +509,36 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) one(raw[i], v + 32 * i);
       if ((since += kBatch) == kFlush) {
-        g();
+        g(static_cast<unsigned>(since * E));
         since = 0;
       }
     }
-    g();
-    for (; v < v1; v += 32) one(get(v), v);
-    g();
+    g(static_cast<unsigned>(since * E));
+    since = 0;
+    for (; v < v1; v += 32, ++since) one(get(v), v);
+    g(static_cast<unsigned>(since * E));
   };
   // The key of a score that `each` hands out.
   auto key_of = [&](float x, int v, int i) {
     return make_key(sc.inf && x == 0.0f ? INFINITY : x, static_cast<uint32_t>(index_of(v, i)));
   };
+  // One score, read again.
+  auto score_at = [&](int v, int i) -> float {
+    T e;
+    if constexpr (HELD)
+      e = reinterpret_cast<const T*>(held + (v - c0))[i];
+    else
+      e = row.p[index_of(v, i)];
+    return Vec<T>::one(e);
+  };
   // Put the scores of a vector that `mask` names into this CTA's list.
-  auto append = [&](unsigned mask, const float (&x)[E], int v) {
+  auto append = [&](unsigned mask, int v) {
     if (mask == 0) return;
     unsigned at = atomicAdd(&s.list_len, static_cast<unsigned>(__popc(mask)));
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (mask >> i & 1u) {
-        if (at < kListCap) list[at] = key_of(x[i], v, i);
-        ++at;
-      }
+    for (; mask != 0; mask &= mask - 1, ++at) {
+      const int i = __ffs(static_cast<int>(mask)) - 1;
+      if (at < kListCap) list[at] = make_key(score_at(v, i), static_cast<uint32_t>(index_of(v, i)));
+    }
   };
   // Clear the bits of the scores whose keys are under `cut`.
   auto only_kept = [&](unsigned mask, const float (&x)[E], int v, u64 cut) {
@@ -550,10 +554,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     v = warp_sum(v);
     if (lane == 0) s.scan[t][cta.warp] = v;
     __syncthreads();
-    u64 r = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) r += s.scan[t][w];
-    return r;
+    return warp_sum(lane < kWarps ? s.scan[t][lane] : 0ull);
   };
   // CTA 0's words [i0, i1) to the others.
   auto tell = [&](int i0, int i1) {
@@ -577,12 +578,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
   // scores (for_k) or weight: say[0], say[1] the first and last position, say[2]
   // scores ahead of the first, say[3] scores down to the last one, say[4] all.
   // Each CTA adds up the cluster's counts for an equal part of the positions.
+  // Where all positions' weights have been summed (`sum`, else 0), the bounds
+  // are taken from the other end too: those of a prefix are the sum less those
+  // of the rest, and near top_p = 1 that rest is small, and so is its error.
   auto clear_counts = [&]() {
     for (int i = threadIdx.x; i < kQuads; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x == 0) s.list_len = 0;
     cta.sync();
   };
-  auto decide = [&](const Bracket& br, bool for_k, u64 target, u64 above, u64 count_above) {
+  auto decide = [&](const Bracket& br, bool for_k, u64 target, u64 above, u64 count_above, u64 sum) {
     cta.sync();  // all counts are there
     const int per = (kQuads + static_cast<int>(cta.size) * kThreads - 1) / (static_cast<int>(cta.size) * kThreads);  // a thread's
     const int q0 = (static_cast<int>(cta.rank) * kThreads + static_cast<int>(threadIdx.x)) * per;
@@ -611,95 +615,93 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
       }
       return c;
     };
-    u64 n = 0, lower = 0, upper = 0;
-    const float step = br.step(), ratio = exp2f(step);
-    float low = exp2f(br.edge(b0)), high = exp2f(br.edge(b0) - step);
+    unsigned n = 0;
+    float lower = 0.0f, upper = 0.0f;
+    const float step = br.step(), ratio = exp2f(step), low0 = exp2f(br.edge(b0)), high0 = exp2f(br.edge(b0) - step);
+    float low = low0, high = high0;
+    uint4 c4 = make_uint4(0u, 0u, 0u, 0u);
     for (int quad = q0; quad < q1; ++quad) {
-      const uint4 c4 = count(quad);
+      c4 = count(quad);
       const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         n += c[i];
-        if (!for_k) {
-          if (c[i]) {
-            lower += lower_sum(low, c[i]);
-            upper += upper_sum(high, c[i]);
-          }
-          high = low;
-          low *= ratio;
-        }
+        const float f = static_cast<float>(c[i]);
+        lower += f * fmaxf(low - 0x1p-36f, 0.0f);
+        upper += f * (high + 0x1p-36f);
+        high = low;
+        low *= ratio;
       }
     }
-    const u64 sn = warp_scan(n, lane), sl = warp_scan(lower, lane), su = warp_scan(upper, lane);
+    // As whole numbers from here on, so that one thread's end is the next one's start.
+    const u64 wl = static_cast<u64>(lower * (kOne * kBelow)), wu = static_cast<u64>(upper * (kOne * kAbove)) + (n > 0);
+    const unsigned sn = warp_scan(n, lane);
+    const u64 sl = warp_scan(wl, lane), su = warp_scan(wu, lane);
     if (lane == 31) {
       s.scan[0][cta.warp] = sn;
       s.scan[1][cta.warp] = sl;
       s.scan[2][cta.warp] = su;
     }
-    if (threadIdx.x == 0) s.say[0] = s.say[1] = kBins - 1;
-    __syncthreads();
-    u64 fn = sn - n, fl = sl - lower, fu = su - upper, all_n = 0, all_l = 0, all_u = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < cta.warp) {
-        fn += s.scan[0][w];
-        fl += s.scan[1][w];
-        fu += s.scan[2][w];
-      }
-      all_n += s.scan[0][w];
-      all_l += s.scan[1][w];
-      all_u += s.scan[2][w];
-    }
-    // The CTAs' totals, and with them the values ahead of this one's part.
-    if (threadIdx.x < cta.size) {
-      remote_store(remote(&s.words[0][cta.rank], threadIdx.x), all_n);
-      remote_store(remote(&s.words[1][cta.rank], threadIdx.x), all_l);
-      remote_store(remote(&s.words[2][cta.rank], threadIdx.x), all_u);
-    }
-    cta.sync();
-    fn += count_above;
-    fl += above;
-    fu += above;
-    u64 all = count_above;
-    for (uint32_t o = 0; o < cta.size; ++o) {
-      if (o < cta.rank) {
-        fn += s.words[0][o];
-        fl += s.words[1][o];
-        fu += s.words[2][o];
-      }
-      all += s.words[0][o];
-    }
     if (threadIdx.x == 0) {
-      s.say[2] = s.say[3] = all;
-      s.say[4] = all;
+      s.say[0] = s.say[1] = kBins - 1;
+      s.say[2] = s.say[3] = ~0ull;  // not told
     }
     __syncthreads();
+    // The warps' and the CTAs' totals, and with them the values ahead of this thread's bins.
+    const bool warp_there = lane < kWarps, warp_ahead = lane < cta.warp;
+    const u64 on = warp_there ? s.scan[0][lane] : 0ull, ol = warp_there ? s.scan[1][lane] : 0ull, ou = warp_there ? s.scan[2][lane] : 0ull;
+    u64 fn = count_above + warp_sum(warp_ahead ? on : 0ull) + sn - n;
+    u64 fl = above + warp_sum(warp_ahead ? ol : 0ull) + sl - wl, fu = above + warp_sum(warp_ahead ? ou : 0ull) + su - wu;
+    u64 all = warp_sum(on), all_l = warp_sum(ol), all_u = warp_sum(ou);
+    if (cta.size > 1) {
+      if (threadIdx.x < cta.size) {
+        remote_store(remote(&s.words[0][cta.rank], threadIdx.x), all);
+        remote_store(remote(&s.words[1][cta.rank], threadIdx.x), all_l);
+        remote_store(remote(&s.words[2][cta.rank], threadIdx.x), all_u);
+      }
+      cta.sync();
+      const bool there = lane < static_cast<int>(cta.size), ahead = lane < static_cast<int>(cta.rank);
+      const u64 cn = there ? s.words[0][lane] : 0ull;
+      all = warp_sum(cn);
+      fn += warp_sum(ahead ? cn : 0ull);
+      const u64 cl = there ? s.words[1][lane] : 0ull, cu = there ? s.words[2][lane] : 0ull;
+      all_l = warp_sum(cl);
+      all_u = warp_sum(cu);
+      fl += warp_sum(ahead ? cl : 0ull);
+      fu += warp_sum(ahead ? cu : 0ull);
+    }
+    // Bounds on the weight down to a point that has the running sums l and u.
+    auto at_least = [&](u64 l, u64 u) { return sum ? max(static_cast<long long>(l), static_cast<long long>(sum - all_u + u)) : static_cast<long long>(l); };
+    auto at_most = [&](u64 l, u64 u) { return sum ? min(static_cast<long long>(u), static_cast<long long>(sum - all_l + l)) : static_cast<long long>(u); };
+    const long long goal = static_cast<long long>(target);
+    if (threadIdx.x == 0) s.say[4] = count_above + all;
     // The thread in whose bins a running value reaches the target tells all.
     auto say = [&](int word, u64 v) {
       for (uint32_t o = 0; o < cta.size; ++o) remote_store(remote(&s.say[word], o), v);
     };
-    cta.sync();  // the words of say that are told have their defaults everywhere
-    if (for_k ? fn < target && fn + n >= target : (fl < target && fl + lower >= target) || (fu < target && fu + upper >= target)) {
-      low = exp2f(br.edge(b0));
-      high = exp2f(br.edge(b0) - step);
+    const u64 nl = fl + wl, nu = fu + wu;
+    const long long start_l = at_least(fl, fu), start_u = at_most(fl, fu);
+    if (n > 0 && (for_k ? fn < target && fn + n >= target
+                        : (start_l < goal && at_least(nl, nu) >= goal) || (start_u < goal && at_most(nl, nu) >= goal))) {
+      low = low0;
+      high = high0;
+      float rl = 0.0f, ru = 0.0f;
+      long long at_l = start_l, at_u = start_u;
       for (int quad = q0; quad < q1; ++quad) {
-        const uint4 c4 = count(quad);
+        if (q1 - q0 > 1) c4 = count(quad);
         const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const u64 b = static_cast<u64>(4 * quad + i);
-          bool first = false, last = false;
-          if (for_k) {
-            first = last = fn < target && fn + c[i] >= target;
-          } else {
-            const u64 l = c[i] ? lower_sum(low, c[i]) : 0, u = c[i] ? upper_sum(high, c[i]) : 0;
-            first = fu < target && fu + u >= target;
-            last = fl < target && fl + l >= target;
-            fl += l;
-            fu += u;
-            high = low;
-            low *= ratio;
-          }
+          const bool end = quad == q1 - 1 && i == 3;
+          const float f = static_cast<float>(c[i]);
+          rl += f * fmaxf(low - 0x1p-36f, 0.0f);
+          ru += f * (high + 0x1p-36f);
+          const u64 run_l = end ? nl : fl + static_cast<u64>(rl * (kOne * kBelow)), run_u = end ? nu : fu + static_cast<u64>(ru * (kOne * kAbove)) + 1;
+          const long long to_l = at_least(run_l, run_u), to_u = at_most(run_l, run_u);
+          const u64 counted = fn;
+          const bool first = for_k ? counted < target && counted + c[i] >= target : at_u < goal && to_u >= goal;
+          const bool last = for_k ? first : at_l < goal && to_l >= goal;
           if (first) {
             say(0, b);
             say(2, fn);
@@ -709,6 +711,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
             say(1, b);
             say(3, fn);
           }
+          at_l = to_l;
+          at_u = to_u;
+          high = low;
+          low *= ratio;
         }
       }
     }
@@ -845,31 +851,29 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     if (static_cast<u64>(q.k) <= static_cast<u64>(cta.size) * kThreads / 2) {
       Bracket br;
       clear_counts();
-      const float z = sc.z(x0[0]), y = __fmaf_rn(z, -static_cast<float>(kBinsPerOctave), 8388608.0f);
+      const float z = sc.z(x0[0]), y = Bracket::pattern(z);
       const int at = br.at(z, y);
       if (at < kBins) atomicAdd(&hist[at], 1u);
-      decide(br, true, static_cast<u64>(q.k), 0, 0);
+      decide(br, true, static_cast<u64>(q.k), 0, 0, 0);
       if (s.say[4] >= static_cast<u64>(q.k)) {
         // Every score down to the bin of the k-th largest of the threads' largest.
         const uint32_t last = static_cast<uint32_t>(s.say[1]) + Bracket::kPattern;
         each(
-            [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
-              uint32_t near = 0xFFFFFFFFu;
-              u64 y2[E / 2];
+            [&](const float (&x)[E], const float (&z)[E], int v) {
+              uint32_t y[E], near = 0xFFFFFFFFu;
 #pragma unroll
-              for (int i = 0; i < E / 2; ++i) {
-                y2[i] = Bracket::pattern2(z[i]);
-                near = min(near, min(static_cast<uint32_t>(y2[i]), static_cast<uint32_t>(y2[i] >> 32)));
+              for (int i = 0; i < E; ++i) {
+                y[i] = __float_as_uint(Bracket::pattern(z[i]));
+                near = min(near, y[i]);
               }
               if (near <= last) {  // few vectors hold any
                 unsigned mask = 0;
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i)
-                  mask |= (static_cast<uint32_t>(y2[i]) <= last ? 1u : 0u) << (2 * i) | (static_cast<uint32_t>(y2[i] >> 32) <= last ? 2u : 0u) << (2 * i);
-                append(mask, x, v);
+                for (int i = 0; i < E; ++i) mask |= (y[i] <= last ? 1u : 0u) << i;
+                append(mask, v);
               }
             },
-            [&] {});
+            [](unsigned) {});
         n = merge_lists();
       }
     }
@@ -898,34 +902,39 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
       const bool sum_it = !for_k;
       Mass m;
       if (!br.fine && cut == 0) {
+        const uint32_t counts = smem_addr(hist) - Bracket::kPattern * 4u;  // a pattern's count, modulo 2^32
         each(
-            [&](const float (&)[E], const u64 (&z)[E / 2], int) {
+            [&](const float (&)[E], const float (&z)[E], int) {
 #pragma unroll
-              for (int i = 0; i < E / 2; ++i) {
-                const u64 y2 = Bracket::pattern2(z[i]);
-                const uint32_t ba = Bracket::bin(low2(y2)), bb = Bracket::bin(high2(y2));
-                if (ba < static_cast<uint32_t>(kBins)) atomicAdd(&hist[ba], 1u);
-                if (bb < static_cast<uint32_t>(kBins)) atomicAdd(&hist[bb], 1u);
-                if (sum_it) m.add(pack2(ex2(low2(z[i])), ex2(high2(z[i]))));
+              for (int i = 0; i < E; ++i) {
+                const uint32_t y = __float_as_uint(Bracket::pattern(z[i]));
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\t"
+                    "setp.lt.u32 p, %1, %2;\n\t"
+                    "@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(counts + y * 4u),
+                    "r"(y), "r"(Bracket::kPattern + kBins)
+                    : "memory");
+              }
+              if (sum_it) {
+#pragma unroll
+                for (int i = 0; i < E; i += 2) m.add(ex2(z[i]), ex2(z[i + 1]));
               }
             },
-            [&] { m.flush(); });
+            [&](unsigned n) { if (sum_it) m.flush(n); });
       } else {
         each(
-            [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
+            [&](const float (&x)[E], const float (&z)[E], int v) {
               const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
 #pragma unroll
-              for (int i = 0; i < E / 2; ++i) {
-                const u64 y2 = Bracket::pattern2(z[i]);
-                const float za = low2(z[i]), zb = high2(z[i]);
-                const int pa = br.at(za, low2(y2)), pb = br.at(zb, high2(y2));
-                const bool ka = in >> (2 * i) & 1u, kb = in >> (2 * i + 1) & 1u;
+              for (int i = 0; i < E; i += 2) {
+                const int pa = br.at(z[i], Bracket::pattern(z[i])), pb = br.at(z[i + 1], Bracket::pattern(z[i + 1]));
+                const bool ka = in >> i & 1u, kb = in >> (i + 1) & 1u;
                 if (ka && pa >= 0 && pa < kBins) atomicAdd(&hist[pa], 1u);
                 if (kb && pb >= 0 && pb < kBins) atomicAdd(&hist[pb], 1u);
-                if (sum_it) m.add(pack2(ka && (!br.fine || pa < 0) ? ex2(za) : 0.0f, kb && (!br.fine || pb < 0) ? ex2(zb) : 0.0f));
+                if (sum_it) m.add(ka && (!br.fine || pa < 0) ? ex2(z[i]) : 0.0f, kb && (!br.fine || pb < 0) ? ex2(z[i + 1]) : 0.0f);
               }
             },
-            [&] { m.flush(); });
+            [&](unsigned n) { if (sum_it) m.flush(n); });
       }
       if (sum_it) {
         const u64 sum = cta.reduce<false>(m.total);  // of all, or of the ones ahead of the finer bins
@@ -935,10 +944,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
           sum_all = sum;
       }
       const u64 target = for_k ? static_cast<u64>(q.k) : share(sum_all, q.part_p);
-      decide(br, for_k, target, above, count_above);
+      decide(br, for_k, target, above, count_above, for_k || br.fine ? 0 : sum_all);
       br.from = static_cast<int>(s.say[0]);
       br.to = static_cast<int>(s.say[1]);
-      const u64 ahead = s.say[2], in = s.say[3] - s.say[2], reach = s.say[4];
+      const u64 ahead = s.say[2], reach = s.say[4];
+      const u64 in = (s.say[3] == ~0ull ? reach : s.say[3]) - ahead;  // a lower bound need not get to the target
       u64 last_key;
       if (for_k && !br.fine && reach <= target) {
         last_key = 0;  // everything that has a weight is among the top_k
@@ -963,42 +973,41 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
           Mass m2;
           if (!br.fine) {
             const uint32_t first = static_cast<uint32_t>(from) + Bracket::kPattern, width = static_cast<uint32_t>(br.to - from);
-            const float edge = __uint_as_float(first);
             const bool weigh = !for_k && !small;
             each(
-                [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
-                  uint32_t near = 0xFFFFFFFFu;
-                  u64 y2[E / 2];
+                [&](const float (&x)[E], const float (&z)[E], int v) {
+                  uint32_t d[E], near = 0xFFFFFFFFu;
 #pragma unroll
-                  for (int i = 0; i < E / 2; ++i) {
-                    y2[i] = Bracket::pattern2(z[i]);
-                    near = min(near, min(static_cast<uint32_t>(y2[i]) - first, static_cast<uint32_t>(y2[i] >> 32) - first));
-                    if (weigh) m2.add(pack2(low2(y2[i]) < edge ? ex2(low2(z[i])) : 0.0f, high2(y2[i]) < edge ? ex2(high2(z[i])) : 0.0f));
+                  for (int i = 0; i < E; ++i) {
+                    d[i] = __float_as_uint(Bracket::pattern(z[i])) - first;
+                    near = min(near, d[i]);
+                  }
+                  if (weigh) {
+#pragma unroll
+                    for (int i = 0; i < E; i += 2)
+                      m2.add(static_cast<int>(d[i]) < 0 ? ex2(z[i]) : 0.0f, static_cast<int>(d[i + 1]) < 0 ? ex2(z[i + 1]) : 0.0f);
                   }
                   if (near <= width) {  // few vectors hold any
                     unsigned mask = 0;
 #pragma unroll
-                    for (int i = 0; i < E / 2; ++i)
-                      mask |= (static_cast<uint32_t>(y2[i]) - first <= width ? 1u : 0u) << (2 * i) |
-                              (static_cast<uint32_t>(y2[i] >> 32) - first <= width ? 2u : 0u) << (2 * i);
-                    append(only_kept(mask, x, v, cut), x, v);
+                    for (int i = 0; i < E; ++i) mask |= (d[i] <= width ? 1u : 0u) << i;
+                    append(only_kept(mask, x, v, cut), v);
                   }
                 },
-                [&] { m2.flush(); });
+                [&](unsigned n) { if (weigh) m2.flush(n); });
           } else {
             each(
-                [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
+                [&](const float (&x)[E], const float (&z)[E], int v) {
                   unsigned mask = 0;
 #pragma unroll
-                  for (int i = 0; i < E / 2; ++i) {
-                    const u64 y2 = Bracket::pattern2(z[i]);
-                    const int pa = br.at(low2(z[i]), low2(y2)), pb = br.at(high2(z[i]), high2(y2));
-                    mask |= (pa >= from && pa <= br.to ? 1u : 0u) << (2 * i) | (pb >= from && pb <= br.to ? 2u : 0u) << (2 * i);
-                    if (!for_k) m2.add(pack2(pa < from ? ex2(low2(z[i])) : 0.0f, pb < from ? ex2(high2(z[i])) : 0.0f));
+                  for (int i = 0; i < E; i += 2) {
+                    const int pa = br.at(z[i], Bracket::pattern(z[i])), pb = br.at(z[i + 1], Bracket::pattern(z[i + 1]));
+                    mask |= (pa >= from && pa <= br.to ? 1u : 0u) << i | (pb >= from && pb <= br.to ? 2u : 0u) << i;
+                    if (!for_k) m2.add(pa < from ? ex2(z[i]) : 0.0f, pb < from ? ex2(z[i + 1]) : 0.0f);
                   }
-                  append(only_kept(mask, x, v, cut), x, v);
+                  append(only_kept(mask, x, v, cut), v);
                 },
-                [&] { m2.flush(); });
+                [&](unsigned n) { if (!for_k) m2.flush(n); });
           }
           if (!for_k && !small) {
             above = cta.reduce<false>(m2.total);
@@ -1073,23 +1082,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
   if (!summed) {
     Mass m;
     each(
-        [&](const float (&x)[E], const u64 (&z)[E / 2], int v) {
-          if (cut == 0) {
+        [&](const float (&x)[E], const float (&z)[E], int v) {
+          const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
+          if (cut == 0 && q.min_p == 0.0f) {
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-              const float ea = ex2(low2(z[i])), eb = ex2(high2(z[i]));
-              m.add(q.min_p == 0.0f ? pack2(ea, eb) : pack2(ea >= q.min_p ? ea : 0.0f, eb >= q.min_p ? eb : 0.0f));
-            }
+            for (int i = 0; i < E; i += 2) m.add(ex2(z[i]), ex2(z[i + 1]));
           } else {
-            const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-              const float ea = ex2(low2(z[i])), eb = ex2(high2(z[i]));
-              m.add(pack2((in >> (2 * i) & 1u) && ea >= q.min_p ? ea : 0.0f, (in >> (2 * i + 1) & 1u) && eb >= q.min_p ? eb : 0.0f));
+            for (int i = 0; i < E; i += 2) {
+              const float ea = ex2(z[i]), eb = ex2(z[i + 1]);
+              m.add((in >> i & 1u) && ea >= q.min_p ? ea : 0.0f, (in >> (i + 1) & 1u) && eb >= q.min_p ? eb : 0.0f);
             }
           }
         },
-        [&] { m.flush(); });
+        [&](unsigned n) { m.flush(n); });
     const u64 own = warp_sum(m.total);
     if (lane == 0) s.kept[cta.warp] = own;
   }
