@@ -50,18 +50,19 @@
 namespace rbf {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kOne = 68719476736.0f;  // 2^36: the largest weight
 constexpr int kBinsPerOctave = 128;
 constexpr int kBins = 37 * kBinsPerOctave + 1;  // z = 0 .. -37, rounded
 constexpr int kQuads = (kBins + 3) / 4;  // the counts are read four at a time
-constexpr int kListCap = kQuads * 2;     // as many 8-byte keys as the counts of all bins take
-constexpr int kMaxHeld = 192 * 1024;  // of a row's scores in one CTA's shared memory
-constexpr int kMaxSmem = kMaxHeld + kListCap * 8;
-constexpr int kSmall = kThreads;  // candidates of a row that one CTA finishes
+// Keys of a list: as many as fit where the counts of all bins are, more where
+// the row is not in shared memory.
+template <bool HELD>
+constexpr int kListCap = HELD ? kQuads * 2 : 8192;
+constexpr int kMaxHeld = 64 * 1024;  // of a row's scores in one CTA's shared memory
+constexpr int kMaxSmem = kMaxHeld + kListCap<true> * 8;
+constexpr int kSmall = 256;              // candidates of a row that one CTA finishes
 
 using u64 = unsigned long long;
 
@@ -298,29 +299,32 @@ __device__ __forceinline__ void remote_store(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
+template <int WARPS>
 struct Shared {
-  u64 part[kWarps];
+  u64 part[WARPS];
   u64 slot[2][kMaxCluster];  // one word per CTA, written by all of them; two turns
-  u64 kept[kWarps];          // the warps' kept sums
+  u64 kept[WARPS];          // the warps' kept sums
   u64 say[8];                // what CTA 0 has decided
-  u64 words[3][kMaxCluster]; // words that every CTA has sent to every other
+  u64 words[4][kMaxCluster]; // words that every CTA has sent to every other
   u64 small_key[kSmall];     // candidates, and what they keep
   u64 small_w[kSmall];
-  unsigned add_lo[kWarps], add_hi[kWarps];
-  u64 scan[3][kWarps];
+  unsigned add_lo[WARPS], add_hi[WARPS];
+  u64 scan[4][WARPS];
+  u64 found[4];              // this CTA's part of say[0] .. say[3]
   int lo, hi;                // the vectors that still may hold the choice
   u64 before;                // kept sum ahead of them
   unsigned list_len;
 };
 
 // The CTAs of a row's cluster, and this one in it.
+template <int WARPS>
 struct Cta {
-  Shared& s;
+  Shared<WARPS>& s;
   uint32_t rank, size;
   int warp, lane;
   int turn = 0;
 
-  __device__ __forceinline__ Cta(Shared& sh) : s(sh) {
+  __device__ __forceinline__ Cta(Shared<WARPS>& sh) : s(sh) {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
     warp = threadIdx.x >> 5;
@@ -340,7 +344,7 @@ struct Cta {
     __syncthreads();  // the words of the last reduction have been read
     if (lane == 0) s.part[warp] = v;
     __syncthreads();
-    u64 r = lane < kWarps ? s.part[lane] : 0ull;
+    u64 r = lane < WARPS ? s.part[lane] : 0ull;
     r = MAX ? warp_max(r) : warp_sum(r);
     if (size == 1) return r;
     if (threadIdx.x < size) remote_store(remote(&s.slot[turn][rank], threadIdx.x), r);
@@ -386,22 +390,25 @@ struct Bracket {
   __device__ __forceinline__ float step() const { return fine ? -1.0f / scale : -1.0f / kBinsPerOctave; }
 };
 // Sums of counts times the weights at the bins' edges bound the sums of weights;
-// they are made in fp32, in units of the largest weight: 2^-9 covers the
-// rounding of z, of the edges and of a few thousand additions, 2^-36 a score
-// the weights' own.
-constexpr float kBelow = 1.0f - 0x1p-9f, kAbove = 1.0f + 0x1p-9f;
+// a thread makes them in fp32, in units of the largest weight: 2^-14 covers the
+// rounding of z (under 2^-18), of the edges and of its few dozen additions,
+// 2^-36 a score the weights' own.
+constexpr float kBelow = 1.0f - 0x1p-14f, kAbove = 1.0f + 0x1p-14f;
 
-template <typename T, bool HELD>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch a) {
+// HELD: a CTA's part of the row is in shared memory.
+template <typename T, bool HELD, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleLaunch a) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kCap = kListCap<HELD>;
   constexpr int E = Vec<T>::kLen;
   constexpr int kFlush = 8192 / E;  // vectors that Mass sums before a flush
   extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ Shared s;
+  __shared__ Shared<kWarps> s;
   unsigned* hist = reinterpret_cast<unsigned*>(dyn);  // kBins counts, or
-  u64* list = reinterpret_cast<u64*>(dyn);            // kListCap keys
-  uint4* held = reinterpret_cast<uint4*>(dyn + kListCap * sizeof(u64));
+  u64* list = reinterpret_cast<u64*>(dyn);            // kCap keys
+  uint4* held = reinterpret_cast<uint4*>(dyn + kCap * sizeof(u64));
 
-  Cta cta(s);
+  Cta<kWarps> cta(s);
   const int lane = cta.lane;
   const int64_t r = blockIdx.x / cta.size;
   const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     unsigned at = atomicAdd(&s.list_len, static_cast<unsigned>(__popc(mask)));
     for (; mask != 0; mask &= mask - 1, ++at) {
       const int i = __ffs(static_cast<int>(mask)) - 1;
-      if (at < kListCap) list[at] = make_key(score_at(v, i), static_cast<uint32_t>(index_of(v, i)));
+      if (at < kCap) list[at] = make_key(score_at(v, i), static_cast<uint32_t>(index_of(v, i)));
     }
   };
   // Clear the bits of the scores whose keys are under `cut`.
@@ -578,15 +585,17 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
   // scores (for_k) or weight: say[0], say[1] the first and last position, say[2]
   // scores ahead of the first, say[3] scores down to the last one, say[4] all.
   // Each CTA adds up the cluster's counts for an equal part of the positions.
-  // Where all positions' weights have been summed (`sum`, else 0), the bounds
-  // are taken from the other end too: those of a prefix are the sum less those
-  // of the rest, and near top_p = 1 that rest is small, and so is its error.
+  // For weights `mine` is the thread's sum of all of them or, with finer bins, of
+  // the ones ahead; the row's goes to sum_all or above, and the target follows.
+  // Where all are summed the bounds are taken from the other end too: those of a
+  // prefix are the sum less those of the rest, and near top_p = 1 that rest is
+  // small, and so is its error.
   auto clear_counts = [&]() {
     for (int i = threadIdx.x; i < kQuads; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x == 0) s.list_len = 0;
-    cta.sync();
+    __syncthreads();
   };
-  auto decide = [&](const Bracket& br, bool for_k, u64 target, u64 above, u64 count_above, u64 sum) {
+  auto decide = [&](const Bracket& br, bool for_k, u64 mine, u64& sum_all, u64& above, u64 count_above, u64& target) {
     cta.sync();  // all counts are there
     const int per = (kQuads + static_cast<int>(cta.size) * kThreads - 1) / (static_cast<int>(cta.size) * kThreads);  // a thread's
     const int q0 = (static_cast<int>(cta.rank) * kThreads + static_cast<int>(threadIdx.x)) * per;
@@ -642,22 +651,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
       s.scan[1][cta.warp] = sl;
       s.scan[2][cta.warp] = su;
     }
+    mine = warp_sum(mine);
+    if (lane == 0) s.scan[3][cta.warp] = mine;
     if (threadIdx.x == 0) {
       s.say[0] = s.say[1] = kBins - 1;
       s.say[2] = s.say[3] = ~0ull;  // not told
+      s.found[0] = s.found[1] = ~0ull;
     }
     __syncthreads();
     // The warps' and the CTAs' totals, and with them the values ahead of this thread's bins.
     const bool warp_there = lane < kWarps, warp_ahead = lane < cta.warp;
     const u64 on = warp_there ? s.scan[0][lane] : 0ull, ol = warp_there ? s.scan[1][lane] : 0ull, ou = warp_there ? s.scan[2][lane] : 0ull;
     u64 fn = count_above + warp_sum(warp_ahead ? on : 0ull) + sn - n;
-    u64 fl = above + warp_sum(warp_ahead ? ol : 0ull) + sl - wl, fu = above + warp_sum(warp_ahead ? ou : 0ull) + su - wu;
-    u64 all = warp_sum(on), all_l = warp_sum(ol), all_u = warp_sum(ou);
+    u64 fl = warp_sum(warp_ahead ? ol : 0ull) + sl - wl, fu = warp_sum(warp_ahead ? ou : 0ull) + su - wu;
+    u64 all = warp_sum(on), all_l = warp_sum(ol), all_u = warp_sum(ou), all_m = warp_sum(warp_there ? s.scan[3][lane] : 0ull);
     if (cta.size > 1) {
       if (threadIdx.x < cta.size) {
         remote_store(remote(&s.words[0][cta.rank], threadIdx.x), all);
         remote_store(remote(&s.words[1][cta.rank], threadIdx.x), all_l);
         remote_store(remote(&s.words[2][cta.rank], threadIdx.x), all_u);
+        remote_store(remote(&s.words[3][cta.rank], threadIdx.x), all_m);
       }
       cta.sync();
       const bool there = lane < static_cast<int>(cta.size), ahead = lane < static_cast<int>(cta.rank);
@@ -669,16 +682,25 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
       all_u = warp_sum(cu);
       fl += warp_sum(ahead ? cl : 0ull);
       fu += warp_sum(ahead ? cu : 0ull);
+      all_m = warp_sum(there ? s.words[3][lane] : 0ull);
     }
+    if (for_k) {
+      target = static_cast<u64>(q.k);
+    } else if (br.fine) {
+      above = all_m;
+    } else {
+      sum_all = all_m;
+      target = share(sum_all, q.part_p);
+    }
+    const u64 sum = for_k || br.fine ? 0 : sum_all;
+    fl += above;
+    fu += above;
     // Bounds on the weight down to a point that has the running sums l and u.
     auto at_least = [&](u64 l, u64 u) { return sum ? max(static_cast<long long>(l), static_cast<long long>(sum - all_u + u)) : static_cast<long long>(l); };
     auto at_most = [&](u64 l, u64 u) { return sum ? min(static_cast<long long>(u), static_cast<long long>(sum - all_l + l)) : static_cast<long long>(u); };
     const long long goal = static_cast<long long>(target);
     if (threadIdx.x == 0) s.say[4] = count_above + all;
-    // The thread in whose bins a running value reaches the target tells all.
-    auto say = [&](int word, u64 v) {
-      for (uint32_t o = 0; o < cta.size; ++o) remote_store(remote(&s.say[word], o), v);
-    };
+    // The thread in whose bins a running value reaches the target says so.
     const u64 nl = fl + wl, nu = fu + wu;
     const long long start_l = at_least(fl, fu), start_u = at_most(fl, fu);
     if (n > 0 && (for_k ? fn < target && fn + n >= target
@@ -703,13 +725,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
           const bool first = for_k ? counted < target && counted + c[i] >= target : at_u < goal && to_u >= goal;
           const bool last = for_k ? first : at_l < goal && to_l >= goal;
           if (first) {
-            say(0, b);
-            say(2, fn);
+            s.found[0] = b;
+            s.found[2] = fn;
           }
           fn += c[i];
           if (last) {
-            say(1, b);
-            say(3, fn);
+            s.found[1] = b;
+            s.found[3] = fn;
           }
           at_l = to_l;
           at_u = to_u;
@@ -718,23 +740,35 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
         }
       }
     }
+    __syncthreads();
+    if (threadIdx.x < 2 * cta.size) {
+      const int w = threadIdx.x & 1;
+      if (s.found[w] != ~0ull) {
+        remote_store(remote(&s.say[w], threadIdx.x >> 1), s.found[w]);
+        remote_store(remote(&s.say[2 + w], threadIdx.x >> 1), s.found[2 + w]);
+      }
+    }
     cta.sync();
   };
 
-  // All CTAs' lists behind CTA 0's; the number of keys (more than kListCap:
-  // they are not all there).
-  auto merge_lists = [&]() -> u64 {
-    __syncthreads();
+  // All CTAs' lists behind CTA 0's; the number of keys (more than kCap:
+  // they are not all there). `sum`, a value of each thread, becomes the row's.
+  auto merge_lists = [&](u64& sum) -> u64 {
+    sum = block_sum(sum, 0);
     if (cta.size == 1) return s.list_len;
     const unsigned mine = s.list_len;
-    if (threadIdx.x < cta.size) remote_store(remote(&s.words[0][cta.rank], threadIdx.x), mine);
+    if (threadIdx.x < cta.size) {
+      remote_store(remote(&s.words[0][cta.rank], threadIdx.x), mine);
+      remote_store(remote(&s.words[1][cta.rank], threadIdx.x), sum);
+    }
     cta.sync();
+    sum = warp_sum(lane < static_cast<int>(cta.size) ? s.words[1][lane] : 0ull);
     u64 all = 0, at = 0;
     for (uint32_t o = 0; o < cta.size; ++o) {
       if (o < cta.rank) at += s.words[0][o];
       all += s.words[0][o];
     }
-    if (cta.rank != 0 && all <= kListCap)
+    if (cta.rank != 0 && all <= kCap)
       for (unsigned i = threadIdx.x; i < mine; i += kThreads) remote_store(remote(&list[at + i], 0), list[i]);
     cta.sync();
     return all;
@@ -749,11 +783,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     const u64 key = t < n ? list[t] : 0ull;
     const float e = t < n ? ex2(sc.z(key_score(key))) : 0.0f;
     const u64 w = fixed(e);
-    s.small_key[t] = key;
-    s.small_w[t] = w;
+    if (t < kSmall) {
+      s.small_key[t] = key;
+      s.small_w[t] = w;
+    }
     __syncthreads();
     int rank = 0;
     u64 ahead = 0;  // weight of the better candidates
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
       const bool better = s.small_key[j] > key;
       rank += better;
@@ -766,10 +803,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     }
     keep = t < n && (rank == 0 || (keep && e >= q.min_p));
     const u64 all = block_sum(keep ? w : 0ull, 1);  // also: everyone has read small_w
-    s.small_w[t] = keep ? w : 0ull;
+    if (t < kSmall) s.small_w[t] = keep ? w : 0ull;
     __syncthreads();
     const uint32_t low = static_cast<uint32_t>(key);  // falls as the index rises
     u64 before = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) before += static_cast<uint32_t>(s.small_key[j]) > low ? s.small_w[j] : 0ull;
     const u64 aim = share(all, q.part_u);
     if (keep && before <= aim && aim < before + w) {
@@ -780,10 +818,25 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
 
   // In CTA 0: the largest key K of the list for which `base` plus the number
   // (for_k) or weight of its keys from K on reaches the target. Keys without
-  // the bits that are the same for all are divided into as many buckets as
-  // there are threads, then the keys of the bucket in which the target is
+  // the bits that are the same for all are divided into kSmall buckets, then the keys of the bucket in which the target is
   // reached again, until a bucket is one key.
   auto list_cut = [&](int len, bool for_k, u64 base, u64 target) -> u64 {
+    if (len <= kSmall) {  // every thread has a key and looks at all of them
+      const int t = threadIdx.x;
+      const u64 key = t < len ? list[t] : 0ull;
+      const u64 w = t < len ? (for_k ? 1ull : weight(key_score(key), sc)) : 0ull;
+      if (t < kSmall) {
+        s.small_key[t] = key;
+        s.small_w[t] = w;
+      }
+      __syncthreads();
+      u64 ahead = base;
+#pragma unroll 8
+      for (int j = 0; j < len; ++j) ahead += s.small_key[j] > key ? s.small_w[j] : 0ull;
+      if (t < len && ahead < target && ahead + w >= target) s.found[0] = key;
+      __syncthreads();
+      return s.found[0];
+    }
     constexpr int kSame = Vec<T>::kSame;
     const int index_bits = 32 - __clz(a.vocab);
     const u64 index_mask = (u64(1) << index_bits) - 1;
@@ -811,8 +864,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     }
     for (;;) {  // the target is reached within [lo, hi]
       const int width = 64 - __clzll(static_cast<long long>(hi - lo));
-      const int shift = max(0, width - 8);  // kThreads = 2^8 buckets
-      s.small_w[threadIdx.x] = 0;
+      const int shift = max(0, width - 8);  // kSmall = 2^8 buckets
+      if (threadIdx.x < kSmall) s.small_w[threadIdx.x] = 0;
       __syncthreads();
       for (int j = threadIdx.x; j < len; j += kThreads) {
         const u64 key = list[j], k = short_key(key);
@@ -820,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
       }
       __syncthreads();
       // From the last bucket down: a thread has one.
-      const int bucket = kThreads - 1 - static_cast<int>(threadIdx.x);
-      const u64 w = s.small_w[bucket];
+      const int bucket = kSmall - 1 - static_cast<int>(threadIdx.x);
+      const u64 w = bucket >= 0 ? s.small_w[bucket] : 0ull;
       const u64 incl = warp_scan(w, lane);
       if (lane == 31) s.scan[2][cta.warp] = incl;
       __syncthreads();
@@ -847,14 +900,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
 
   if (by_k) {
     // ----------------------------------------------- 3. the k best, in a list
-    u64 n = kListCap + 1;
+    u64 n = kCap + 1;
     if (static_cast<u64>(q.k) <= static_cast<u64>(cta.size) * kThreads / 2) {
       Bracket br;
       clear_counts();
       const float z = sc.z(x0[0]), y = Bracket::pattern(z);
       const int at = br.at(z, y);
       if (at < kBins) atomicAdd(&hist[at], 1u);
-      decide(br, true, static_cast<u64>(q.k), 0, 0, 0);
+      u64 none = 0, goal = 0;
+      decide(br, true, 0, none, none, 0, goal);
       if (s.say[4] >= static_cast<u64>(q.k)) {
         // Every score down to the bin of the k-th largest of the threads' largest.
         const uint32_t last = static_cast<uint32_t>(s.say[1]) + Bracket::kPattern;
@@ -874,14 +928,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
               }
             },
             [](unsigned) {});
-        n = merge_lists();
+        n = merge_lists(none);
       }
     }
     if (n <= kSmall) {
       if (cta.rank == 0) finish_small(static_cast<int>(n), 0);
       return;
     }
-    if (n <= kListCap) {
+    if (n <= kCap) {
       if (cta.rank == 0) {
         const u64 key = list_cut(static_cast<int>(n), true, 0, static_cast<u64>(q.k));
         if (threadIdx.x == 0) s.say[6] = key;
@@ -896,6 +950,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
     u64 above = 0;                      // sum of weights ahead of the finer bins
     u64 count_above = 0;                // and number of scores
     u64 sum_all = 0;                    // sum of what top_k kept
+    u64 target = 0;                     // number or weight at which the prefix ends
     bool for_k = by_k && cut == 0;      // which of the two ends is looked for
     for (;;) {
       clear_counts();
@@ -936,15 +991,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
             },
             [&](unsigned n) { if (sum_it) m.flush(n); });
       }
-      if (sum_it) {
-        const u64 sum = cta.reduce<false>(m.total);  // of all, or of the ones ahead of the finer bins
-        if (br.fine)
-          above = sum;
-        else
-          sum_all = sum;
-      }
-      const u64 target = for_k ? static_cast<u64>(q.k) : share(sum_all, q.part_p);
-      decide(br, for_k, target, above, count_above, for_k || br.fine ? 0 : sum_all);
+      decide(br, for_k, m.total, sum_all, above, count_above, target);
       br.from = static_cast<int>(s.say[0]);
       br.to = static_cast<int>(s.say[1]);
       const u64 ahead = s.say[2], reach = s.say[4];
@@ -954,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
         last_key = 0;  // everything that has a weight is among the top_k
       } else {
         const bool small = !for_k && !br.fine && ahead + in <= kSmall;  // all that may be kept
-        if (!small && in > kListCap && !br.fine) {
+        if (!small && in > kCap && !br.fine) {
           // Divide the bins again.
           Bracket f;
           f.fine = true;
@@ -967,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
           cta.sync();  // what CTA 0 said has been read
           continue;
         }
-        if (small || in <= kListCap) {
+        if (small || in <= kCap) {
           // ------------------------------------------------- 4. gather
           const int from = small ? 0 : br.from;
           Mass m2;
@@ -1010,11 +1057,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
                 [&](unsigned n) { if (!for_k) m2.flush(n); });
           }
           if (!for_k && !small) {
-            above = cta.reduce<false>(m2.total);
             const u64 own = warp_sum(m2.total);
             if (lane == 0) s.kept[cta.warp] = own;
           }
-          const int len = static_cast<int>(merge_lists());
+          u64 ahead_sum = m2.total;
+          const int len = static_cast<int>(merge_lists(ahead_sum));
+          above = ahead_sum;
           if (small) {
             if (cta.rank == 0) finish_small(len, sum_all);
             return;
@@ -1039,16 +1087,32 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
               const int v = (static_cast<int>(key_index(key)) + row.lead) / E;
               int o = static_cast<int>(int64_t(v - c0) * kWarps / (c1 - c0));
               while (v >= part_of(c0, c1, o + 1)) ++o;  // the division may round down across a part's start
-              atomicAdd(&s.add_lo[o], static_cast<unsigned>(w & 0xFFFFFu));  // kListCap of them stay under 2^32
-              atomicAdd(&s.add_hi[o], static_cast<unsigned>(w >> 20));
+              atomicAdd(&s.add_lo[o], static_cast<unsigned>(w & 0x7FFFFu));  // 2^13 of them stay under 2^32
+              atomicAdd(&s.add_hi[o], static_cast<unsigned>(w >> 19));
             }
             __syncthreads();
             if (threadIdx.x < kWarps)
-              s.kept[threadIdx.x] += (static_cast<u64>(s.add_hi[threadIdx.x]) << 20) + s.add_lo[threadIdx.x];
+              s.kept[threadIdx.x] += (static_cast<u64>(s.add_hi[threadIdx.x]) << 19) + s.add_lo[threadIdx.x];
           }
         } else {
-          // Equal scores by the thousand: halve the interval of keys.
-          u64 lo = cut, hi = make_key(top, 0) + 1;
+          // Equal scores by the thousand: halve the interval between the
+          // smallest and the largest key of the finer bins.
+          u64 lo = 0, hi = 0;  // the complement of the smallest; the largest
+          each(
+              [&](const float (&x)[E], const float (&z)[E], int v) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                  const int at = br.at(z[i], Bracket::pattern(z[i]));
+                  const u64 key = key_of(x[i], v, i);
+                  if (at >= br.from && at <= br.to && key >= cut) {
+                    lo = umax64(lo, ~key);
+                    hi = umax64(hi, key);
+                  }
+                }
+              },
+              [](unsigned) {});
+          lo = ~cta.template reduce<true>(lo);
+          hi = cta.template reduce<true>(hi) + 1;
           while (hi - lo > 1) {
             const u64 mid = lo + (hi - lo) / 2;
             u64 c = 0;
@@ -1171,9 +1235,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleLaunch 
   }
 }
 
-template <typename T, bool HELD>
+template <typename T, bool HELD, int kThreads>
 cudaError_t launch_t(const SampleLaunch& a, int cluster, int held_bytes, cudaStream_t st) {
-  auto fn = sample_kernel<T, HELD>;
+  auto fn = sample_kernel<T, HELD, kThreads>;
   static PerDeviceOnce once;
   const cudaError_t ready = once.run([fn] {
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -1183,7 +1247,7 @@ cudaError_t launch_t(const SampleLaunch& a, int cluster, int held_bytes, cudaStr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kListCap * sizeof(u64) + static_cast<size_t>(held_bytes);
+  cfg.dynamicSmemBytes = kListCap<HELD> * sizeof(u64) + static_cast<size_t>(held_bytes);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1198,13 +1262,16 @@ cudaError_t launch_t(const SampleLaunch& a, int cluster, int held_bytes, cudaStr
 template <typename T>
 cudaError_t launch_rows(const SampleLaunch& a, cudaStream_t st) {
   const int64_t bytes = int64_t(a.vocab) * sizeof(T) + 32;
-  // A CTA's part in shared memory: 32 KB leaves room for four CTAs an SM, whose
-  // reads overlap the others' passes.
+  // A CTA's part in shared memory: 32 KB leaves room for four CTAs an SM (of 57
+  // KB with the counts), whose reads overlap the others' passes.
   int cluster = 1;
   while (cluster < kMaxCluster && bytes / cluster > 32 * 1024) cluster *= 2;
   const int64_t held = (bytes + cluster - 1) / cluster / 16 * 16 + 32;
-  if (held <= kMaxHeld) return launch_t<T, true>(a, cluster, static_cast<int>(held), st);
-  return launch_t<T, false>(a, cluster, 0, st);
+  if (held <= kMaxHeld) return launch_t<T, true, 256>(a, cluster, static_cast<int>(held), st);
+  // Longer parts are read again from L2, with two CTAs an SM: a cluster of 16
+  // CTAs that fill an SM each finds room in few of the GPU's clusters of SMs (8
+  // rows of 1M: 28 us, 37 with 1,024 threads a CTA and half of the rows waiting).
+  return launch_t<T, false, 512>(a, cluster, 0, st);
 }
 
 }  // namespace

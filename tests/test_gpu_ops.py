@@ -435,3 +435,24 @@ def test_handle_limits(ops):
             bad()
         assert e.value.status == rbf.RBF_ERR_INVALID_VALUE
     small.close()
+
+
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 300000), ("f32", 70001)])
+def test_sample_thousands_of_equal_scores(ops, dtype, vocab):
+    """The kept prefix ends among thousands of equal scores, which no bins divide."""
+    g = np.random.default_rng(vocab)
+    x = on_gpu(np.where(g.random((4, vocab)) < 0.3, g.integers(-3, 3, (4, vocab)), -1).astype(np.float32), FLOATS[dtype])
+    u = g.random(4).astype(np.float32)
+    check_exact(ops, x, u, top_k=[vocab // 2, 5000, 2, vocab - 3])
+    check_exact(ops, x, u, top_p=np.array([0.5, 0.9, 0.01, 0.99], np.float32))
+    check_exact(ops, x, u, top_k=[vocab // 2, 5000, 300, vocab - 3], top_p=np.array([0.5, 0.9, 0.7, 0.99], np.float32))
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_sample_sorted_rows(ops, order):
+    """Sorted scores put all candidates into one part of the row."""
+    x = torch.sort(3 * torch.randn(3, 50000, device="cuda"), dim=1, descending=order < 0)[0].contiguous()
+    u = np.array([0.1, 0.5, 0.99], np.float32)
+    check_allowed(ops, x, u, top_k=[3, 300, 4000])
+    check_allowed(ops, x, u, top_p=np.array([0.5, 0.9, 0.99], np.float32))
+    check_allowed(ops, x, u, top_k=[50, 300, 4000], top_p=np.array([0.5, 0.9, 0.99], np.float32), min_p=0.001)
