@@ -559,12 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------- MMA issuer
     // The whole warp walks and waits, so that addresses and descriptors stay
     // in uniform registers, and one elected lane issues: 20 cycles an MMA of
-    // 32 tokens instead of 45 from a branch on the lane's number. An MMA of
-    // 256 tokens takes 130, and few are queued, so from 128 tokens on the next
-    // stage's barrier is looked at before the second half of this one is issued.
+    // 32 tokens instead of 45 from a branch on the lane's number.
     if (leader) {
       constexpr uint32_t idesc = make_idesc(kPairChannels, NT, 0u);
-      constexpr bool kPeek = NT >= 128;
       const bool even = (lane & 1) == 0;  // even lanes wait for the channels while odd ones wait for the tokens
       Slot<kRing> s;
       Slot<S::kXRing> xs;
@@ -579,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem_base + static_cast<uint32_t>(as.i * NT);
           tc_fence_after();
           for (int kk = k; kk < kend && ok; ++kk) {
-            if (!kPeek || !ready) {
+            if (!ready) {
               ok = __all_sync(kFullMask, mbar_wait(even ? &c_full[s.i] : &x_full[xs.i], even ? s.phase : xs.phase, p.timeout_ns));
               if (!ok) break;
             }
@@ -587,26 +584,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b0 = sw128_kmajor_desc(xring + xs.i * S::kXBytes);
             const uint64_t b1 = sw128_kmajor_desc(xring + xs.i * S::kXBytes + S::kXBytes / 2);
             const uint32_t c = tmem_base + S::kAcc * NT + static_cast<uint32_t>(s.i * kStageCols);
-            const bool one_lane = elect_one();
-            if (one_lane) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                umma_pair_ts(d, c + static_cast<uint32_t>(8 * i), b0 + static_cast<uint64_t>(2 * i), idesc,
-                             (kk != k) | (i != 0));
-            }
-            __syncwarp();
             Slot<kRing> next = s;
             next.advance();
             xs.advance();
-            if (kPeek)
-              ready = __all_sync(kFullMask, mbar_try_wait(even ? &c_full[next.i] : &x_full[xs.i], even ? next.phase : xs.phase));
-            if (one_lane) {
+            // Looked at now, and the answer used when this stage's MMAs are issued.
+            const bool there = mbar_try_wait(even ? &c_full[next.i] : &x_full[xs.i], even ? next.phase : xs.phase);
+            if (elect_one()) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                umma_pair_ts(d, c + static_cast<uint32_t>(8 * (i + 4)), b1 + static_cast<uint64_t>(2 * i), idesc, 1u);
+              for (int i = 0; i < kDepth / 16; ++i)
+                umma_pair_ts(d, c + static_cast<uint32_t>(8 * i), (i < 4 ? b0 : b1) + static_cast<uint64_t>(2 * (i & 3)), idesc,
+                             (kk != k) | (i != 0));
               umma_commit_pair(&done[s.i]);
             }
             __syncwarp();
+            ready = __all_sync(kFullMask, there);
             s = next;
           }
           if (ok && elect_one()) umma_commit_pair(&acc_full[as.i]);
