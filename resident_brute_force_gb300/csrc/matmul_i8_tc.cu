@@ -67,6 +67,11 @@ constexpr int kThreads = (2 + kWorkers + 1) * 32;
 constexpr int kTmemCols = 512;       // the accumulator first, then the ring of converted channels
 constexpr int kStageCols = kDepth / 2;
 constexpr int kRingBudget = 224 * 1024;
+// Stages' time that an exchange of partial sums takes: with 16 tokens, 1024 x
+// 8192 takes 18.5 us shared and 30.8 not, 4096 x 4096 18.1 and 18.6, 10007 x
+// 1536 with 37 tokens 19.4 and 12.4; 4096 x 4096 with 100 tokens 22.9 and 20.6.
+template <int NT>
+constexpr int kSplitCost = NT <= 64 ? 20 : 32;
 
 // OUT: what is stored: 0 the sums (int32), 1 fp32, 2 bf16, 3 fp16.
 template <int NT, int OUT>
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* meet = drain + 1;                // the workers of this CTA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
   __shared__ int abort_flag;
-  __shared__ unsigned last_flag;
+  __shared__ unsigned last_flag[2];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -626,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Warp-uniform: whether every lane's wait has ended in time.
     auto fine = [&](bool in_time) { return __all_sync(kFullMask, in_time) != 0; };
     uint32_t meet_phase = 0;
+    int flag = 0;
     auto workers_meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(meet);
@@ -780,22 +786,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         int* mine = slot_of(pair);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) __stcg(mine + c * kChannels, static_cast<int>(acc[c]));
-        __threadfence();
+        // One thread's fences order all of the CTA's: they have met before and meet after.
         ok = workers_meet();
         if (!ok) break;
         if (threadIdx.x == 64) {
+          __threadfence();
           const unsigned n = atomicAdd(&p.arrived[first * 2 + static_cast<int>(rank)], 1u) + 1u;
           const bool fin = n == static_cast<unsigned>(last - first + 1);
           if (fin) p.arrived[first * 2 + static_cast<int>(rank)] = 0u;
           __threadfence();
-          last_flag = fin ? 1u : 0u;
+          last_flag[flag] = fin ? 1u : 0u;
         }
         ok = workers_meet();
         if (!ok) break;
-        const bool fin = *reinterpret_cast<volatile unsigned*>(&last_flag) != 0;
-        __threadfence();
-        ok = workers_meet();  // last_flag may be written again
-        if (!ok) break;
+        const bool fin = *reinterpret_cast<volatile unsigned*>(&last_flag[flag]) != 0;
+        flag ^= 1;  // the next tile's is another word: this one may still be read
         if (!fin) continue;
         for (int who = first; who <= last; ++who) {
           if (who == pair) continue;
@@ -918,9 +923,10 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   p.timeout_ns = w.timeout_ns;
   const int64_t max_pairs = w.num_sms / 2;
   const int64_t total = static_cast<int64_t>(p.tiles) * p.stages;
-  // Whole tiles from four rounds on (the last round then costs a fifth at
-  // most), or where they come out even.
-  p.split = !(p.tiles >= 4 * max_pairs || p.tiles % max_pairs == 0);
+  // Shares of all stages where the rounds of whole tiles take longer by more
+  // than the exchange of partial sums does, in stages' time.
+  const int64_t rounds = (p.tiles + max_pairs - 1) / max_pairs;
+  p.split = rounds * p.stages > (total + max_pairs - 1) / max_pairs + kSplitCost<NT>;
   const int64_t pairs = p.split ? std::min(max_pairs, total) : std::min<int64_t>(max_pairs, p.tiles);
 
   auto fn = matmul_i8_pair_kernel<NT, OUT>;
@@ -979,7 +985,14 @@ cudaError_t launch_matmul_i8_tc(const MatmulI8Launch& a, const MatmulI8Workspace
   if (a.m <= 32) return launch_out<32>(a, w, st);
   if (a.m <= 64) return launch_out<64>(a, w, st);
   if (a.m <= 128) return launch_out<128>(a, w, st);
-  return launch_out<256>(a, w, st);
+  // A stage of 256 tokens takes 7/4 of one of 128 (0.40 us; the accumulator is
+  // one and waits to be read): whichever needs less time for its rounds of
+  // tiles. 256 x 8192 x 4096 takes 22.7 us with 128 and 33.0 with 256, 512
+  // tokens 35.0 and 33.3, 1000 tokens 62.4 and 58.8, 4096 tokens 202 and 186.
+  const int64_t pairs = w.num_sms / 2, channels = (a.n + kPairChannels - 1) / kPairChannels;
+  const int64_t rounds_128 = ((a.m + 127) / 128 * channels + pairs - 1) / pairs;
+  const int64_t rounds_256 = ((a.m + 255) / 256 * channels + pairs - 1) / pairs;
+  return rounds_256 * 7 < rounds_128 * 4 ? launch_out<256>(a, w, st) : launch_out<128>(a, w, st);
 }
 
 }  // namespace rbf

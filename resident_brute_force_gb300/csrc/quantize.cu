@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kQuantThreads)
 constexpr int kHeld = 4;  // groups of eight values a thread holds
 
 template <typename T, int THREADS, bool F16>
-__global__ void __launch_bounds__(kQuantThreads)
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 && THREADS > 32 ? 6 : 1)
     quantize_rows_held_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, const Out o) {
   pdl_launch_dependents();
   constexpr int kRows = kQuantThreads / THREADS;
@@ -76,12 +76,12 @@ __global__ void __launch_bounds__(kQuantThreads)
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / THREADS;
   if (kRows > 1 && r >= rows) return;  // whole warps
   const T* row = x + r * ld_x;
-  float v[kHeld][8];
+  Eight<T> v[kHeld];
   uint32_t top = 0;
 #pragma unroll
   for (int g = 0; g < kHeld; ++g) {
     const int c = (g * THREADS + t) * 8;
-    if (c < cols) load8(row + c, cols - c, v[g]);
+    if (c < cols) v[g].load(row + c, cols - c);
   }
 #pragma unroll
   for (int g = 0; g < kHeld; ++g)

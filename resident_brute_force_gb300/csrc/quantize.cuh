@@ -61,23 +61,26 @@ __device__ __forceinline__ uint32_t pack_bytes(float a, float b, float c, float 
   return __byte_perm(lo, hi, 0x5410);
 }
 
-// Eight values on a 16-byte boundary, zero from `live` on.
+// Eight values as they are in memory, read from a 16-byte boundary, zero from
+// `live` on.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int live, float (&x)[8]) {
-  if (live >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+struct Eight {
+  uint4 raw[sizeof(T) / 2];
+
+  __device__ __forceinline__ void load(const T* p, int live) {
+    if (live >= 8) {
+#pragma unroll
+      for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
     } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
+      for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      T* e = reinterpret_cast<T*>(raw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < live) e[i] = p[i];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < live ? to_f32(p[i]) : 0.0f;
   }
-}
+  __device__ __forceinline__ float operator[](int i) const { return to_f32(reinterpret_cast<const T*>(raw)[i]); }
+};
 
 }  // namespace rbf
