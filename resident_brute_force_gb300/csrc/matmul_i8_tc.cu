@@ -323,7 +323,7 @@ struct Part {
 // 64-byte swizzle (16-byte piece q of row r at q ^ (r / 2 % 4)) that spreads a
 // block's rows over all banks. From there one tiled TMA store a warp and tile
 // writes them and clips them at the matrix' edges; where the output's rows are
-// not on 16-byte boundaries, the warp's lanes store them.
+// not on 16-byte boundaries, or end between them, the warp's lanes store them.
 
 // The last tile's results have been read out of `buf`.
 template <int OUT>
@@ -339,7 +339,8 @@ __device__ __forceinline__ void store_end(const Params& p, const CUtensorMap* ma
                                           int lane) {
   if constexpr (OUT >= 2) {
     if (t.j0 >= p.n || t.live == 0) return;
-    if (p.tma_out) {
+    // The tensor store's clipping ends at 16 bytes, not at an element.
+    if (p.tma_out && (t.j0 + 32 <= p.n || p.n % 8 == 0)) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
