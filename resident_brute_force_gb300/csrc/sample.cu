@@ -25,10 +25,12 @@
 //   2. Without top_k and top_p a second pass sums the weights, per warp.
 //   3. top_k: of the threads' largest scores (distinct scores of the row), the
 //      k-th largest bounds the row's k-th from below, so one pass gathers
-//      little more than the k best into a list. top_p: a pass counts the
+//      little more than the k best into a list, from which top_p is found
+//      too. top_p, and a top_k past half of the threads: a pass counts the
 //      scores in bins of 2^(1/128) in weight and sums the weights; the counts
-//      bound the sums above each bin edge, which leaves two or three bins in
-//      which the prefix can end.
+//      bound the sums above each bin edge, which leaves one to three bins in
+//      which the prefix can end. With such a top_k, top_p takes two more
+//      passes, for its share of the weight that top_k kept.
 //   4. Few candidates (kSmall): one CTA finishes the row, every thread finding
 //      the rank and the running weight of its candidate by looking at all.
 //      Else the scores of those bins are gathered in a list, where K is found
@@ -38,6 +40,19 @@
 // Where a list does not hold the bins' scores they are divided into finer
 // bins; scores that coincide by the thousand (no bins divide them) leave K to
 // be found by halving the interval of keys, one pass over the row a step.
+//
+// What bounds it: the instructions of the passes over scores that are on chip
+// (conversion, scaling, bin and weight are some eight instructions a score),
+// the shared-memory atomics of the counts (11 to 14 lanes a clock and SM), and
+// per row some ten exchanges across the cluster at 450 clocks each. The text
+// counts too: the kernel is 150 to 177 KB, more than the instruction cache, and
+// passes that few rows take are loops over single scores (with every loop
+// unrolled it was 296 to 432 KB; 256 x 128,000 top_p from cold 143 us, now 133,
+// top_k 700 with top_p 230, now 124).
+// Measured (us, the bytes alone at the copy rate in brackets): 1 x 10,000 fp32
+// top_k + top_p 14 (0.006); 61 x 100,003 bf16 top_p 39 (1.8); 256 x 128,000 bf16
+// top_p 124, top_k <= 100 62, top_k 5,000-9,000 115, neither 43 (9.7);
+// 8 x 1,000,000 fp32 min_p 25, top_p 68 (4.7).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -134,6 +149,18 @@ __device__ __forceinline__ uint4 vec_none() {
   return make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
 }
 
+// Scores i0 .. i0 + kLen - 1 of a row of n, -infinity where there are none; out
+// of line, for the one or two vectors of a row that reach past it.
+template <typename T>
+__device__ __noinline__ uint4 load_edge(const T* p, int i0, int n) {
+  uint4 r = vec_none<T>();
+  T* e = reinterpret_cast<T*>(&r);
+#pragma unroll 1
+  for (int i = 0; i < Vec<T>::kLen; ++i)
+    if (i0 + i >= 0 && i0 + i < n) e[i] = p[i0 + i];
+  return r;
+}
+
 // A row as 16-byte vectors on 16-byte boundaries: vector v holds the elements
 // v * kLen - lead .. of it. The vectors at either end may reach past the row;
 // those are read element by element, -infinity outside. A NaN becomes -infinity.
@@ -149,12 +176,7 @@ struct Row {
   __device__ __forceinline__ uint4 load(int v) const {
     const int i0 = v * Vec<T>::kLen - lead;
     if (i0 >= 0 && i0 + Vec<T>::kLen <= n) return vec_max<T>(*reinterpret_cast<const uint4*>(p + i0), vec_none<T>());
-    uint4 r = vec_none<T>();
-    T* e = reinterpret_cast<T*>(&r);
-#pragma unroll
-    for (int i = 0; i < Vec<T>::kLen; ++i)
-      if (i0 + i >= 0 && i0 + i < n) e[i] = p[i0 + i];
-    return vec_max<T>(r, vec_none<T>());
+    return vec_max<T>(load_edge(p, i0, n), vec_none<T>());
   }
 };
 
@@ -444,11 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         best = vec_max<T>(best, raw[i]);
       }
     }
+#pragma unroll 1
     for (; v < f1; v += 32) {
       const uint4 raw = vec_max<T>(src[v], vec_none<T>());
       if constexpr (HELD) held[v - c0] = raw;
       best = vec_max<T>(best, raw);
     }
+#pragma unroll 1
     for (int e = lane; e < 2; e += 32) {
       const int w = e == 0 ? v0 : v1 - 1;
       if (v0 >= v1 || (e == 1 && w == v0) || (w >= f0 && w < f1)) continue;
@@ -474,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // The best index alone: the first one at the largest score.
   if (q.k == 1) {
     u64 first = 0;
+#pragma unroll 1
     for (int v = v0 + lane; v < v1; v += 32) {
       float x[E];
       Vec<T>::unpack(get(v), x);
@@ -489,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     return;
   }
 
-  // f(scores, their z, vector) for this warp's vectors, some loads under way a
+  // f(the scores' z, vector) for this warp's vectors, some loads under way a
   // lane; after at most kFlush vectors g(number of scores since the last one).
   auto each = [&](auto&& f, auto&& g) {
     auto one = [&](const uint4& raw, int v) {
@@ -505,9 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         z[i] = low2(z2);
         z[i + 1] = high2(z2);
       }
-      f(x, z, v);
+      f(z, v);
     };
-    constexpr int kBatch = HELD ? 2 : 4;
+    constexpr int kBatch = HELD ? 1 : 4;
     int v = v0 + lane, since = 0;
     for (; v + 32 * (kBatch - 1) < v1; v += 32 * kBatch) {
       uint4 raw[kBatch];
@@ -522,21 +547,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
     g(static_cast<unsigned>(since * E));
     since = 0;
+#pragma unroll 1
     for (; v < v1; v += 32, ++since) one(get(v), v);
     g(static_cast<unsigned>(since * E));
   };
-  // The key of a score that `each` hands out.
-  auto key_of = [&](float x, int v, int i) {
-    return make_key(sc.inf && x == 0.0f ? INFINITY : x, static_cast<uint32_t>(index_of(v, i)));
-  };
-  // One score, read again.
+  // One score, read again (its index is one of the row's).
   auto score_at = [&](int v, int i) -> float {
-    T e;
     if constexpr (HELD)
-      e = reinterpret_cast<const T*>(held + (v - c0))[i];
+      return Vec<T>::one(reinterpret_cast<const T*>(held + (v - c0))[i]);
     else
-      e = row.p[index_of(v, i)];
-    return Vec<T>::one(e);
+      return fmaxf(Vec<T>::one(row.p[index_of(v, i)]), -INFINITY);
+  };
+  // f(score, key) for this warp's scores, one at a time: for the passes that few
+  // rows take, in a twentieth of the code.
+  auto each_one = [&](auto&& f) {
+#pragma unroll 1
+    for (int v = v0 + lane; v < v1; v += 32) {
+#pragma unroll 1
+      for (int i = 0; i < E; ++i) {
+        const int index = index_of(v, i);
+        if (index < 0 || index >= row.n) continue;
+        const float x = score_at(v, i);
+        f(x, make_key(x, static_cast<uint32_t>(index)));
+      }
+    }
   };
   // Put the scores of a vector that `mask` names into this CTA's list.
   auto append = [&](unsigned mask, int v) {
@@ -546,15 +580,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       const int i = __ffs(static_cast<int>(mask)) - 1;
       if (at < kCap) list[at] = make_key(score_at(v, i), static_cast<uint32_t>(index_of(v, i)));
     }
-  };
-  // Clear the bits of the scores whose keys are under `cut`.
-  auto only_kept = [&](unsigned mask, const float (&x)[E], int v, u64 cut) {
-    if (cut != 0 && mask != 0) {
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if ((mask >> i & 1u) && key_of(x[i], v, i) < cut) mask &= ~(1u << i);
-    }
-    return mask;
   };
   // Sum over CTA 0's threads of a value each, for all of them; `t` names one of three words a warp.
   auto block_sum = [&](u64 v, int t) {
@@ -575,10 +600,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   u64 cut = 0;           // keys from here on are kept
   bool summed = false;   // s.kept has the warps' kept sums
 
-  // Kept weight of a score, once the cut is known.
-  auto kept = [&](float x, int index) -> u64 {
-    const float e = ex2(sc.z(x));
+  // Kept weight of a score, once the cut is known, and of a vector's scores.
+  auto kept = [&](int v, int i) -> u64 {
+    const int index = index_of(v, i);
+    if (index < 0 || index >= row.n) return 0;
+    const float x = score_at(v, i), e = ex2(sc.z(x));
     return e >= q.min_p && make_key(x, static_cast<uint32_t>(index)) >= cut ? fixed(e) : 0ull;
+  };
+  auto kept_of = [&](int v) {
+    u64 sum = 0;
+#pragma unroll 2
+    for (int i = 0; i < E; ++i) sum += kept(v, i);
+    return sum;
   };
 
   // Counts of the scores by position, and where a prefix ends that has `target`
@@ -591,11 +624,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // prefix are the sum less those of the rest, and near top_p = 1 that rest is
   // small, and so is its error.
   auto clear_counts = [&]() {
+#pragma unroll 1
     for (int i = threadIdx.x; i < kQuads; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x == 0) s.list_len = 0;
     __syncthreads();
   };
-  auto decide = [&](const Bracket& br, bool for_k, u64 mine, u64& sum_all, u64& above, u64 count_above, u64& target) {
+  auto decide = [&](const Bracket& br, bool for_k, u64 mine, u64 sum_k, u64& sum_all, u64& above, u64 count_above, u64& target) {
     cta.sync();  // all counts are there
     const int per = (kQuads + static_cast<int>(cta.size) * kThreads - 1) / (static_cast<int>(cta.size) * kThreads);  // a thread's
     const int q0 = (static_cast<int>(cta.rank) * kThreads + static_cast<int>(threadIdx.x)) * per;
@@ -603,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     // The cluster's counts of four positions, eight CTAs' loads under way at once.
     auto count = [&](int quad) {
       uint4 c = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
       for (uint32_t o0 = 0; o0 < cta.size; o0 += 8) {
         uint4 got[8];
 #pragma unroll
@@ -629,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     const float step = br.step(), ratio = exp2f(step), low0 = exp2f(br.edge(b0)), high0 = exp2f(br.edge(b0) - step);
     float low = low0, high = high0;
     uint4 c4 = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
     for (int quad = q0; quad < q1; ++quad) {
       c4 = count(quad);
       const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
@@ -690,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       above = all_m;
     } else {
       sum_all = all_m;
-      target = share(sum_all, q.part_p);
+      target = share(sum_k ? sum_k : sum_all, q.part_p);
     }
     const u64 sum = for_k || br.fine ? 0 : sum_all;
     fl += above;
@@ -709,7 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       high = high0;
       float rl = 0.0f, ru = 0.0f;
       long long at_l = start_l, at_u = start_u;
-      for (int quad = q0; quad < q1; ++quad) {
+  #pragma unroll 1
+    for (int quad = q0; quad < q1; ++quad) {
         if (q1 - q0 > 1) c4 = count(quad);
         const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
@@ -755,8 +792,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // they are not all there). `sum`, a value of each thread, becomes the row's.
   auto merge_lists = [&](u64& sum) -> u64 {
     sum = block_sum(sum, 0);
-    if (cta.size == 1) return s.list_len;
     const unsigned mine = s.list_len;
+    if (cta.size == 1) {
+      __syncthreads();  // the next pass may set it back
+      return mine;
+    }
     if (threadIdx.x < cta.size) {
       remote_store(remote(&s.words[0][cta.rank], threadIdx.x), mine);
       remote_store(remote(&s.words[1][cta.rank], threadIdx.x), sum);
@@ -764,11 +804,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     cta.sync();
     sum = warp_sum(lane < static_cast<int>(cta.size) ? s.words[1][lane] : 0ull);
     u64 all = 0, at = 0;
+#pragma unroll 1
     for (uint32_t o = 0; o < cta.size; ++o) {
       if (o < cta.rank) at += s.words[0][o];
       all += s.words[0][o];
     }
     if (cta.rank != 0 && all <= kCap)
+#pragma unroll 1
       for (unsigned i = threadIdx.x; i < mine; i += kThreads) remote_store(remote(&list[at + i], 0), list[i]);
     cta.sync();
     return all;
@@ -842,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     const u64 index_mask = (u64(1) << index_bits) - 1;
     auto short_key = [&](u64 key) { return (key >> (32 + kSame)) << index_bits | (key & index_mask); };
     u64 lo = ~0ull, hi = 0;
+#pragma unroll 1
     for (int j = threadIdx.x; j < len; j += kThreads) {
       const u64 k = short_key(list[j]);
       lo = umin64(lo, k);
@@ -867,6 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       const int shift = max(0, width - 8);  // kSmall = 2^8 buckets
       if (threadIdx.x < kSmall) s.small_w[threadIdx.x] = 0;
       __syncthreads();
+#pragma unroll 1
       for (int j = threadIdx.x; j < len; j += kThreads) {
         const u64 key = list[j], k = short_key(key);
         if (k >= lo && k <= hi) atomicAdd(&s.small_w[(k - lo) >> shift], for_k ? 1ull : weight(key_score(key), sc));
@@ -892,74 +936,112 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       hi = umin64(hi, lo + ((u64(1) << shift) - 1));
       if (shift == 0) break;
     }
+#pragma unroll 1
     for (int j = threadIdx.x; j < len; j += kThreads)
       if (short_key(list[j]) == lo) s.small_key[2] = list[j];
     __syncthreads();
     return s.small_key[2];
   };
 
-  if (by_k) {
+  // In CTA 0: the weight of the list's keys from `first` on.
+  auto list_sum = [&](int len, u64 first) {
+    u64 sum = 0;
+#pragma unroll 1
+    for (int j = threadIdx.x; j < len; j += kThreads)
+      if (list[j] >= first) sum += weight(key_score(list[j]), sc);
+    return block_sum(sum, 2);
+  };
+  // The warps' kept sums: what is ahead of a listed part of the scores (s.kept
+  // has it), and this CTA's keys of the list (its first ones, in CTA 0's too).
+  auto sum_listed = [&]() {
+    const int own_len = static_cast<int>(s.list_len);
+    if (threadIdx.x < kWarps) s.add_lo[threadIdx.x] = s.add_hi[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int j = threadIdx.x; j < own_len; j += kThreads) {
+      const u64 key = list[j];
+      if (key < cut) continue;
+      const float e = ex2(sc.z(key_score(key)));
+      if (e < q.min_p) continue;
+      const u64 w = fixed(e);
+      const int v = (static_cast<int>(key_index(key)) + row.lead) / E;
+      int o = static_cast<int>(int64_t(v - c0) * kWarps / (c1 - c0));
+      while (v >= part_of(c0, c1, o + 1)) ++o;  // the division may round down across a part's start
+      atomicAdd(&s.add_lo[o], static_cast<unsigned>(w & 0x7FFFFu));  // 2^13 of them stay under 2^32
+      atomicAdd(&s.add_hi[o], static_cast<unsigned>(w >> 19));
+    }
+    __syncthreads();
+    if (threadIdx.x < kWarps) s.kept[threadIdx.x] += (static_cast<u64>(s.add_hi[threadIdx.x]) << 19) + s.add_lo[threadIdx.x];
+    summed = true;
+  };
+
+  if (by_k && static_cast<u64>(q.k) <= static_cast<u64>(cta.size) * kThreads / 2) {
     // ----------------------------------------------- 3. the k best, in a list
-    u64 n = kCap + 1;
-    if (static_cast<u64>(q.k) <= static_cast<u64>(cta.size) * kThreads / 2) {
-      Bracket br;
-      clear_counts();
-      const float z = sc.z(x0[0]), y = Bracket::pattern(z);
-      const int at = br.at(z, y);
-      if (at < kBins) atomicAdd(&hist[at], 1u);
-      u64 none = 0, goal = 0;
-      decide(br, true, 0, none, none, 0, goal);
-      if (s.say[4] >= static_cast<u64>(q.k)) {
-        // Every score down to the bin of the k-th largest of the threads' largest.
-        const uint32_t last = static_cast<uint32_t>(s.say[1]) + Bracket::kPattern;
-        each(
-            [&](const float (&x)[E], const float (&z)[E], int v) {
-              uint32_t y[E], near = 0xFFFFFFFFu;
-#pragma unroll
-              for (int i = 0; i < E; ++i) {
-                y[i] = __float_as_uint(Bracket::pattern(z[i]));
-                near = min(near, y[i]);
-              }
-              if (near <= last) {  // few vectors hold any
-                unsigned mask = 0;
-#pragma unroll
-                for (int i = 0; i < E; ++i) mask |= (y[i] <= last ? 1u : 0u) << i;
-                append(mask, v);
-              }
-            },
-            [](unsigned) {});
-        n = merge_lists(none);
-      }
-    }
-    if (n <= kSmall) {
-      if (cta.rank == 0) finish_small(static_cast<int>(n), 0);
-      return;
-    }
-    if (n <= kCap) {
-      if (cta.rank == 0) {
-        const u64 key = list_cut(static_cast<int>(n), true, 0, static_cast<u64>(q.k));
-        if (threadIdx.x == 0) s.say[6] = key;
-      }
-      tell(6, 7);
-      cut = s.say[6];
-    }
-  }
-  if (by_p || (by_k && cut == 0)) {
-    // -------------------------------------- bins, for a large top_k, then top_p
     Bracket br;
-    u64 above = 0;                      // sum of weights ahead of the finer bins
-    u64 count_above = 0;                // and number of scores
-    u64 sum_all = 0;                    // sum of what top_k kept
-    u64 target = 0;                     // number or weight at which the prefix ends
-    bool for_k = by_k && cut == 0;      // which of the two ends is looked for
+    clear_counts();
+    const float z = sc.z(x0[0]), y = Bracket::pattern(z);
+    const int at = br.at(z, y);
+    if (at < kBins) atomicAdd(&hist[at], 1u);
+    u64 none = 0, goal = 0;
+    decide(br, true, 0, 0, none, none, 0, goal);
+    if (s.say[4] >= static_cast<u64>(q.k)) {
+      // Every score down to the bin of the k-th largest of the threads' largest.
+      const uint32_t last = static_cast<uint32_t>(s.say[1]) + Bracket::kPattern;
+      each(
+          [&](const float (&z)[E], int v) {
+            uint32_t y[E], near = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              y[i] = __float_as_uint(Bracket::pattern(z[i]));
+              near = min(near, y[i]);
+            }
+            if (near <= last) {  // few vectors hold any
+              unsigned mask = 0;
+#pragma unroll
+              for (int i = 0; i < E; ++i) mask |= (y[i] <= last ? 1u : 0u) << i;
+              append(mask, v);
+            }
+          },
+          [](unsigned) {});
+      const u64 n = merge_lists(none);
+      if (n <= kSmall) {
+        if (cta.rank == 0) finish_small(static_cast<int>(n), 0);
+        return;
+      }
+      if (n <= kCap) {
+        if (cta.rank == 0) {
+          const int len = static_cast<int>(n);
+          u64 key = list_cut(len, true, 0, static_cast<u64>(q.k));
+          if (by_p) {  // a share of the list's keys from there on
+            key = umax64(key, list_cut(len, false, 0, share(list_sum(len, key), q.part_p)));
+          }
+          if (threadIdx.x == 0) s.say[6] = key;
+        }
+        tell(6, 7);
+        cut = s.say[6];
+        if (lane == 0) s.kept[cta.warp] = 0;
+        sum_listed();
+      }
+    }
+    cta.sync();  // what was said has been read
+  }
+  if ((by_k || by_p) && !summed) {
+    // --------------------------------- bins, for a large top_k, then top_p
+    Bracket br;
+    u64 above = 0;         // sum of weights ahead of the bins in question
+    u64 count_above = 0;   // number of scores ahead of the finer bins
+    u64 sum_k = 0;         // sum of what top_k kept, if not all
+    u64 sum_all = 0;       // sum of all
+    u64 target = 0;        // number or weight at which the prefix ends
+    bool for_k = by_k;     // which of the two ends is looked for
     for (;;) {
       clear_counts();
-      const bool sum_it = !for_k;
       Mass m;
-      if (!br.fine && cut == 0) {
+      u64 sum = 0;
+      if (!br.fine) {
         const uint32_t counts = smem_addr(hist) - Bracket::kPattern * 4u;  // a pattern's count, modulo 2^32
         each(
-            [&](const float (&)[E], const float (&z)[E], int) {
+            [&](const float (&z)[E], int) {
 #pragma unroll
               for (int i = 0; i < E; ++i) {
                 const uint32_t y = __float_as_uint(Bracket::pattern(z[i]));
@@ -970,38 +1052,33 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
                     "r"(y), "r"(Bracket::kPattern + kBins)
                     : "memory");
               }
-              if (sum_it) {
+              if (!for_k) {
 #pragma unroll
                 for (int i = 0; i < E; i += 2) m.add(ex2(z[i]), ex2(z[i + 1]));
               }
             },
-            [&](unsigned n) { if (sum_it) m.flush(n); });
+            [&](unsigned n) { if (!for_k) m.flush(n); });
+        sum = m.total;
       } else {
-        each(
-            [&](const float (&x)[E], const float (&z)[E], int v) {
-              const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
-#pragma unroll
-              for (int i = 0; i < E; i += 2) {
-                const int pa = br.at(z[i], Bracket::pattern(z[i])), pb = br.at(z[i + 1], Bracket::pattern(z[i + 1]));
-                const bool ka = in >> i & 1u, kb = in >> (i + 1) & 1u;
-                if (ka && pa >= 0 && pa < kBins) atomicAdd(&hist[pa], 1u);
-                if (kb && pb >= 0 && pb < kBins) atomicAdd(&hist[pb], 1u);
-                if (sum_it) m.add(ka && (!br.fine || pa < 0) ? ex2(z[i]) : 0.0f, kb && (!br.fine || pb < 0) ? ex2(z[i + 1]) : 0.0f);
-              }
-            },
-            [&](unsigned n) { if (sum_it) m.flush(n); });
+        each_one([&](float x, u64) {
+          const float z = sc.z(x);
+          const int at = br.at(z, Bracket::pattern(z));
+          if (at >= 0 && at < kBins) atomicAdd(&hist[at], 1u);
+          if (!for_k && at < 0) sum += fixed(ex2(z));
+        });
       }
-      decide(br, for_k, m.total, sum_all, above, count_above, target);
+      decide(br, for_k, sum, sum_k, sum_all, above, count_above, target);
+      const u64 reach = s.say[4];
+      const u64 ahead = s.say[2];
+      const u64 in = (s.say[3] == ~0ull ? reach : s.say[3]) - ahead;  // a lower bound need not get to the target
       br.from = static_cast<int>(s.say[0]);
       br.to = static_cast<int>(s.say[1]);
-      const u64 ahead = s.say[2], reach = s.say[4];
-      const u64 in = (s.say[3] == ~0ull ? reach : s.say[3]) - ahead;  // a lower bound need not get to the target
-      u64 last_key;
-      if (for_k && !br.fine && reach <= target) {
-        last_key = 0;  // everything that has a weight is among the top_k
-      } else {
+      u64 last_key = 0;  // 0: everything that has a weight is among the top_k
+      if (br.fine || !for_k || reach > target) {
         const bool small = !for_k && !br.fine && ahead + in <= kSmall;  // all that may be kept
-        if (!small && in > kCap && !br.fine) {
+        if (small) br.from = 0;
+        const bool listed = small || in <= kCap;
+        if (!listed && !br.fine) {
           // Divide the bins again.
           Bracket f;
           f.fine = true;
@@ -1011,18 +1088,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
           f.scale = static_cast<float>(kBins) * kBinsPerOctave / static_cast<float>(br.to - br.from + 1);
           br = f;
           count_above = ahead;
-          cta.sync();  // what CTA 0 said has been read
+          cta.sync();
           continue;
         }
-        if (small || in <= kCap) {
-          // ------------------------------------------------- 4. gather
-          const int from = small ? 0 : br.from;
-          Mass m2;
+        if (listed) {
+          // --------------------------------------------------- 4. gather
+          const bool weigh = !small;
+          u64 ahead_sum = 0;
           if (!br.fine) {
-            const uint32_t first = static_cast<uint32_t>(from) + Bracket::kPattern, width = static_cast<uint32_t>(br.to - from);
-            const bool weigh = !for_k && !small;
+            const uint32_t first = static_cast<uint32_t>(br.from) + Bracket::kPattern, width = static_cast<uint32_t>(br.to - br.from);
+            Mass m2;
             each(
-                [&](const float (&x)[E], const float (&z)[E], int v) {
+                [&](const float (&z)[E], int v) {
                   uint32_t d[E], near = 0xFFFFFFFFu;
 #pragma unroll
                   for (int i = 0; i < E; ++i) {
@@ -1038,102 +1115,80 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
                     unsigned mask = 0;
 #pragma unroll
                     for (int i = 0; i < E; ++i) mask |= (d[i] <= width ? 1u : 0u) << i;
-                    append(only_kept(mask, x, v, cut), v);
+                    append(mask, v);
                   }
                 },
                 [&](unsigned n) { if (weigh) m2.flush(n); });
+            ahead_sum = m2.total;
           } else {
-            each(
-                [&](const float (&x)[E], const float (&z)[E], int v) {
-                  unsigned mask = 0;
-#pragma unroll
-                  for (int i = 0; i < E; i += 2) {
-                    const int pa = br.at(z[i], Bracket::pattern(z[i])), pb = br.at(z[i + 1], Bracket::pattern(z[i + 1]));
-                    mask |= (pa >= from && pa <= br.to ? 1u : 0u) << i | (pb >= from && pb <= br.to ? 2u : 0u) << i;
-                    if (!for_k) m2.add(pa < from ? ex2(z[i]) : 0.0f, pb < from ? ex2(z[i + 1]) : 0.0f);
-                  }
-                  append(only_kept(mask, x, v, cut), v);
-                },
-                [&](unsigned n) { if (!for_k) m2.flush(n); });
+            each_one([&](float x, u64 key) {
+              const float z = sc.z(x);
+              const int at = br.at(z, Bracket::pattern(z));
+              if (at >= br.from && at <= br.to) {
+                const unsigned n = atomicAdd(&s.list_len, 1u);
+                if (n < kCap) list[n] = key;
+              }
+              if (weigh && at < br.from) ahead_sum += fixed(ex2(z));
+            });
           }
-          if (!for_k && !small) {
-            const u64 own = warp_sum(m2.total);
-            if (lane == 0) s.kept[cta.warp] = own;
-          }
-          u64 ahead_sum = m2.total;
-          const int len = static_cast<int>(merge_lists(ahead_sum));
+          const u64 own = warp_sum(ahead_sum);
+          if (lane == 0) s.kept[cta.warp] = own;
+          const u64 len = merge_lists(ahead_sum);
           above = ahead_sum;
           if (small) {
-            if (cta.rank == 0) finish_small(len, sum_all);
+            if (cta.rank == 0) finish_small(static_cast<int>(len), sum_k ? sum_k : sum_all);
             return;
           }
           if (cta.rank == 0) {
-            const u64 key = list_cut(len, for_k, for_k ? ahead : above, target);
-            if (threadIdx.x == 0) s.say[6] = key;
-          }
-          tell(6, 7);
-          last_key = s.say[6];
-          if (!for_k && q.min_p == 0.0f) {
-            // The warps' kept sums: the weights ahead of the bins, and this
-            // CTA's keys of the list (its first ones, in CTA 0's too).
-            summed = true;
-            const int own_len = static_cast<int>(s.list_len);
-            if (threadIdx.x < kWarps) s.add_lo[threadIdx.x] = s.add_hi[threadIdx.x] = 0;
-            __syncthreads();
-            for (int j = threadIdx.x; j < own_len; j += kThreads) {
-              const u64 key = list[j];
-              if (key < last_key) continue;
-              const u64 w = weight(key_score(key), sc);
-              const int v = (static_cast<int>(key_index(key)) + row.lead) / E;
-              int o = static_cast<int>(int64_t(v - c0) * kWarps / (c1 - c0));
-              while (v >= part_of(c0, c1, o + 1)) ++o;  // the division may round down across a part's start
-              atomicAdd(&s.add_lo[o], static_cast<unsigned>(w & 0x7FFFFu));  // 2^13 of them stay under 2^32
-              atomicAdd(&s.add_hi[o], static_cast<unsigned>(w >> 19));
+            const u64 key = list_cut(static_cast<int>(len), for_k, for_k ? ahead : above, target);
+            const u64 in_list = for_k && by_p ? list_sum(static_cast<int>(len), key) : 0;
+            if (threadIdx.x == 0) {
+              s.say[5] = in_list;
+              s.say[6] = key;
             }
-            __syncthreads();
-            if (threadIdx.x < kWarps)
-              s.kept[threadIdx.x] += (static_cast<u64>(s.add_hi[threadIdx.x]) << 19) + s.add_lo[threadIdx.x];
+          }
+          tell(5, 7);
+          last_key = s.say[6];
+          sum_k = above + s.say[5];
+          if (!(for_k && by_p) && q.min_p == 0.0f) {
+            cut = last_key;
+            sum_listed();
           }
         } else {
           // Equal scores by the thousand: halve the interval between the
           // smallest and the largest key of the finer bins.
           u64 lo = 0, hi = 0;  // the complement of the smallest; the largest
-          each(
-              [&](const float (&x)[E], const float (&z)[E], int v) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                  const int at = br.at(z[i], Bracket::pattern(z[i]));
-                  const u64 key = key_of(x[i], v, i);
-                  if (at >= br.from && at <= br.to && key >= cut) {
-                    lo = umax64(lo, ~key);
-                    hi = umax64(hi, key);
-                  }
-                }
-              },
-              [](unsigned) {});
+          each_one([&](float x, u64 key) {
+            const float z = sc.z(x);
+            const int at = br.at(z, Bracket::pattern(z));
+            if (at >= br.from && at <= br.to) {
+              lo = umax64(lo, ~key);
+              hi = umax64(hi, key);
+            }
+          });
           lo = ~cta.template reduce<true>(lo);
           hi = cta.template reduce<true>(hi) + 1;
           while (hi - lo > 1) {
             const u64 mid = lo + (hi - lo) / 2;
             u64 c = 0;
-            for (int v = v0 + lane; v < v1; v += 32) {
-              float x[E];
-              Vec<T>::unpack(get(v), x);
-#pragma unroll
-              for (int i = 0; i < E; ++i)
-                if (make_key(x[i], static_cast<uint32_t>(index_of(v, i))) >= mid) c += for_k ? 1ull : weight(x[i], sc);
-            }
-            if (cta.reduce<false>(c) >= target)
+            each_one([&](float x, u64 key) {
+              if (key >= mid) c += for_k ? 1ull : weight(x, sc);
+            });
+            if (cta.template reduce<false>(c) >= target)
               lo = mid;
             else
               hi = mid;
           }
           last_key = lo;
+          if (for_k && by_p) {
+            each_one([&](float x, u64 key) { sum_k += key >= lo ? weight(x, sc) : 0ull; });
+            sum_k = cta.template reduce<false>(sum_k);
+          }
         }
       }
-      cut = last_key;
+      cut = umax64(cut, last_key);
       if (!for_k || !by_p) break;
-      // Now top_p, among what top_k kept.
+      // Now top_p, of the weight that top_k kept: it ends no later.
       for_k = false;
       above = 0;
       count_above = 0;
@@ -1144,24 +1199,28 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
 
   // ------------------------------------------------- the warps' kept sums
   if (!summed) {
-    Mass m;
-    each(
-        [&](const float (&x)[E], const float (&z)[E], int v) {
-          const unsigned in = only_kept((1u << E) - 1u, x, v, cut);
-          if (cut == 0 && q.min_p == 0.0f) {
-#pragma unroll
-            for (int i = 0; i < E; i += 2) m.add(ex2(z[i]), ex2(z[i + 1]));
-          } else {
+    u64 sum = 0;
+    if (cut == 0) {
+      Mass m;
+      each(
+          [&](const float (&z)[E], int) {
+            const float least = q.min_p;
 #pragma unroll
             for (int i = 0; i < E; i += 2) {
               const float ea = ex2(z[i]), eb = ex2(z[i + 1]);
-              m.add((in >> i & 1u) && ea >= q.min_p ? ea : 0.0f, (in >> (i + 1) & 1u) && eb >= q.min_p ? eb : 0.0f);
+              m.add(ea >= least ? ea : 0.0f, eb >= least ? eb : 0.0f);
             }
-          }
-        },
-        [&](unsigned n) { m.flush(n); });
-    const u64 own = warp_sum(m.total);
-    if (lane == 0) s.kept[cta.warp] = own;
+          },
+          [&](unsigned n) { m.flush(n); });
+      sum = m.total;
+    } else {
+      each_one([&](float x, u64 key) {
+        const float e = ex2(sc.z(x));
+        if (key >= cut && e >= q.min_p) sum += fixed(e);
+      });
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) s.kept[cta.warp] = sum;
   }
   __syncthreads();
   const u64 total = cta.reduce<false>(lane == 0 ? s.kept[cta.warp] : 0ull);
@@ -1169,6 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   u64 before = 0;
   u64 mine_all = total;
   if (cta.size > 1) {
+#pragma unroll 1
     for (uint32_t c = 0; c < cta.rank; ++c) before += s.slot[cta.turn ^ 1][c];
     mine_all = s.slot[cta.turn ^ 1][cta.rank];
   }
@@ -1197,12 +1257,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     if (n1 - n0 <= 32) break;
     u64 part = 0;
     const int m1 = part_of(n0, n1, cta.warp + 1);
-    for (int v = part_of(n0, n1, cta.warp) + lane; v < m1; v += 32) {
-      float x[E];
-      Vec<T>::unpack(get(v), x);
-#pragma unroll
-      for (int i = 0; i < E; ++i) part += kept(x[i], index_of(v, i));
-    }
+#pragma unroll 1
+    for (int v = part_of(n0, n1, cta.warp) + lane; v < m1; v += 32) part += kept_of(v);
     part = warp_sum(part);
     if (lane == 0) s.kept[cta.warp] = part;
     __syncthreads();
@@ -1210,26 +1266,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   __syncthreads();
   if (cta.warp == 0) {
     const int v = s.lo + lane;
-    u64 mine[E];
-    u64 sum = 0;
-    if (v < s.hi) {
-      float x[E];
-      Vec<T>::unpack(get(v), x);
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        mine[i] = kept(x[i], index_of(v, i));
-        sum += mine[i];
-      }
-    }
+    const u64 sum = v < s.hi ? kept_of(v) : 0ull;
     u64 run = s.before + warp_scan(sum, lane) - sum;
     if (sum > 0 && run <= aim && aim < run + sum) {
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < E; ++i) {
-        if (run <= aim && aim < run + mine[i]) {
+        const u64 w = kept(v, i);
+        if (run <= aim && aim < run + w) {
           a.token[r] = index_of(v, i);
-          if (a.logprob) a.logprob[r] = log_share(mine[i], total);
+          if (a.logprob) a.logprob[r] = log_share(w, total);
         }
-        run += mine[i];
+        run += w;
       }
     }
   }
@@ -1270,7 +1317,8 @@ cudaError_t launch_rows(const SampleLaunch& a, cudaStream_t st) {
   if (held <= kMaxHeld) return launch_t<T, true, 256>(a, cluster, static_cast<int>(held), st);
   // Longer parts are read again from L2, with two CTAs an SM: a cluster of 16
   // CTAs that fill an SM each finds room in few of the GPU's clusters of SMs (8
-  // rows of 1M: 28 us, 37 with 1,024 threads a CTA and half of the rows waiting).
+  // rows of 1M with min_p: 28 us against 37 with 1,024 threads a CTA, half of
+  // the rows waiting; 25 since the text is shorter).
   return launch_t<T, false, 512>(a, cluster, 0, st);
 }
 
