@@ -37,38 +37,47 @@ struct Out {
   float* scale;
 };
 
-// One CTA per row, any strides, alignments and lengths: two reads of the row,
-// the second from cache.
-template <typename T>
+// Any strides, alignments and lengths, THREADS threads a row: two reads of it,
+// the second from cache. 200,000 x 65 bf16: 205 us with a CTA a row, 35 with a
+// warp; 100,000 x 333: 131 and 33. 30,000 x 2,500 (rows on 8-byte boundaries):
+// 84 us, 82 with a row's values kept in registers, which leaves fewer CTAs an
+// SM and costs longer and shorter rows a quarter.
+template <typename T, int THREADS>
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_rows_any_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, const Out o) {
   pdl_launch_dependents();  // a product may become resident now; it waits for these rows
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+  constexpr int kRows = kQuantThreads / THREADS;
+  const int t = threadIdx.x % THREADS;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / THREADS; r < rows; r += static_cast<int64_t>(gridDim.x) * kRows) {
     const T* row = x + r * ld_x;
     uint32_t top = 0;
-    for (int j = threadIdx.x; j < cols; j += kQuantThreads)
-      top = max(top, __float_as_uint(to_f32(row[j])) & 0x7FFFFFFFu);
-    const RowScale s = row_scale(block_max(top));
+    for (int j = t; j < cols; j += THREADS) top = max(top, __float_as_uint(to_f32(row[j])) & 0x7FFFFFFFu);
+    const RowScale s = row_scale(THREADS == 32 ? __reduce_max_sync(kFullMask, top) : block_max(top));
     if (o.f16) {
-      for (int j = threadIdx.x; j < o.pitch; j += kQuantThreads)
+      for (int j = t; j < o.pitch; j += THREADS)
         o.f16[r * o.pitch + j] = __float2half_rn(j < cols ? quantize_sum(to_f32(row[j]), s) - kRounder : 0.0f);
-      if (threadIdx.x == 0) atomicMax(o.block_l1, 128u * 127u);  // the bound of any row: not worth a reduction here
+      if (t == 0) atomicMax(o.block_l1, 128u * 127u);  // the bound of any row: not worth a reduction here
     } else {
-      for (int j = threadIdx.x; j < cols; j += kQuantThreads)
+      for (int j = t; j < cols; j += THREADS)
         o.q[r * o.ld_q + j] = static_cast<int8_t>(__float_as_uint(quantize_sum(to_f32(row[j]), s)));
     }
-    if (threadIdx.x == 0) o.scale[r] = s.scale;
-    __syncthreads();  // block_max's shared words are used again
+    if (t == 0) o.scale[r] = s.scale;
+    if (THREADS > 32) __syncthreads();  // block_max's shared words are used again
   }
 }
 
 // THREADS threads a row (a warp up to 1,024 values, else the CTA up to 8,192),
 // which stays in registers: one read of it and one write, eight values a
 // thread at a time. Rows start on 16-byte boundaries, int8 rows on 8-byte ones.
+// Bound by memory once a value costs about five instructions (the magnitudes
+// are compared as T's own patterns, two a word): 16,384 x 8,192 bf16 59.8 us =
+// 6.73 TB/s, 0.99 of the copy rate (87.7 with fourteen instructions a value);
+// 200,000 x 1,024 89; 200,000 x 768 fp32 113; 65,536 x 4,096 bf16 131 (139 with
+// six CTAs an SM, the eight need 32 registers).
 constexpr int kHeld = 4;  // groups of eight values a thread holds
 
 template <typename T, int THREADS, bool F16>
-__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 && THREADS > 32 ? 6 : 1)
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 && THREADS > 32 ? 8 : 1)
     quantize_rows_held_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, const Out o) {
   pdl_launch_dependents();
   constexpr int kRows = kQuantThreads / THREADS;
@@ -81,14 +90,22 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 && THREADS > 32 
 #pragma unroll
   for (int g = 0; g < kHeld; ++g) {
     const int c = (g * THREADS + t) * 8;
+    v[g].clear();
     if (c < cols) v[g].load(row + c, cols - c);
   }
 #pragma unroll
-  for (int g = 0; g < kHeld; ++g)
-    if ((g * THREADS + t) * 8 < cols)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[g][i]) & 0x7FFFFFFFu);
+  for (int g = 0; g < kHeld; ++g) top = v[g].top(top);
+  top = Eight<T>::code(top);
   const RowScale s = row_scale(THREADS == 32 ? __reduce_max_sync(kFullMask, top) : block_max(top));
+  if (s.pre != 1.0f) {  // few rows: the values are scaled up, or the row has none (inv is 0) and they are zeros
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g) {
+      if (s.inv == 0.0f)
+        v[g].clear();
+      else
+        v[g].scale_by(s.pre);
+    }
+  }
   if (t == 0) o.scale[r] = s.scale;
   const int end = F16 ? o.pitch : cols;
   float l1_top = 0.0f;
@@ -98,17 +115,18 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 && THREADS > 32 
     if (c >= end) break;  // whole groups of 16 threads: the pitch is a multiple of 128
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = c < cols ? quantize_sum(v[g][i], s) : kRounder;
+    for (int i = 0; i < 8; ++i) q[i] = __fadd_rn(__fmul_rn(v[g][i], s.inv), kRounder);
     if constexpr (F16) {
       __half2 h[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        h[i] = __floats2half2_rn(__fsub_rn(q[2 * i], kRounder), __fsub_rn(q[2 * i + 1], kRounder));
-      *reinterpret_cast<uint4*>(o.f16 + r * o.pitch + c) = *reinterpret_cast<const uint4*>(h);
-      // 16 threads hold the 128 values of a stage.
       float l1 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) l1 += fabsf(q[i] - kRounder);
+      for (int i = 0; i < 4; ++i) {
+        const float lo = __fsub_rn(q[2 * i], kRounder), hi = __fsub_rn(q[2 * i + 1], kRounder);
+        h[i] = __floats2half2_rn(lo, hi);
+        l1 += fabsf(lo) + fabsf(hi);
+      }
+      *reinterpret_cast<uint4*>(o.f16 + r * o.pitch + c) = *reinterpret_cast<const uint4*>(h);
+      // 16 threads hold the 128 values of a stage.
       const unsigned half = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) l1 += __shfl_xor_sync(half, l1, d);
@@ -150,9 +168,12 @@ cudaError_t launch_t(const QuantizeLaunch& a, cudaStream_t st) {
     quantize_rows_held_kernel<T, 32, F16><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
   } else if (aligned && width <= kQuantThreads * 8 * kHeld) {
     quantize_rows_held_kernel<T, kQuantThreads, F16><<<static_cast<unsigned>(a.rows), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
+  } else if (width <= 32 * 8 * kHeld) {
+    const int64_t grid = std::min<int64_t>((a.rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32), int64_t(1) << 20);
+    quantize_rows_any_kernel<T, 32><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
   } else {
     const int64_t grid = std::min<int64_t>(a.rows, int64_t(1) << 20);
-    quantize_rows_any_kernel<T><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
+    quantize_rows_any_kernel<T, kQuantThreads><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
   }
   return cudaGetLastError();
 }

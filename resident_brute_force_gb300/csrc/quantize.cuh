@@ -12,6 +12,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace rbf {
 
@@ -72,15 +73,43 @@ struct Eight {
 #pragma unroll
       for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
     } else {
-#pragma unroll
-      for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      clear();
       T* e = reinterpret_cast<T*>(raw);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < live) e[i] = p[i];
     }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // Words 0 .. 2 sizeof(T) - 1 as they are in memory.
+  __device__ __forceinline__ uint32_t& word(int i) { return reinterpret_cast<uint32_t*>(raw)[i]; }
   __device__ __forceinline__ float operator[](int i) const { return to_f32(reinterpret_cast<const T*>(raw)[i]); }
+  // The largest magnitude so far as T's own pattern (16-bit types: in each
+  // half), and that as the fp32 pattern that row_scale takes.
+  __device__ __forceinline__ uint32_t top(uint32_t t) {
+#pragma unroll
+    for (unsigned i = 0; i < 2 * sizeof(T); ++i)
+      t = sizeof(T) == 4 ? max(t, word(i) & 0x7FFFFFFFu) : __vmaxu2(t, word(i) & 0x7FFF7FFFu);
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t code(uint32_t t) {
+    if constexpr (sizeof(T) == 4) return t;
+    const uint32_t one = max(t >> 16, t & 0xFFFFu);
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) return one << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(one))));
+  }
+  // The values times `pre`, a power of two that leaves them within T (exact).
+  __device__ __forceinline__ void scale_by(float pre) {
+    T* e = reinterpret_cast<T*>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) e[i] *= pre;
+      if constexpr (std::is_same_v<T, __nv_bfloat16>) e[i] = __float2bfloat16_rn(__bfloat162float(e[i]) * pre);
+    }
+  }
 };
 
 }  // namespace rbf
