@@ -21,7 +21,8 @@
  *     they enqueue work and return; a tensor that another stream has written or
  *     will reuse is ordered by the caller. One handle serves one call at a time.
  *   - The handle owns its workspace, allocated in rbf_ops_create; a call
- *     allocates nothing.
+ *     allocates nothing. Calls may be captured in a graph; its replays use the
+ *     same workspace and are ordered with the handle's other calls by the caller.
  *   - Outputs do not overlap inputs.
  *   - An empty call (zero rows or columns of output) does nothing: RBF_OK.
  */

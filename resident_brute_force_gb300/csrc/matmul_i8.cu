@@ -44,7 +44,9 @@ __device__ __forceinline__ void store_out(const Epilogue& e, int64_t i, int64_t 
 // --------------------------------------------------- any strides, dp4a
 //
 // A 64 x 64 tile a CTA of 256 threads, 4 x 4 sums a thread, 64 values of
-// depth a step through shared memory, four products an instruction (dp4a).
+// depth a step through shared memory, four products an instruction (dp4a). For
+// operands that no tensor map can describe (b off 16-byte boundaries) and for a
+// depth of zero: bound by the dp4a rate and by the loads' instructions.
 
 constexpr int kAnyTile = 64;
 constexpr int kAnyWords = 16;  // 4-byte words of one row and step

@@ -29,7 +29,9 @@ struct rbf_ops {
   float* row_scale = nullptr;    // linear_i8_dev: the rows' scales
   int* partial = nullptr;        // the product's partial sums of shared tiles
   unsigned* arrived = nullptr;   // and their counters
-  unsigned* block_l1 = nullptr;  // two words, used by turns: a product clears the next one's
+  // Two words, used by turns: a product clears the next one's. A replayed graph
+  // uses one of them out of turn; what it then finds is a larger bound, no smaller one.
+  unsigned* block_l1 = nullptr;
   int turn = 0;
   int* errw = nullptr;           // error bits of the kernels since the last check
   uint64_t timeout_ns = 2000000000ull;  // bound on every device-side wait

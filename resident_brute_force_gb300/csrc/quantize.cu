@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kQuantThreads)
 // THREADS threads a row (a warp up to 1,024 values, else the CTA up to 8,192),
 // which stays in registers: one read of it and one write, eight values a
 // thread at a time. Rows start on 16-byte boundaries, int8 rows on 8-byte ones.
-// Bound by memory once a value costs about five instructions (the magnitudes
-// are compared as T's own patterns, two a word): 16,384 x 8,192 bf16 59.8 us =
+// Bound by memory now that a value costs ten instructions (the magnitudes are
+// compared as T's own patterns, two a word): 16,384 x 8,192 bf16 59.8 us =
 // 6.73 TB/s, 0.99 of the copy rate (87.7 with fourteen instructions a value);
 // 200,000 x 1,024 89; 200,000 x 768 fp32 113; 65,536 x 4,096 bf16 131 (139 with
 // six CTAs an SM, the eight need 32 registers).

@@ -41,9 +41,10 @@
 // bins; scores that coincide by the thousand (no bins divide them) leave K to
 // be found by halving the interval of keys, one pass over the row a step.
 //
-// What bounds it: the instructions of the passes over scores that are on chip
-// (conversion, scaling, bin and weight are some eight instructions a score),
-// the shared-memory atomics of the counts (11 to 14 lanes a clock and SM), and
+// What bounds it: instructions (256 x 128,000 top_p: 73 a score, of which the
+// passes over scores that are on chip are about half, the rest the fixed part
+// of a CTA), the shared-memory atomics of the counts (11 to 14 lanes a clock
+// and SM), and
 // per row some ten exchanges across the cluster at 450 clocks each. The text
 // counts too: the kernel is 150 to 177 KB, more than the instruction cache, and
 // passes that few rows take are loops over single scores (with every loop
