@@ -54,7 +54,7 @@ typedef enum rbf_dtype {
  * values (1 .. 2^20 and 1 .. RBF_OPS_MAX_DEPTH; max_rows counts the rows of
  * the first operand, the queries or tokens; the second operand's rows are not
  * limited). Its workspace is max_rows x max_depth 16-bit numbers, and up to
- * 40 MB for partial sums.
+ * 40 MB for partial sums and 32 MB for rows that are put on 16-byte boundaries.
  *   cuda_stream  stream of every call (NULL: the handle creates its own;
  *                cudaStreamLegacy names the default stream)
  * Errors: INVALID_VALUE, OUT_OF_MEMORY, CUDA. */

@@ -114,6 +114,7 @@ struct Params {
   int split;         // 1: equal shares of all stages, 0: whole tiles
   int tma_out;       // 1: 16-bit results may be stored by TMA
   int read_once;     // 1: the channels are read once (one token tile)
+  int wait_channels; // 1: the kernel before this one writes them
   const unsigned* block_l1;  // the largest sum of |a| over a token's 128 values of a stage
   unsigned* block_l1_next;   // the next launch's, to be zero for it
   int* partial;      // split: two tiles of partial sums per CTA
@@ -496,9 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------- channels (bytes)
-    // They are never written by the kernel launched just before this one, so
-    // their loads start while that one still runs.
+    // Where the kernel launched just before this one does not write them, their
+    // loads start while that one still runs.
     if (lane == 0) {
+      if (p.wait_channels) pdl_wait();
       const uint64_t policy = p.read_once ? l2_policy_evict_first() : l2_policy_evict_last();
       Slot<S::kWStages> s;
       int armed = 0;
@@ -926,6 +928,7 @@ cudaError_t launch_t(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaSt
   p.token_tiles = static_cast<int>((a.m + NT - 1) / NT);
   p.tiles = static_cast<int>((a.n + kPairChannels - 1) / kPairChannels * p.token_tiles);
   p.read_once = p.token_tiles == 1;
+  p.wait_channels = a.b_is_new;
   p.block_l1 = w.block_l1;
   p.block_l1_next = w.block_l1_next;
   p.partial = w.partial;
@@ -976,11 +979,10 @@ int matmul_i8_pitch(int k) { return (k + kDepth - 1) / kDepth * kDepth; }
 
 size_t matmul_i8_partial_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * kChannels * 256 * sizeof(int); }
 
-bool matmul_i8_tc_fits(const MatmulI8Launch& a) {
-  // The tensor map wants 16-byte boundaries and 32-bit coordinates; the kernel counts stages in 32 bits.
-  const double stages = (a.n / 256.0 + 1) * (a.m / (a.m <= 128 ? 32.0 : 256.0) + 1) * (a.k / 128.0 + 1);
-  return a.k > 0 && (reinterpret_cast<uintptr_t>(a.b) & 15) == 0 && a.ld_b % 16 == 0 && a.n <= INT32_MAX - kPairChannels &&
-         stages < 2.0e9;
+int64_t matmul_i8_tc_rows(int64_t m, int k) {
+  // The tensor map has 32-bit coordinates; the kernel counts stages in 32 bits.
+  const double stages = (m / (m <= 128 ? 32.0 : 256.0) + 1) * (k / 128.0 + 1);  // of 256 rows
+  return std::min<int64_t>(static_cast<int64_t>(2.0e9 / stages) - 1, INT32_MAX / kPairChannels - 1) * kPairChannels;
 }
 
 cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, const MatmulI8Workspace& w,

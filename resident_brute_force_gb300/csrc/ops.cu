@@ -33,6 +33,7 @@ struct rbf_ops {
   // uses one of them out of turn; what it then finds is a larger bound, no smaller one.
   unsigned* block_l1 = nullptr;
   int turn = 0;
+  int8_t* staged = nullptr;      // rows of b put on 16-byte boundaries, kStagedBytes
   int* errw = nullptr;           // error bits of the kernels since the last check
   uint64_t timeout_ns = 2000000000ull;  // bound on every device-side wait
 
@@ -42,6 +43,8 @@ struct rbf_ops {
 };
 
 namespace {
+
+constexpr size_t kStagedBytes = size_t(32) << 20;  // a part of b that L2 holds between its two kernels
 
 rbf_status cuda_fail(rbf_ops* o, cudaError_t err) {
   o->last_cuda_error = static_cast<int>(err);
@@ -66,6 +69,7 @@ void release(rbf_ops* o) {
   cudaFree(o->partial);
   cudaFree(o->arrived);
   cudaFree(o->block_l1);
+  cudaFree(o->staged);
   cudaFree(o->errw);
   if (o->own_stream && o->stream) cudaStreamDestroy(o->stream);
   delete o;
@@ -110,6 +114,41 @@ MatmulI8Workspace take_workspace(rbf_ops* o) {
   return w;
 }
 
+// The product as its kernels see it, or the first of its parts: as many rows of
+// b as a launch takes and, where they do not start on 16-byte boundaries, as the
+// room holds in which they are put on them.
+MatmulI8Launch first_part(const rbf_ops* o, const MatmulI8Launch& a) {
+  MatmulI8Launch f = a;
+  f.n = std::min(a.n, matmul_i8_tc_rows(a.m, a.k));
+  if (!aligned(a.b, 16) || a.ld_b % 16 != 0) {
+    const int pitch = (a.k + 15) / 16 * 16;
+    f.b = o->staged;
+    f.ld_b = pitch;
+    f.n = std::min<int64_t>(f.n, static_cast<int64_t>(kStagedBytes / pitch / 256 * 256));
+    f.b_is_new = true;
+  }
+  return f;
+}
+
+// launch(part) for all parts of a.
+template <typename F>
+rbf_status each_part(rbf_ops* o, const MatmulI8Launch& a, const MatmulI8Launch& first, F&& launch) {
+  for (int64_t j = 0; j < a.n; j += first.n) {
+    MatmulI8Launch part = first;
+    part.n = std::min(first.n, a.n - j);
+    part.b_scale = a.b_scale ? a.b_scale + j : nullptr;
+    part.bias = a.bias ? a.bias + j : nullptr;
+    part.out = static_cast<char*>(a.out) + j * dtype_bytes(a.out_dtype);
+    if (first.b_is_new)
+      OPS_LAUNCH(o, launch_pitch_rows(a.b + j * a.ld_b, a.ld_b, part.n, a.k, o->staged, static_cast<int>(first.ld_b), o->num_sms,
+                                      o->stream));
+    else
+      part.b = a.b + j * a.ld_b;
+    OPS_LAUNCH(o, launch(part));
+  }
+  return RBF_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -142,6 +181,7 @@ rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream
                   cudaMalloc(&o->arrived, o->num_sms * sizeof(unsigned)) == cudaSuccess &&
                   cudaMalloc(&o->row_scale, static_cast<size_t>(max_rows) * sizeof(float)) == cudaSuccess &&
                   cudaMalloc(&o->block_l1, 2 * sizeof(unsigned)) == cudaSuccess &&
+                  cudaMalloc(&o->staged, kStagedBytes) == cudaSuccess &&
                   cudaMalloc(&o->errw, 4 * sizeof(int)) == cudaSuccess;
   if (!ok) {
     cudaGetLastError();
@@ -232,18 +272,16 @@ rbf_status matmul_i8_dev(rbf_ops* o, const int8_t* d_a, int64_t ld_a, const floa
   if (!matrix_ok(d_a, 1, m, k, ld_a)) return RBF_ERR_INVALID_VALUE;
   if (out_dtype == RBF_DTYPE_I32 && (d_a_scale || d_b_scale || d_bias)) return RBF_ERR_INVALID_VALUE;
   if (m == 0 || n == 0) return RBF_OK;
-  if (matmul_i8_few_fits(a)) {
-    OPS_LAUNCH(o, launch_matmul_i8_few(a, d_a, ld_a, kI8, o->num_sms, o->stream));
+  if (k == 0) {
+    OPS_LAUNCH(o, launch_matmul_i8_empty(a, o->num_sms, o->stream));
     return RBF_OK;
   }
-  if (!matmul_i8_tc_fits(a)) {
-    OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
-    return RBF_OK;
-  }
+  const MatmulI8Launch first = first_part(o, a);
+  if (matmul_i8_few_fits(first))
+    return each_part(o, a, first, [&](const MatmulI8Launch& p) { return launch_matmul_i8_few(p, d_a, ld_a, kI8, o->num_sms, o->stream); });
   const MatmulI8Workspace w = take_workspace(o);
   OPS_LAUNCH(o, launch_expand_rows(d_a, ld_a, m, k, w, o->stream));
-  OPS_LAUNCH(o, launch_matmul_i8_tc(a, w, o->stream));
-  return RBF_OK;
+  return each_part(o, a, first, [&](const MatmulI8Launch& p) { return launch_matmul_i8_tc(p, w, o->stream); });
 }
 
 rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t ld_x, const int8_t* d_w,
@@ -268,10 +306,14 @@ rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t
   if (rbf_status st = check_matmul(o, a)) return st;
   if (!matrix_ok(d_x, dtype_bytes(x_dtype), m, k, ld_x)) return RBF_ERR_INVALID_VALUE;
   if (m == 0 || n == 0) return RBF_OK;
-  if (matmul_i8_few_fits(a)) {
-    OPS_LAUNCH(o, launch_matmul_i8_few(a, d_x, ld_x, x_dtype, o->num_sms, o->stream));
+  if (k == 0) {
+    a.a_scale = nullptr;
+    OPS_LAUNCH(o, launch_matmul_i8_empty(a, o->num_sms, o->stream));
     return RBF_OK;
   }
+  const MatmulI8Launch first = first_part(o, a);
+  if (matmul_i8_few_fits(first))
+    return each_part(o, a, first, [&](const MatmulI8Launch& p) { return launch_matmul_i8_few(p, d_x, ld_x, x_dtype, o->num_sms, o->stream); });
   QuantizeLaunch q;
   q.x = d_x;
   q.dtype = x_dtype;
@@ -279,21 +321,12 @@ rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t
   q.rows = m;
   q.cols = k;
   q.scale = o->row_scale;
-  if (!matmul_i8_tc_fits(a)) {
-    // The workspace holds the rows as bytes here, in half of its room.
-    q.q = static_cast<int8_t*>(o->rows_f16);
-    q.ld_q = a.ld_a;
-    OPS_LAUNCH(o, launch_quantize_rows(q, o->stream));
-    OPS_LAUNCH(o, launch_matmul_i8_any(a, o->stream));
-    return RBF_OK;
-  }
   const MatmulI8Workspace w = take_workspace(o);
   q.f16 = w.rows_f16;
   q.f16_pitch = matmul_i8_pitch(k);
   q.block_l1 = w.block_l1;
   OPS_LAUNCH(o, launch_quantize_rows(q, o->stream));
-  OPS_LAUNCH(o, launch_matmul_i8_tc(a, w, o->stream));
-  return RBF_OK;
+  return each_part(o, a, first, [&](const MatmulI8Launch& p) { return launch_matmul_i8_tc(p, w, o->stream); });
 }
 
 rbf_status sample_dev(rbf_ops* o, const void* d_logits, rbf_dtype dtype, int64_t ld, int64_t rows, int32_t vocab,

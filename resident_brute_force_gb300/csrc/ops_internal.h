@@ -48,9 +48,14 @@ struct MatmulI8Launch {
   int64_t m = 0;
   int64_t n = 0;
   int k = 0;
+  bool b_is_new = false;  // b is written by the kernel enqueued just before
 };
-// Any strides and alignments.
-cudaError_t launch_matmul_i8_any(const MatmulI8Launch& a, cudaStream_t stream);
+// Rows of k bytes to rows of `pitch` bytes (a multiple of 16 from k on, whose
+// last ones are not set), which start on 16-byte boundaries.
+cudaError_t launch_pitch_rows(const int8_t* b, int64_t ld_b, int64_t rows, int k, int8_t* out, int pitch, int num_sms,
+                              cudaStream_t stream);
+// The result of a depth of zero: 0 times the scales, plus the bias.
+cudaError_t launch_matmul_i8_empty(const MatmulI8Launch& a, int num_sms, cudaStream_t stream);
 
 // Up to four tokens, in one launch: 8-bit ones (dtype kI8), or floating-point
 // ones that it quantises. a.a and a.ld_a are not used, nor a.a_scale with the
@@ -75,7 +80,7 @@ struct MatmulI8Workspace {
 };
 int matmul_i8_pitch(int k);  // fp16 numbers per workspace row
 size_t matmul_i8_partial_bytes(int num_sms);
-bool matmul_i8_tc_fits(const MatmulI8Launch& a);
+int64_t matmul_i8_tc_rows(int64_t m, int k);  // most rows of b that one launch takes
 cudaError_t launch_expand_rows(const int8_t* a, int64_t ld_a, int64_t m, int k, const MatmulI8Workspace& w,
                                cudaStream_t stream);
 cudaError_t launch_matmul_i8_tc(const MatmulI8Launch& a, const MatmulI8Workspace& w, cudaStream_t stream);

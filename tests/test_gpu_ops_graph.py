@@ -1,9 +1,8 @@
 """The scoring-head calls captured in a graph and replayed on other inputs give the eager calls' results bit for bit."""
 import pytest
+import torch
 
-torch = pytest.importorskip("torch")
-
-import resident_brute_force_gb300 as rbf  # noqa: E402
+import resident_brute_force_gb300 as rbf
 
 pytestmark = pytest.mark.gpu
 
