@@ -359,6 +359,15 @@ struct Cta {
     else
       __syncthreads();
   }
+  // A CTA's shared memory may be written by others once it has started: all
+  // arrive at the kernel's start and wait ahead of the first remote store (at
+  // `reduce`), with the read of the row in between.
+  __device__ __forceinline__ void started() const {
+    if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  __device__ __forceinline__ void all_started() const {
+    if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
   // Sum (or largest) of every thread's v over the cluster; s.slot[turn ^ 1]
   // keeps the CTAs' own until the reduction after the next.
   template <bool MAX>
@@ -432,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   uint4* held = reinterpret_cast<uint4*>(dyn + kCap * sizeof(u64));
 
   Cta<kWarps> cta(s);
+  cta.started();
   const int lane = cta.lane;
   const int64_t r = blockIdx.x / cta.size;
   const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
@@ -486,6 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   Vec<T>::unpack(best, x0);
 #pragma unroll
   for (int i = 1; i < E; ++i) x0[0] = fmaxf(x0[0], x0[i]);
+  __syncwarp();  // the barrier is for converged warps
+  cta.all_started();
   const float top = score_from_code(static_cast<uint32_t>(cta.reduce<true>(score_code(x0[0]))));
   if (top == -INFINITY) {  // nothing else
     if (cta.rank == 0 && threadIdx.x == 0) {

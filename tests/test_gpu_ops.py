@@ -456,3 +456,27 @@ def test_sample_sorted_rows(ops, order):
     check_allowed(ops, x, u, top_k=[3, 300, 4000])
     check_allowed(ops, x, u, top_p=np.array([0.5, 0.9, 0.99], np.float32))
     check_allowed(ops, x, u, top_k=[50, 300, 4000], top_p=np.array([0.5, 0.9, 0.99], np.float32), min_p=0.001)
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 10000), (64, 10001), (300, 17000), (9, 150001), (4, 400000)])
+def test_sample_clusters_beside_other_work(ops, rows, vocab):
+    """Another stream's kernels come and go, so that the CTAs of a row's cluster find room at different times: every
+    call has the row's one result (whole-numbered scores, whose weights are powers of two)."""
+    g = np.random.default_rng(vocab)
+    x = g.integers(-30, 4, (rows, vocab)).astype(np.float32)
+    x[:, vocab // 3] = 9.0
+    u = g.random(rows).astype(np.float32)
+    want = [ref.sample_exact(x[i], float(u[i]), top_p=0.9)[0] for i in range(min(rows, 6))]
+    dx, du = on_gpu(x), torch.from_numpy(u).cuda()
+    t, p = torch.full((rows,), float(ref.LOG2E), device="cuda"), torch.full((rows,), 0.9, device="cuda")
+    tokens = [torch.full((rows,), -7, dtype=torch.int32, device="cuda") for _ in range(40)]
+    other, busy = torch.cuda.Stream(), torch.zeros(1 << 22, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        for _ in range(200):
+            busy.add_(1.0)
+    for token in tokens:
+        ops.sample_dev(dx, du, token, temperature=t, top_p=p)
+    torch.cuda.synchronize()
+    assert tokens[0][:6].tolist() == want
+    assert all(torch.equal(token, tokens[0]) for token in tokens)
