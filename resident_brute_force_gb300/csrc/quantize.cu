@@ -47,18 +47,19 @@ __global__ void __launch_bounds__(kQuantThreads)
     quantize_rows_any_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, const Out o) {
   pdl_launch_dependents();  // a product may become resident now; it waits for these rows
   constexpr int kRows = kQuantThreads / THREADS;
-  const int t = threadIdx.x % THREADS;
+  // Unsigned: a column's number plus a step may pass 2^31 at the end of a row.
+  const unsigned t = threadIdx.x % THREADS, n = static_cast<unsigned>(cols), pitch = static_cast<unsigned>(o.pitch);
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / THREADS; r < rows; r += static_cast<int64_t>(gridDim.x) * kRows) {
     const T* row = x + r * ld_x;
     uint32_t top = 0;
-    for (int j = t; j < cols; j += THREADS) top = max(top, __float_as_uint(to_f32(row[j])) & 0x7FFFFFFFu);
+    for (unsigned j = t; j < n; j += THREADS) top = max(top, __float_as_uint(to_f32(row[j])) & 0x7FFFFFFFu);
     const RowScale s = row_scale(THREADS == 32 ? __reduce_max_sync(kFullMask, top) : block_max(top));
     if (o.f16) {
-      for (int j = t; j < o.pitch; j += THREADS)
-        o.f16[r * o.pitch + j] = __float2half_rn(j < cols ? quantize_sum(to_f32(row[j]), s) - kRounder : 0.0f);
+      for (unsigned j = t; j < pitch; j += THREADS)
+        o.f16[r * o.pitch + j] = __float2half_rn(j < n ? quantize_sum(to_f32(row[j]), s) - kRounder : 0.0f);
       if (t == 0) atomicMax(o.block_l1, 128u * 127u);  // the bound of any row: not worth a reduction here
     } else {
-      for (int j = t; j < cols; j += THREADS)
+      for (unsigned j = t; j < n; j += THREADS)
         o.q[r * o.ld_q + j] = static_cast<int8_t>(__float_as_uint(quantize_sum(to_f32(row[j]), s)));
     }
     if (t == 0) o.scale[r] = s.scale;

@@ -480,3 +480,23 @@ def test_sample_clusters_beside_other_work(ops, rows, vocab):
     torch.cuda.synchronize()
     assert tokens[0][:6].tolist() == want
     assert all(torch.equal(token, tokens[0]) for token in tokens)
+
+
+def test_quantize_the_longest_row(ops):
+    """2^31 - 1 columns, the most that a call takes: column numbers do not pass 32 bits at the row's end."""
+    cols = (1 << 31) - 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.empty(1, cols, dtype=torch.bfloat16, device="cuda")
+    for c in range(0, cols, 1 << 28):
+        x[:, c:c + (1 << 28)] = torch.randn(1, min(1 << 28, cols - c), generator=g, device="cuda")
+    x[0, -1] = 100.0  # the largest one is the last
+    whole = torch.full((1, cols + 65), 77, dtype=torch.int8, device="cuda")
+    scale = torch.empty(1, device="cuda")
+    ops.quantize_rows_i8_dev(x, whole[:, :cols], scale)
+    assert scale[0].item() == np.float32(100) * (np.float32(1) / np.float32(127))
+    factor = float((np.float32(1) / np.float32(100)) * np.float32(127))
+    for c in range(0, cols, 1 << 28):
+        part = x[:, c:c + (1 << 28)].float()
+        assert torch.equal(whole[:, c:min(c + (1 << 28), cols)], (part * factor).round_().to(torch.int8))
+    assert bool((whole[:, cols:] == 77).all())
