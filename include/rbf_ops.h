@@ -61,6 +61,9 @@ typedef enum rbf_dtype {
 rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream, rbf_ops** out);
 /* Waits for the handle's stream, then frees everything. NULL is fine. */
 rbf_status rbf_ops_destroy(rbf_ops* ops);
+/* The handle's device: the one that was current when it was created. A call
+ * made while another one is current is refused (INVALID_VALUE). */
+int32_t rbf_ops_device(rbf_ops* ops);
 /* The handle's stream. */
 void* rbf_ops_stream(rbf_ops* ops);
 /* The CUDA error behind the last RBF_ERR_CUDA. */

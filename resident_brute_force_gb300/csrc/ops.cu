@@ -62,7 +62,32 @@ rbf_status cuda_fail(rbf_ops* o, cudaError_t err) {
     ++(o)->launches;                                                     \
   } while (0)
 
+// The handle's stream (the default one is each device's own) and its workspace
+// belong to its device: no work is enqueued while another one is current.
+bool on_its_device(const rbf_ops* o) {
+  int current = -1;
+  return cudaGetDevice(&current) == cudaSuccess && current == o->device;
+}
+
+// The handle's device, current for a wait or a release.
+class DeviceScope {
+ public:
+  explicit DeviceScope(int device) {
+    changed_ = cudaGetDevice(&before_) == cudaSuccess && before_ != device && cudaSetDevice(device) == cudaSuccess;
+  }
+  ~DeviceScope() {
+    if (changed_) cudaSetDevice(before_);
+  }
+  DeviceScope(const DeviceScope&) = delete;
+  DeviceScope& operator=(const DeviceScope&) = delete;
+
+ private:
+  int before_ = 0;
+  bool changed_ = false;
+};
+
 void release(rbf_ops* o) {
+  const DeviceScope scope(o->device);
   if (o->stream) cudaStreamSynchronize(o->stream);
   cudaFree(o->rows_f16);
   cudaFree(o->row_scale);
@@ -204,12 +229,14 @@ rbf_status rbf_ops_destroy(rbf_ops* o) {
   return RBF_OK;
 }
 
+int32_t rbf_ops_device(rbf_ops* o) { return o ? o->device : -1; }
 void* rbf_ops_stream(rbf_ops* o) { return o ? o->stream : nullptr; }
 int32_t rbf_ops_last_cuda_error(rbf_ops* o) { return o ? o->last_cuda_error : 0; }
 int32_t rbf_ops_last_launches(rbf_ops* o) { return o ? o->launches : 0; }
 
 rbf_status rbf_ops_check_device_error(rbf_ops* o) {
   if (!o) return RBF_ERR_INVALID_VALUE;
+  const DeviceScope scope(o->device);
   int e = 0;
   cudaError_t st = cudaMemcpyAsync(&e, o->errw, sizeof(int), cudaMemcpyDeviceToHost, o->stream);
   if (st == cudaSuccess) st = cudaStreamSynchronize(o->stream);
@@ -232,6 +259,7 @@ rbf_status quantize_rows_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, 
                                 int32_t cols, int8_t* d_q, int64_t ld_q, float* d_scale) {
   if (!o || !float_dtype(x_dtype) || rows < 0 || cols < 0 || rows > INT32_MAX) return RBF_ERR_INVALID_VALUE;
   o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
   if (!matrix_ok(d_x, dtype_bytes(x_dtype), rows, cols, ld_x) || !matrix_ok(d_q, 1, rows, cols, ld_q))
     return RBF_ERR_INVALID_VALUE;
   if (rows == 0) return RBF_OK;
@@ -254,6 +282,7 @@ rbf_status matmul_i8_dev(rbf_ops* o, const int8_t* d_a, int64_t ld_a, const floa
                          int64_t ld_out, int64_t m, int64_t n, int32_t k) {
   if (!o || !(float_dtype(out_dtype) || out_dtype == RBF_DTYPE_I32)) return RBF_ERR_INVALID_VALUE;
   o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
   MatmulI8Launch a;
   a.a = d_a;
   a.ld_a = ld_a;
@@ -289,6 +318,7 @@ rbf_status linear_i8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t
                          int64_t ld_out, int64_t m, int64_t n, int32_t k) {
   if (!o || !float_dtype(x_dtype) || !float_dtype(out_dtype)) return RBF_ERR_INVALID_VALUE;
   o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
   MatmulI8Launch a;
   a.a = static_cast<const int8_t*>(o->rows_f16);
   a.ld_a = matmul_i8_pitch(k);
@@ -335,6 +365,7 @@ rbf_status sample_dev(rbf_ops* o, const void* d_logits, rbf_dtype dtype, int64_t
   if (!o || !float_dtype(dtype) || rows < 0 || rows > INT32_MAX || vocab < 0 || vocab > RBF_OPS_MAX_VOCAB)
     return RBF_ERR_INVALID_VALUE;
   o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
   if (!matrix_ok(d_logits, dtype_bytes(dtype), rows, vocab, ld)) return RBF_ERR_INVALID_VALUE;
   if (rows == 0) return RBF_OK;
   if (!d_u || !d_token || !floats_ok(d_u) || !floats_ok(d_temperature) || !floats_ok(d_top_k) || !floats_ok(d_top_p) ||

@@ -24,6 +24,7 @@ _S = ctypes.c_int
 _binding.SIGNATURES.update({
     "rbf_ops_create": (_S, [_I64, _I32, _P, ctypes.POINTER(_P)]),
     "rbf_ops_destroy": (_S, [_P]),
+    "rbf_ops_device": (_I32, [_P]),
     "rbf_ops_stream": (_P, [_P]),
     "rbf_ops_last_cuda_error": (_I32, [_P]),
     "rbf_ops_last_launches": (_I32, [_P]),
@@ -48,27 +49,34 @@ def _dtypes() -> dict:
 
 
 # The checks below run before every launch: messages are put together only when one fails.
+# device: the handle's, which every tensor has to be on.
 
-def _float_matrix(t, what: str, integers: bool = False):
+def _float_matrix(t, what: str, device, integers: bool = False):
     """Device pointer, row stride, rows, columns and dtype code of a 2-D CUDA tensor with contiguous rows."""
     code = _dtypes().get(t.dtype)
     if code is None or code < 0 or (code == RBF_DTYPE_I32 and not integers):
         raise TypeError(f"{what} is {t.dtype}: expected float32, bfloat16 or float16" + (" or int32" if integers else ""))
-    return *_matrix(t, what), code
+    return *_matrix(t, what, device), code
 
 
-def _i8_matrix(t, what: str):
+def _i8_matrix(t, what: str, device):
     if _dtypes().get(t.dtype) != -1:
         raise TypeError(f"{what} is {t.dtype}: expected int8")
-    return _matrix(t, what)
+    return _matrix(t, what, device)
 
 
-def _matrix(t, what: str):
+def _same_device(t, what: str, device) -> None:
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what} is on device {t.get_device()}, the handle on device {device}")
+
+
+def _matrix(t, what: str, device):
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{what} is a 2-D tensor")
     if not t.is_cuda:
         raise TypeError(f"{what}: expected a CUDA tensor")
+    _same_device(t, what, device)
     rows, cols = shape
     ld, step = t.stride()
     if cols > 1 and step != 1:
@@ -80,14 +88,16 @@ def _matrix(t, what: str):
     return t.data_ptr(), ld, rows, cols
 
 
-def _vector(t, count: int, what: str, dtype: str = "float32", optional: bool = True):
+def _vector(t, count: int, what: str, device, dtype: str = "float32", optional: bool = True):
     if t is None:
         if not optional:
             raise ValueError(f"{what} is required")
         return None
     if t.numel() != count:
         raise ValueError(f"{what} has {t.numel()} entries, expected {count}")
-    return _dev_ptr(t, dtype)
+    p = _dev_ptr(t, dtype)
+    _same_device(t, what, device)
+    return p
 
 
 def _same(got, want, what: str) -> None:
@@ -100,8 +110,12 @@ class Ops:
     up to ``max_rows`` rows of up to ``max_depth`` values. Like an engine, one
     handle serves one call at a time; every call is enqueued on the handle's
     stream (``stream``: a torch stream or a raw handle; None: a stream of its
-    own). Outputs are given by the caller; a tensor used here must not be
-    handed to another stream before this one has reached the call."""
+    own). The handle belongs to the device that was current then: tensors are on
+    that one, and calls are made with it current. Outputs are given by the
+    caller; a tensor used here must not be handed to another stream before this
+    one has reached the call."""
+
+    _device = None  # of the handle
 
     def __init__(self, max_rows: int, max_depth: int, stream=None):
         self.lib = load_library()
@@ -114,6 +128,7 @@ class Ops:
         if st != RBF_OK:
             raise RbfError(st, "rbf_ops_create")
         self._h = handle
+        self._device = self.lib.rbf_ops_device(handle)
         self._stream_ref = stream
 
     # -- lifetime
@@ -158,46 +173,52 @@ class Ops:
     # -- operators
     def quantize_rows_i8_dev(self, d_x, d_q, d_scale) -> None:
         """Rows of d_x [rows, cols] (float32, bfloat16 or float16) to int8 d_q with one scale a row in d_scale."""
-        x, ld_x, rows, cols, dtype = _float_matrix(d_x, "d_x")
-        q, ld_q, q_rows, q_cols = _i8_matrix(d_q, "d_q")
+        on = self._device
+        x, ld_x, rows, cols, dtype = _float_matrix(d_x, "d_x", on)
+        q, ld_q, q_rows, q_cols = _i8_matrix(d_q, "d_q", on)
         _same((q_rows, q_cols), (rows, cols), "the shape of d_q")
         self._check(self.lib.quantize_rows_i8_dev(self._h, x, dtype, ld_x, rows, cols, q, ld_q,
-                                                  _vector(d_scale, rows, "d_scale", optional=False)),
+                                                  _vector(d_scale, rows, "d_scale", on, optional=False)),
                     "quantize_rows_i8_dev")
 
     def matmul_i8_dev(self, d_a, d_a_scale, d_b, d_b_scale, d_out, bias=None) -> None:
         """d_out [m, n] = d_a [m, k] times d_b [n, k] transposed, both int8, each row of either with its scale (None:
         1), plus bias [n]. An int32 d_out takes the sums themselves, without scales or bias."""
-        a, ld_a, m, k = _i8_matrix(d_a, "d_a")
-        b, ld_b, n, b_cols = _i8_matrix(d_b, "d_b")
-        out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", integers=True)
+        on = self._device
+        a, ld_a, m, k = _i8_matrix(d_a, "d_a", on)
+        b, ld_b, n, b_cols = _i8_matrix(d_b, "d_b", on)
+        out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", on, integers=True)
         _same(b_cols, k, "the depth of d_b")
         _same((out_rows, out_cols), (m, n), "the shape of d_out")
-        self._check(self.lib.matmul_i8_dev(self._h, a, ld_a, _vector(d_a_scale, m, "d_a_scale"), b, ld_b,
-                                           _vector(d_b_scale, n, "d_b_scale"), _vector(bias, n, "bias"), out, dtype,
-                                           ld_out, m, n, k), "matmul_i8_dev")
+        self._check(self.lib.matmul_i8_dev(self._h, a, ld_a, _vector(d_a_scale, m, "d_a_scale", on), b, ld_b,
+                                           _vector(d_b_scale, n, "d_b_scale", on), _vector(bias, n, "bias", on), out,
+                                           dtype, ld_out, m, n, k), "matmul_i8_dev")
 
     def linear_i8_dev(self, d_x, d_w, d_w_scale, d_out, bias=None) -> None:
         """d_out [m, n] = d_x [m, k] (quantised by rows) times the int8 weights d_w [n, k] transposed, times the
         weights' row scales d_w_scale (None: 1), plus bias [n]."""
-        x, ld_x, m, k, x_dtype = _float_matrix(d_x, "d_x")
-        w, ld_w, n, w_cols = _i8_matrix(d_w, "d_w")
-        out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out")
+        on = self._device
+        x, ld_x, m, k, x_dtype = _float_matrix(d_x, "d_x", on)
+        w, ld_w, n, w_cols = _i8_matrix(d_w, "d_w", on)
+        out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", on)
         _same(w_cols, k, "the depth of d_w")
         _same((out_rows, out_cols), (m, n), "the shape of d_out")
-        self._check(self.lib.linear_i8_dev(self._h, x, x_dtype, ld_x, w, ld_w, _vector(d_w_scale, n, "d_w_scale"),
-                                           _vector(bias, n, "bias"), out, dtype, ld_out, m, n, k), "linear_i8_dev")
+        self._check(self.lib.linear_i8_dev(self._h, x, x_dtype, ld_x, w, ld_w,
+                                           _vector(d_w_scale, n, "d_w_scale", on), _vector(bias, n, "bias", on), out,
+                                           dtype, ld_out, m, n, k), "linear_i8_dev")
 
     def sample_dev(self, d_logits, d_u, d_token, d_logprob=None, temperature=None, top_k=None, top_p=None,
                    min_p=None) -> None:
         """One index a row of d_logits [rows, vocab] into d_token (int32; -1 where every score is -infinity), and the
         log of its share into d_logprob. d_u: one random number in [0, 1) a row; temperature, top_p and min_p (float32)
         and top_k (int32): one entry a row, or None."""
-        x, ld, rows, vocab, dtype = _float_matrix(d_logits, "d_logits")
+        on = self._device
+        x, ld, rows, vocab, dtype = _float_matrix(d_logits, "d_logits", on)
         self._check(self.lib.sample_dev(self._h, x, dtype, ld, rows, vocab,
-                                        _vector(d_u, rows, "d_u", optional=False),
-                                        _vector(temperature, rows, "temperature"),
-                                        _vector(top_k, rows, "top_k", "int32"), _vector(top_p, rows, "top_p"),
-                                        _vector(min_p, rows, "min_p"),
-                                        _vector(d_token, rows, "d_token", "int32", optional=False),
-                                        _vector(d_logprob, rows, "d_logprob")), "sample_dev")
+                                        _vector(d_u, rows, "d_u", on, optional=False),
+                                        _vector(temperature, rows, "temperature", on),
+                                        _vector(top_k, rows, "top_k", on, "int32"),
+                                        _vector(top_p, rows, "top_p", on),
+                                        _vector(min_p, rows, "min_p", on),
+                                        _vector(d_token, rows, "d_token", on, "int32", optional=False),
+                                        _vector(d_logprob, rows, "d_logprob", on)), "sample_dev")

@@ -107,3 +107,41 @@ def test_c_entry_points_refuse_without_a_handle():
     assert lib.matmul_i8_dev(None, 16, 4, None, 16, 4, None, None, 16, 0, 4, 1, 4, 4) == bad
     assert lib.linear_i8_dev(None, 16, 0, 4, 16, 4, None, None, 16, 0, 4, 1, 4, 4) == bad
     assert lib.sample_dev(None, 16, 0, 4, 1, 4, 16, None, None, None, None, 16, None) == bad
+
+
+class _On(_Cuda):
+    """A stand-in on a device of its own."""
+
+    def __init__(self, t, device):
+        super().__init__(t)
+        self._device = device
+
+    def get_device(self):
+        return self._device
+
+
+CALLS = {
+    "quantize_rows_i8_dev": [("d_x", (3, 4), torch.float32), ("d_q", (3, 4), torch.int8), ("d_scale", (3,), torch.float32)],
+    "matmul_i8_dev": [("d_a", (2, 8), torch.int8), ("d_a_scale", (2,), torch.float32), ("d_b", (3, 8), torch.int8),
+                      ("d_b_scale", (3,), torch.float32), ("d_out", (2, 3), torch.float32), ("bias", (3,), torch.float32)],
+    "linear_i8_dev": [("d_x", (2, 8), torch.float32), ("d_w", (3, 8), torch.int8), ("d_w_scale", (3,), torch.float32),
+                      ("d_out", (2, 3), torch.float32), ("bias", (3,), torch.float32)],
+    "sample_dev": [("d_logits", (2, 8), torch.float32), ("d_u", (2,), torch.float32), ("d_token", (2,), torch.int32),
+                   ("d_logprob", (2,), torch.float32), ("temperature", (2,), torch.float32), ("top_k", (2,), torch.int32),
+                   ("top_p", (2,), torch.float32), ("min_p", (2,), torch.float32)],
+}
+
+
+@pytest.mark.parametrize("call,other", [(call, a[0]) for call, args in CALLS.items() for a in args])
+def test_tensors_of_another_device_are_refused(ops, call, other):
+    ops._device = 1
+    args = {name: _On(torch.zeros(shape, dtype=dtype), 0 if name == other else 1) for name, shape, dtype in CALLS[call]}
+    with pytest.raises(ValueError, match="device"):
+        getattr(ops, call)(**args)
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_tensors_of_the_handles_device_pass(ops, call):
+    ops._device = 1
+    with pytest.raises(AssertionError, match="reached the library"):
+        getattr(ops, call)(**{name: _On(torch.zeros(shape, dtype=dtype), 1) for name, shape, dtype in CALLS[call]})
