@@ -500,3 +500,17 @@ def test_quantize_the_longest_row(ops):
         part = x[:, c:c + (1 << 28)].float()
         assert torch.equal(whole[:, c:min(c + (1 << 28), cols)], (part * factor).round_().to(torch.int8))
     assert bool((whole[:, cols:] == 77).all())
+
+
+@pytest.mark.parametrize("temperature", [1e-45, 1e-39, 4e-39, 4.5e-39, 1e-30])
+@pytest.mark.parametrize("vocab", [40, 5000, 300000])
+def test_sample_temperatures_next_to_zero(ops, vocab, temperature):
+    """Every temperature above 0 draws: so near to it among the scores that equal the best one."""
+    g = np.random.default_rng(vocab)
+    x = on_gpu(np.minimum(g.integers(-30, 6, (4, vocab)), 4).astype(np.float32))
+    u = np.array([0.0, 0.3, 0.7, 0.999], np.float32)
+    check_allowed(ops, x, u, temperature=temperature)
+    check_allowed(ops, x, u, temperature=temperature, min_p=0.1)
+    check_allowed(ops, x, u, temperature=temperature, top_k=[2, 7, 30, vocab - 1])
+    check_allowed(ops, x, u, temperature=temperature, top_p=np.array([0.1, 0.5, 0.9, 0.99], np.float32))
+    check_allowed(ops, x, u, temperature=temperature, top_k=[2, 7, 30, vocab - 1], top_p=np.float32(0.6), min_p=0.5)
