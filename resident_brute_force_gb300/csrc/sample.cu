@@ -196,8 +196,9 @@ __device__ __forceinline__ Ask read_ask(const SampleLaunch& a, int64_t r) {
   const float t = a.temperature ? a.temperature[r] : 1.0f;
   const bool warm = t > 0.0f;  // also false for a NaN
   // A finite rate above 0: an infinite temperature would make (-infinity) * 0 of
-  // a masked score, and one under 4.24e-39 0 * infinity of the best score.
-  q.rate = warm ? fminf(fmaxf(__fdiv_rn(kLog2e, t), 1.17549435e-38f), 3.40282347e38f) : kLog2e;
+  // a masked score, and one under 4.24e-39 0 * infinity of the best score. The
+  // smallest float leaves every finite score the weight 1, to 2^-20.
+  q.rate = warm ? fminf(fmaxf(__fdiv_rn(kLog2e, t), 1.4e-45f), 3.40282347e38f) : kLog2e;
   const int k = a.top_k ? a.top_k[r] : 0;
   q.k = !warm ? 1 : (k > 0 && k < a.vocab ? k : a.vocab);
   const float p = a.top_p ? a.top_p[r] : 1.0f;

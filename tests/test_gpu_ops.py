@@ -514,3 +514,20 @@ def test_sample_temperatures_next_to_zero(ops, vocab, temperature):
     check_allowed(ops, x, u, temperature=temperature, top_k=[2, 7, 30, vocab - 1])
     check_allowed(ops, x, u, temperature=temperature, top_p=np.array([0.1, 0.5, 0.9, 0.99], np.float32))
     check_allowed(ops, x, u, temperature=temperature, top_k=[2, 7, 30, vocab - 1], top_p=np.float32(0.6), min_p=0.5)
+
+
+@pytest.mark.parametrize("temperature", [1e38, 1.3e38, 3e38, math.inf])
+def test_sample_temperatures_next_to_infinity(ops, temperature):
+    """Finite scores as far apart as their type allows, among them masks of its lowest value: at infinite temperature
+    all are alike. (Scores whose difference passes the largest float are infinitely far apart.)"""
+    lowest = torch.finfo(torch.float32).min
+    g = np.random.default_rng(3)
+    x = g.standard_normal((3, 2000)).astype(np.float32)
+    x[0, g.random(2000) < 0.5] = lowest
+    x[1] *= np.float32(3e37)
+    x[2] = np.where(g.random(2000) < 0.9, np.float32(lowest), np.float32(-1e38))
+    x = on_gpu(x)
+    for u in (0.0, 0.2, 0.61, 0.9999):
+        check_allowed(ops, x, u, temperature=temperature)
+        check_allowed(ops, x, u, temperature=temperature, top_p=np.float32(0.4))
+        check_allowed(ops, x, u, temperature=temperature, min_p=0.3)
