@@ -74,6 +74,11 @@ int32_t rbf_ops_last_launches(rbf_ops* ops);
  * reported since the last check: RBF_ERR_TIMEOUT if a bounded device-side
  * wait ran out (the outputs of that call are not valid), else RBF_OK. */
 rbf_status rbf_ops_check_device_error(rbf_ops* ops);
+/* Bound on each device-side wait of the calls that follow, in nanoseconds
+ * (default 2e9, at least 1e6: copies in flight have landed by then). A wait is
+ * for another part of the same kernel to go one step on, so the bound does not
+ * limit how long a call takes. */
+rbf_status rbf_ops_set_timeout(rbf_ops* ops, int64_t nanoseconds);
 /* The next `count` kernel launches report failure without being issued
  * (tests of the error path; touches no GPU state). 0 clears. */
 rbf_status rbf_ops_inject_host_fault(rbf_ops* ops, int32_t count);

@@ -624,12 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok && lane == 0 && !aborted()) give_up(kErrConsumerTimeout);
-      // Every MMA (they read both CTAs' memories) is done before either exits.
       if (elect_one()) umma_commit_pair(drain);
       __syncwarp();
     }
-    if (!mbar_wait(drain, 0, p.timeout_ns)) atomicOr(p.err, kErrDrainTimeout);
-    __syncwarp();
   } else {
     // -------------------------------------------------------------- workers
     const int group = (warp - 2) >> 2;
@@ -840,6 +837,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // Every MMA (they read both CTAs' memories) is done before either exits. The
+  // wait's bound starts here, when the CTA's workers have seen the last sums:
+  // from the kernel's start it would be one on the whole product's time.
+  if (warp == 1) {
+    if (!mbar_wait(drain, 0, p.timeout_ns)) atomicOr(p.err, kErrDrainTimeout);
+    __syncwarp();
+  }
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);

@@ -249,6 +249,12 @@ rbf_status rbf_ops_check_device_error(rbf_ops* o) {
   return e ? RBF_ERR_TIMEOUT : RBF_OK;
 }
 
+rbf_status rbf_ops_set_timeout(rbf_ops* o, int64_t nanoseconds) {
+  if (!o || nanoseconds < 1000000) return RBF_ERR_INVALID_VALUE;
+  o->timeout_ns = static_cast<uint64_t>(nanoseconds);
+  return RBF_OK;
+}
+
 rbf_status rbf_ops_inject_host_fault(rbf_ops* o, int32_t count) {
   if (!o || count < 0) return RBF_ERR_INVALID_VALUE;
   o->fault_count = count;

@@ -29,6 +29,7 @@ _binding.SIGNATURES.update({
     "rbf_ops_last_cuda_error": (_I32, [_P]),
     "rbf_ops_last_launches": (_I32, [_P]),
     "rbf_ops_check_device_error": (_S, [_P]),
+    "rbf_ops_set_timeout": (_S, [_P, _I64]),
     "rbf_ops_inject_host_fault": (_S, [_P, _I32]),
     "quantize_rows_i8_dev": (_S, [_P, _P, _S, _I64, _I64, _I32, _P, _I64, _P]),
     "matmul_i8_dev": (_S, [_P, _P, _I64, _P, _P, _I64, _P, _P, _P, _S, _I64, _I64, _I64, _I32]),
@@ -166,6 +167,10 @@ class Ops:
     def check_device_error(self) -> int:
         """Wait for the stream; the status its kernels reported since the last check."""
         return self.lib.rbf_ops_check_device_error(self._h)
+
+    def set_timeout(self, nanoseconds: int) -> None:
+        """Bound each device-side wait of later calls (default 2e9, at least 1e6); it does not limit a call's time."""
+        self._check(self.lib.rbf_ops_set_timeout(self._h, int(nanoseconds)), "rbf_ops_set_timeout")
 
     def inject_host_fault(self, count: int) -> None:
         self._check(self.lib.rbf_ops_inject_host_fault(self._h, int(count)), "rbf_ops_inject_host_fault")

@@ -111,3 +111,30 @@ def test_aligned_padded_outputs(name, m, n, k):
     unit = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 0.0}[name]  # the last rounding, on top of three in fp32
     assert (off <= (unit + 4 * 2.0 ** -24) * np.abs(want) + (2.0 ** -25 if name == "f16" else 0)).all()
     assert bool((whole[:m, n:] == 5).all()) and bool((whole[m] == 5).all())
+
+
+def test_a_product_may_take_longer_than_a_wait():
+    """The bound on device-side waits is one on a step of the kernel: a product that takes several times as long is no
+    timeout, and its result is the one that the kernel for few tokens gives."""
+    m, n, k, bound = 4096, 131072, 32768, 4_000_000
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    a = torch.randint(-128, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
+    b = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    scale = torch.rand(m, generator=g, device="cuda") * 1e-4
+    out, few = torch.empty(m, n, dtype=torch.bfloat16, device="cuda"), torch.empty(2, n, dtype=torch.bfloat16, device="cuda")
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    with rbf.Ops(m, k, stream=torch.cuda.current_stream()) as o:
+        for bad in (0, -1, 999_999):
+            with pytest.raises(rbf.RbfError):
+                o.set_timeout(bad)
+        o.set_timeout(bound)
+        o.matmul_i8_dev(a[:64], scale[:64], b[:1000], None, out[:64, :1000])  # loads the kernels
+        begin.record()
+        o.matmul_i8_dev(a, scale, b, None, out)
+        end.record()
+        assert o.check_device_error() == rbf.RBF_OK
+        assert begin.elapsed_time(end) * 1e6 > 2 * bound  # else the bound was not passed
+        for i in (0, m - 2):
+            o.matmul_i8_dev(a[i:i + 2], scale[i:i + 2], b, None, few)
+            assert torch.equal(out[i:i + 2], few)
