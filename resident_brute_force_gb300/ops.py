@@ -89,6 +89,21 @@ def _matrix(t, what: str, device):
     return t.data_ptr(), ld, rows, cols
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _row_length(cols: int, what: str) -> int:
+    """A row's length as the library takes it: ctypes would cut a larger one to its low 32 bits."""
+    if cols > _INT32_MAX:
+        raise ValueError(f"the rows of {what} have {cols} values, more than 2^31 - 1")
+    return cols
+
+
+def _int(value: int, bits: int) -> int:
+    """A number as a signed integer of that many bits, at its limit where it is past that (the library refuses it)."""
+    return max(-(1 << bits - 1), min(int(value), (1 << bits - 1) - 1))
+
+
 def _vector(t, count: int, what: str, device, dtype: str = "float32", optional: bool = True):
     if t is None:
         if not optional:
@@ -124,7 +139,7 @@ class Ops:
         if stream is not None:
             s = (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) or _STREAM_LEGACY
         handle = ctypes.c_void_p()
-        st = self.lib.rbf_ops_create(int(max_rows), int(max_depth), ctypes.c_void_p(s) if s else None,
+        st = self.lib.rbf_ops_create(_int(max_rows, 64), _int(max_depth, 32), ctypes.c_void_p(s) if s else None,
                                      ctypes.byref(handle))
         if st != RBF_OK:
             raise RbfError(st, "rbf_ops_create")
@@ -170,10 +185,10 @@ class Ops:
 
     def set_timeout(self, nanoseconds: int) -> None:
         """Bound each device-side wait of later calls (default 2e9, at least 1e6); it does not limit a call's time."""
-        self._check(self.lib.rbf_ops_set_timeout(self._h, int(nanoseconds)), "rbf_ops_set_timeout")
+        self._check(self.lib.rbf_ops_set_timeout(self._h, _int(nanoseconds, 64)), "rbf_ops_set_timeout")
 
     def inject_host_fault(self, count: int) -> None:
-        self._check(self.lib.rbf_ops_inject_host_fault(self._h, int(count)), "rbf_ops_inject_host_fault")
+        self._check(self.lib.rbf_ops_inject_host_fault(self._h, _int(count, 32)), "rbf_ops_inject_host_fault")
 
     # -- operators
     def quantize_rows_i8_dev(self, d_x, d_q, d_scale) -> None:
@@ -182,7 +197,7 @@ class Ops:
         x, ld_x, rows, cols, dtype = _float_matrix(d_x, "d_x", on)
         q, ld_q, q_rows, q_cols = _i8_matrix(d_q, "d_q", on)
         _same((q_rows, q_cols), (rows, cols), "the shape of d_q")
-        self._check(self.lib.quantize_rows_i8_dev(self._h, x, dtype, ld_x, rows, cols, q, ld_q,
+        self._check(self.lib.quantize_rows_i8_dev(self._h, x, dtype, ld_x, rows, _row_length(cols, "d_x"), q, ld_q,
                                                   _vector(d_scale, rows, "d_scale", on, optional=False)),
                     "quantize_rows_i8_dev")
 
@@ -193,7 +208,7 @@ class Ops:
         a, ld_a, m, k = _i8_matrix(d_a, "d_a", on)
         b, ld_b, n, b_cols = _i8_matrix(d_b, "d_b", on)
         out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", on, integers=True)
-        _same(b_cols, k, "the depth of d_b")
+        _same(b_cols, _row_length(k, "d_a"), "the depth of d_b")
         _same((out_rows, out_cols), (m, n), "the shape of d_out")
         self._check(self.lib.matmul_i8_dev(self._h, a, ld_a, _vector(d_a_scale, m, "d_a_scale", on), b, ld_b,
                                            _vector(d_b_scale, n, "d_b_scale", on), _vector(bias, n, "bias", on), out,
@@ -206,7 +221,7 @@ class Ops:
         x, ld_x, m, k, x_dtype = _float_matrix(d_x, "d_x", on)
         w, ld_w, n, w_cols = _i8_matrix(d_w, "d_w", on)
         out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", on)
-        _same(w_cols, k, "the depth of d_w")
+        _same(w_cols, _row_length(k, "d_x"), "the depth of d_w")
         _same((out_rows, out_cols), (m, n), "the shape of d_out")
         self._check(self.lib.linear_i8_dev(self._h, x, x_dtype, ld_x, w, ld_w,
                                            _vector(d_w_scale, n, "d_w_scale", on), _vector(bias, n, "bias", on), out,
@@ -219,7 +234,7 @@ class Ops:
         and top_k (int32): one entry a row, or None."""
         on = self._device
         x, ld, rows, vocab, dtype = _float_matrix(d_logits, "d_logits", on)
-        self._check(self.lib.sample_dev(self._h, x, dtype, ld, rows, vocab,
+        self._check(self.lib.sample_dev(self._h, x, dtype, ld, rows, _row_length(vocab, "d_logits"),
                                         _vector(d_u, rows, "d_u", on, optional=False),
                                         _vector(temperature, rows, "temperature", on),
                                         _vector(top_k, rows, "top_k", on, "int32"),

@@ -145,3 +145,33 @@ def test_tensors_of_the_handles_device_pass(ops, call):
     ops._device = 1
     with pytest.raises(AssertionError, match="reached the library"):
         getattr(ops, call)(**{name: _On(torch.zeros(shape, dtype=dtype), 1) for name, shape, dtype in CALLS[call]})
+
+
+@pytest.mark.parametrize("cols", [2 ** 31, 2 ** 32, 2 ** 32 + 8])
+@pytest.mark.parametrize("call", CALLS)
+def test_rows_past_31_bits_are_refused(ops, call, cols):
+    """Not cut to their low 32 bits on the way to the library."""
+    args = {}
+    for name, shape, dtype in CALLS[call]:
+        if name in ("d_x", "d_q", "d_a", "d_b", "d_w", "d_logits"):
+            shape = (shape[0], cols)
+        args[name] = _Cuda(torch.empty(shape, dtype=dtype, device="meta"))
+    with pytest.raises(ValueError, match="2\\^31"):
+        getattr(ops, call)(**args)
+
+
+@pytest.mark.parametrize("size,as_passed", [((1, 2 ** 32 + 64), (1, 2 ** 31 - 1)), ((2 ** 64 + 4, 64), (2 ** 63 - 1, 64)),
+                                            ((1, -(2 ** 32) + 64), (1, -(2 ** 31))), ((4, 64), (4, 64))])
+def test_handle_sizes_reach_the_library_as_they_are(monkeypatch, size, as_passed):
+    """A size past what the library's type holds is passed as one that it refuses."""
+    import types
+    seen = []
+
+    def create(rows, depth, stream, out):
+        seen.append((rows, depth))
+        return rbf.RBF_ERR_INVALID_VALUE
+
+    monkeypatch.setattr(binding, "load_library", lambda: types.SimpleNamespace(rbf_ops_create=create))
+    with pytest.raises(rbf.RbfError):
+        rbf.Ops(*size)
+    assert seen == [as_passed]
