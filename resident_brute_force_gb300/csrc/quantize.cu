@@ -42,24 +42,25 @@ struct Out {
 // warp; 100,000 x 333: 131 and 33. 30,000 x 2,500 (rows on 8-byte boundaries):
 // 84 us, 82 with a row's values kept in registers, which leaves fewer CTAs an
 // SM and costs longer and shorter rows a quarter.
-template <typename T, int THREADS>
+// J holds a column's number plus a step: unsigned for rows that end within a
+// step of 2^31, int for all others (as unsigned numbers 30,000 x 2,500 takes 96).
+template <typename T, int THREADS, typename J>
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_rows_any_kernel(const T* __restrict__ x, int64_t ld_x, int64_t rows, int cols, const Out o) {
   pdl_launch_dependents();  // a product may become resident now; it waits for these rows
   constexpr int kRows = kQuantThreads / THREADS;
-  // Unsigned: a column's number plus a step may pass 2^31 at the end of a row.
-  const unsigned t = threadIdx.x % THREADS, n = static_cast<unsigned>(cols), pitch = static_cast<unsigned>(o.pitch);
+  const J t = threadIdx.x % THREADS, n = cols, pitch = o.pitch;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / THREADS; r < rows; r += static_cast<int64_t>(gridDim.x) * kRows) {
     const T* row = x + r * ld_x;
     uint32_t top = 0;
-    for (unsigned j = t; j < n; j += THREADS) top = max(top, __float_as_uint(to_f32(row[j])) & 0x7FFFFFFFu);
+    for (J j = t; j < n; j += THREADS) top = max(top, __float_as_uint(to_f32(row[j])) & 0x7FFFFFFFu);
     const RowScale s = row_scale(THREADS == 32 ? __reduce_max_sync(kFullMask, top) : block_max(top));
     if (o.f16) {
-      for (unsigned j = t; j < pitch; j += THREADS)
+      for (J j = t; j < pitch; j += THREADS)
         o.f16[r * o.pitch + j] = __float2half_rn(j < n ? quantize_sum(to_f32(row[j]), s) - kRounder : 0.0f);
       if (t == 0) atomicMax(o.block_l1, 128u * 127u);  // the bound of any row: not worth a reduction here
     } else {
-      for (unsigned j = t; j < n; j += THREADS)
+      for (J j = t; j < n; j += THREADS)
         o.q[r * o.ld_q + j] = static_cast<int8_t>(__float_as_uint(quantize_sum(to_f32(row[j]), s)));
     }
     if (t == 0) o.scale[r] = s.scale;
@@ -171,10 +172,11 @@ cudaError_t launch_t(const QuantizeLaunch& a, cudaStream_t st) {
     quantize_rows_held_kernel<T, kQuantThreads, F16><<<static_cast<unsigned>(a.rows), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
   } else if (width <= 32 * 8 * kHeld) {
     const int64_t grid = std::min<int64_t>((a.rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32), int64_t(1) << 20);
-    quantize_rows_any_kernel<T, 32><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
+    quantize_rows_any_kernel<T, 32, int><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
   } else {
     const int64_t grid = std::min<int64_t>(a.rows, int64_t(1) << 20);
-    quantize_rows_any_kernel<T, kQuantThreads><<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
+    auto fn = a.cols > INT32_MAX - kQuantThreads ? quantize_rows_any_kernel<T, kQuantThreads, unsigned> : quantize_rows_any_kernel<T, kQuantThreads, int>;
+    fn<<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(x, a.ld_x, a.rows, a.cols, o);
   }
   return cudaGetLastError();
 }
