@@ -363,9 +363,10 @@ struct Cta {
   }
   // A CTA's shared memory may be written by others once it has started: all
   // arrive at the kernel's start and wait ahead of the first remote store (at
-  // `reduce`), with the read of the row in between.
+  // `reduce`), with the read of the row in between. The arrival has nothing to
+  // release: a relaxed one saves 0.6 to 1.7 us of 15 to 45.
   __device__ __forceinline__ void started() const {
-    if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   }
   __device__ __forceinline__ void all_started() const {
     if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
