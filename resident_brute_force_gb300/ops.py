@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _binding
-from ._binding import RBF_OK, RbfError, _dev_ptr, load_library
+from ._binding import RBF_OK, RbfError, load_library
 
 RBF_DTYPE_F32 = 0
 RBF_DTYPE_BF16 = 1
@@ -49,7 +49,8 @@ def _dtypes() -> dict:
     return _DTYPES
 
 
-# The checks below run before every launch: messages are put together only when one fails.
+# The checks below run before every launch: messages are put together only when one fails. Every call's first one
+# is of a matrix' type, which fills _DTYPES.
 # device: the handle's, which every tensor has to be on.
 
 def _float_matrix(t, what: str, device, integers: bool = False):
@@ -66,22 +67,28 @@ def _i8_matrix(t, what: str, device):
     return _matrix(t, what, device)
 
 
-def _same_device(t, what: str, device) -> None:
-    if device is not None and t.get_device() != device:
+def _wrong_device(t, what: str, device) -> None:
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    if device is not None:
         raise ValueError(f"{what} is on device {t.get_device()}, the handle on device {device}")
+
+
+_INT32_MAX = 2 ** 31 - 1
 
 
 def _matrix(t, what: str, device):
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{what} is a 2-D tensor")
-    if not t.is_cuda:
-        raise TypeError(f"{what}: expected a CUDA tensor")
-    _same_device(t, what, device)
+    if t.get_device() != device:
+        _wrong_device(t, what, device)
     rows, cols = shape
     ld, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{what}: the values of a row must be contiguous")
+    if cols > _INT32_MAX:  # the library's type: ctypes would cut it to its low 32 bits
+        raise ValueError(f"the rows of {what} have {cols} values, more than 2^31 - 1")
     if rows <= 1:
         ld = max(ld, cols, 1)  # one row: any stride
     elif ld < cols:
@@ -89,31 +96,25 @@ def _matrix(t, what: str, device):
     return t.data_ptr(), ld, rows, cols
 
 
-_INT32_MAX = 2 ** 31 - 1
-
-
-def _row_length(cols: int, what: str) -> int:
-    """A row's length as the library takes it: ctypes would cut a larger one to its low 32 bits."""
-    if cols > _INT32_MAX:
-        raise ValueError(f"the rows of {what} have {cols} values, more than 2^31 - 1")
-    return cols
-
-
 def _int(value: int, bits: int) -> int:
     """A number as a signed integer of that many bits, at its limit where it is past that (the library refuses it)."""
     return max(-(1 << bits - 1), min(int(value), (1 << bits - 1) - 1))
 
 
-def _vector(t, count: int, what: str, device, dtype: str = "float32", optional: bool = True):
+def _vector(t, count: int, what: str, device, code: int = RBF_DTYPE_F32, optional: bool = True):
     if t is None:
         if not optional:
             raise ValueError(f"{what} is required")
         return None
     if t.numel() != count:
         raise ValueError(f"{what} has {t.numel()} entries, expected {count}")
-    p = _dev_ptr(t, dtype)
-    _same_device(t, what, device)
-    return p
+    if t.get_device() != device:
+        _wrong_device(t, what, device)
+    if _DTYPES.get(t.dtype) != code:
+        raise TypeError(f"{what} is {t.dtype}: expected {'int32' if code == RBF_DTYPE_I32 else 'float32'}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
 def _same(got, want, what: str) -> None:
@@ -197,7 +198,7 @@ class Ops:
         x, ld_x, rows, cols, dtype = _float_matrix(d_x, "d_x", on)
         q, ld_q, q_rows, q_cols = _i8_matrix(d_q, "d_q", on)
         _same((q_rows, q_cols), (rows, cols), "the shape of d_q")
-        self._check(self.lib.quantize_rows_i8_dev(self._h, x, dtype, ld_x, rows, _row_length(cols, "d_x"), q, ld_q,
+        self._check(self.lib.quantize_rows_i8_dev(self._h, x, dtype, ld_x, rows, cols, q, ld_q,
                                                   _vector(d_scale, rows, "d_scale", on, optional=False)),
                     "quantize_rows_i8_dev")
 
@@ -208,7 +209,7 @@ class Ops:
         a, ld_a, m, k = _i8_matrix(d_a, "d_a", on)
         b, ld_b, n, b_cols = _i8_matrix(d_b, "d_b", on)
         out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", on, integers=True)
-        _same(b_cols, _row_length(k, "d_a"), "the depth of d_b")
+        _same(b_cols, k, "the depth of d_b")
         _same((out_rows, out_cols), (m, n), "the shape of d_out")
         self._check(self.lib.matmul_i8_dev(self._h, a, ld_a, _vector(d_a_scale, m, "d_a_scale", on), b, ld_b,
                                            _vector(d_b_scale, n, "d_b_scale", on), _vector(bias, n, "bias", on), out,
@@ -221,7 +222,7 @@ class Ops:
         x, ld_x, m, k, x_dtype = _float_matrix(d_x, "d_x", on)
         w, ld_w, n, w_cols = _i8_matrix(d_w, "d_w", on)
         out, ld_out, out_rows, out_cols, dtype = _float_matrix(d_out, "d_out", on)
-        _same(w_cols, _row_length(k, "d_x"), "the depth of d_w")
+        _same(w_cols, k, "the depth of d_w")
         _same((out_rows, out_cols), (m, n), "the shape of d_out")
         self._check(self.lib.linear_i8_dev(self._h, x, x_dtype, ld_x, w, ld_w,
                                            _vector(d_w_scale, n, "d_w_scale", on), _vector(bias, n, "bias", on), out,
@@ -234,11 +235,11 @@ class Ops:
         and top_k (int32): one entry a row, or None."""
         on = self._device
         x, ld, rows, vocab, dtype = _float_matrix(d_logits, "d_logits", on)
-        self._check(self.lib.sample_dev(self._h, x, dtype, ld, rows, _row_length(vocab, "d_logits"),
+        self._check(self.lib.sample_dev(self._h, x, dtype, ld, rows, vocab,
                                         _vector(d_u, rows, "d_u", on, optional=False),
                                         _vector(temperature, rows, "temperature", on),
-                                        _vector(top_k, rows, "top_k", on, "int32"),
+                                        _vector(top_k, rows, "top_k", on, RBF_DTYPE_I32),
                                         _vector(top_p, rows, "top_p", on),
                                         _vector(min_p, rows, "min_p", on),
-                                        _vector(d_token, rows, "d_token", on, "int32", optional=False),
+                                        _vector(d_token, rows, "d_token", on, RBF_DTYPE_I32, optional=False),
                                         _vector(d_logprob, rows, "d_logprob", on)), "sample_dev")
