@@ -103,12 +103,15 @@ rbf_status quantize_rows_i8_dev(rbf_ops* ops, const void* d_x, rbf_dtype x_dtype
  *   d_a        [m, k] int8, stride ld_a (queries or tokens); m <= max_rows
  *   d_a_scale  [m] fp32 (NULL: 1)
  *   d_b        [n, k] int8, stride ld_b (corpus rows, or a layer's output
- *              channels); from a 16-byte boundary and with ld_b a multiple of 16
- *              it goes through the tensor cores, else through a slower kernel
+ *              channels); fastest from a 16-byte boundary with ld_b a multiple
+ *              of 16: other rows are first put on such boundaries, up to 32 MB
+ *              at a time, in the handle's workspace (one more launch a part)
  *   d_b_scale  [n] fp32 (NULL: 1)
  *   d_bias     [n] fp32 (NULL: none)
  *   d_out      [m, n] of out_dtype, stride ld_out
- * k = 0 gives the bias (or zeros). k <= max_depth.
+ * Up to four tokens of up to 96 KB take one launch (dp4a), more a launch that
+ * expands them and the tensor cores' one; the sums are the same.
+ * k = 0: the sums are 0. k <= max_depth.
  * Errors: INVALID_VALUE, CUDA; a device-side timeout through
  * rbf_ops_check_device_error. */
 rbf_status matmul_i8_dev(rbf_ops* ops, const int8_t* d_a, int64_t ld_a, const float* d_a_scale, const int8_t* d_b,
@@ -128,7 +131,8 @@ rbf_status linear_i8_dev(rbf_ops* ops, const void* d_x, rbf_dtype x_dtype, int64
 /* Draw one index from each row of scores.
  *
  * With x the row's scores (a NaN counts as -infinity) and T its temperature,
- * index j has the weight 2^((x_j - max x) log2(e) / T), computed in fp32 and
+ * index j has the weight 2^((x_j - max x) log2(e) / T), computed in fp32 (log2(e) / T
+ * as a finite number above 0: at infinite T every finite score has the weight 1) and
  * held as a whole multiple of 2^-36, so that every sum of weights below is
  * exact and the result depends on no order of summation. In the order of
  * rbf.h (higher score first, on equal scores the lower index):

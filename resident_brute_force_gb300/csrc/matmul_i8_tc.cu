@@ -3,8 +3,9 @@
 //
 //   out[i, j] = a_scale[i] * b_scale[j] * sum_k a[i, k] b[j, k] + bias[j]
 //
-// sm_103a has no 8-bit integer tensor instruction (tcgen05 kind::i8 does not
-// assemble for it), but fp16 holds every 8-bit integer, and the product of two
+// tcgen05 takes no 8-bit integers on sm_103a (kind::i8 does not assemble for
+// it; the warp-level mma.sync of them does, at a rate that was not measured),
+// but fp16 holds every 8-bit integer, and the product of two
 // of them, up to 2^14, is exact in the fp32 accumulator as long as the running
 // sum stays within 2^24: for 1,024 products whatever their values, and for as
 // many stages of 128 as the largest sum of |a| over one of them allows (it is
@@ -45,12 +46,12 @@
 // another pair.
 //
 // What bounds it, measured: with 32 to 64 tokens b's bytes (1M x 768 to bf16:
-// 142 to 146 us, 114 for the bytes alone); with 128 and more the converting
+// 139 to 144 us, 114 for the bytes alone); with 128 and more the converting
 // warps and the tensor pipe together (4096 x 8192 x 4096 from bf16 182 us of any
 // bytes, 163 of the normally distributed ones, which draw less power: 1.51 and
 // 1.69 PFLOP/s); with 256 tokens and a shallow depth the one accumulator that
 // tensor memory has room for beside the ring, which is drained between tiles
-// (256 x 1M x 768 to bf16 289 us, 1.36 PFLOP/s, of a tile's 9,400 clocks some
+// (256 x 1M x 768 to bf16 286 us back to back, 1.38 PFLOP/s, of a tile's 9,400 clocks some
 // 3,200 from its last MMA to the next one's first).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

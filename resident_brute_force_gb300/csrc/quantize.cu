@@ -41,7 +41,8 @@ struct Out {
 // the second from cache. 200,000 x 65 bf16: 205 us with a CTA a row, 35 with a
 // warp; 100,000 x 333: 131 and 33. 30,000 x 2,500 (rows on 8-byte boundaries):
 // 84 us, 82 with a row's values kept in registers, which leaves fewer CTAs an
-// SM and costs longer and shorter rows a quarter.
+// SM and costs longer and shorter rows a quarter. 8,192 x 14,336, too wide for
+// the kernel below: 93 us, 52 for its bytes once.
 // J holds a column's number plus a step: unsigned for rows that end within a
 // step of 2^31, int for all others (as unsigned numbers 30,000 x 2,500 takes 96).
 template <typename T, int THREADS, typename J>
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kQuantThreads)
 // which stays in registers: one read of it and one write, eight values a
 // thread at a time. Rows start on 16-byte boundaries, int8 rows on 8-byte ones.
 // Bound by memory now that a value costs ten instructions (the magnitudes are
-// compared as T's own patterns, two a word): 16,384 x 8,192 bf16 59.8 us =
+// compared as T's own patterns, two a word): 16,384 x 8,192 bf16 60 us =
 // 6.73 TB/s, 0.99 of the copy rate (87.7 with fourteen instructions a value);
 // 200,000 x 1,024 89; 200,000 x 768 fp32 113; 65,536 x 4,096 bf16 131 (139 with
 // six CTAs an SM, the eight need 32 registers).

@@ -41,19 +41,23 @@
 // bins; scores that coincide by the thousand (no bins divide them) leave K to
 // be found by halving the interval of keys, one pass over the row a step.
 //
-// What bounds it: instructions (256 x 128,000 top_p: 73 a score, of which the
-// passes over scores that are on chip are about half, the rest the fixed part
-// of a CTA), the shared-memory atomics of the counts (11 to 14 lanes a clock
-// and SM), and
+// What bounds it: with top_p, instructions for half of the time (256 x 128,000:
+// 73 a score, of which the passes over scores that are on chip are about half,
+// the rest the fixed part of a CTA) and barriers for most of the other half;
+// with no filter and with top_k (27 and 29 a score, 52 and 42 % of the issue
+// slots) the first read, whose waves have nothing else under way, and barriers;
+// with few rows latency (1 x 10,000: 22 % of the issue slots of two SMs; 8 x
+// 1,000,000 min_p, read again from L2: 27 %). The shared-memory atomics of the
+// counts go at 11 to 14 lanes a clock and SM, and there are
 // per row some ten exchanges across the cluster at 450 clocks each. The text
 // counts too: the kernel is 150 to 177 KB, more than the instruction cache, and
 // passes that few rows take are loops over single scores (with every loop
 // unrolled it was 296 to 432 KB; 256 x 128,000 top_p from cold 143 us, now 133,
 // top_k 700 with top_p 230, now 124).
 // Measured (us, the bytes alone at the copy rate in brackets): 1 x 10,000 fp32
-// top_k + top_p 14 (0.006); 61 x 100,003 bf16 top_p 39 (1.8); 256 x 128,000 bf16
-// top_p 124, top_k <= 100 62, top_k 5,000-9,000 115, neither 43 (9.7);
-// 8 x 1,000,000 fp32 min_p 25, top_p 68 (4.7).
+// top_k + top_p 12 to 14 (0.006); 61 x 100,003 bf16 top_p 39 (1.8); 256 x 128,000
+// bf16 top_p 124, top_k <= 100 62, top_k 5,000-9,000 115, neither 43.5, best index
+// 35 (9.6); 8 x 1,000,000 fp32 min_p 25, top_p 66 (4.7).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
