@@ -18,6 +18,7 @@ from ._binding import (  # noqa: F401
     RBF_OPT_TIMEOUT_NS, RBF_OPT_SCHEDULE, RBF_OPT_BATCH_SAMPLE, RBF_OPT_HOST_READ, FAULT_COPY, FAULT_LAUNCH,
 )
 from .ops import (  # noqa: F401
-    Ops, RBF_DTYPE_F32, RBF_DTYPE_BF16, RBF_DTYPE_F16, RBF_DTYPE_I32, RBF_OPS_MAX_DEPTH, RBF_OPS_MAX_VOCAB,
+    Ops, RBF_DTYPE_F32, RBF_DTYPE_BF16, RBF_DTYPE_F16, RBF_DTYPE_I32, RBF_DTYPE_E4M3, RBF_DTYPE_E5M2, RBF_OPS_MAX_DEPTH,
+    RBF_OPS_MAX_VOCAB, RBF_OPS_MAX_DRAFTS, RBF_OPS_MAX_TEACHER,
 )
 from ._build import build  # noqa: F401

@@ -24,7 +24,7 @@ CHECKS_LIB_PATH = os.path.join(HERE, "librbf_checks.so")
 
 SOURCES = ["engine.cu", "score_select.cu", "merge.cu", "topk_i32.cu", "noalloc.cu", "gemm_select.cu", "normalize.cu",
            "ops.cu", "quantize.cu", "matmul_i8.cu", "matmul_i8_tc.cu", "matmul_i8_few.cu",
-           "sample.cu"]
+           "sample.cu", "quantize_f8.cu", "matmul_f8.cu", "verify.cu", "distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -33,6 +33,7 @@ struct rbf_ops {
   // uses one of them out of turn; what it then finds is a larger bound, no smaller one.
   unsigned* block_l1 = nullptr;
   int turn = 0;
+  VerifyPart* parts = nullptr;   // verify_dev: what parts of rows say, verify_max_parts
   int8_t* staged = nullptr;      // rows of b put on 16-byte boundaries, kStagedBytes
   int* errw = nullptr;           // error bits of the kernels since the last check
   uint64_t timeout_ns = 2000000000ull;  // bound on every device-side wait
@@ -95,6 +96,7 @@ void release(rbf_ops* o) {
   cudaFree(o->arrived);
   cudaFree(o->block_l1);
   cudaFree(o->staged);
+  cudaFree(o->parts);
   cudaFree(o->errw);
   if (o->own_stream && o->stream) cudaStreamDestroy(o->stream);
   delete o;
@@ -112,6 +114,10 @@ bool matrix_ok(const void* p, int elem, int64_t rows, int64_t cols, int64_t ld) 
   if (!p || !aligned(p, elem)) return false;
   return ld <= (INT64_MAX / 8) / std::max<int64_t>(rows, 1);
 }
+
+bool f8_dtype(rbf_dtype t) { return t == RBF_DTYPE_E4M3 || t == RBF_DTYPE_E5M2; }
+
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
 
 bool floats_ok(const void* p) { return !p || aligned(p, 4); }
 
@@ -207,6 +213,7 @@ rbf_status rbf_ops_create(int64_t max_rows, int32_t max_depth, void* cuda_stream
                   cudaMalloc(&o->row_scale, static_cast<size_t>(max_rows) * sizeof(float)) == cudaSuccess &&
                   cudaMalloc(&o->block_l1, 2 * sizeof(unsigned)) == cudaSuccess &&
                   cudaMalloc(&o->staged, kStagedBytes) == cudaSuccess &&
+                  cudaMalloc(&o->parts, static_cast<size_t>(verify_max_parts(max_rows, o->num_sms)) * sizeof(VerifyPart)) == cudaSuccess &&
                   cudaMalloc(&o->errw, 4 * sizeof(int)) == cudaSuccess;
   if (!ok) {
     cudaGetLastError();
@@ -391,6 +398,156 @@ rbf_status sample_dev(rbf_ops* o, const void* d_logits, rbf_dtype dtype, int64_t
   a.token = d_token;
   a.logprob = d_logprob;
   OPS_LAUNCH(o, launch_sample(a, o->stream));
+  return RBF_OK;
+}
+
+rbf_status quantize_f8_dev(rbf_ops* o, const void* d_x, rbf_dtype x_dtype, int64_t ld_x, int64_t rows, int32_t cols,
+                           int32_t block_rows, void* d_q, rbf_dtype q_dtype, int64_t ld_q, float* d_scale,
+                           int64_t ld_scale) {
+  if (!o || !float_dtype(x_dtype) || !f8_dtype(q_dtype) || rows < 0 || cols < 0 || rows > INT32_MAX ||
+      (block_rows != 1 && block_rows != 128))
+    return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
+  const int64_t scale_rows = block_rows == 1 ? rows : blocks_of(rows);
+  if (!matrix_ok(d_x, dtype_bytes(x_dtype), rows, cols, ld_x) || !matrix_ok(d_q, 1, rows, cols, ld_q) ||
+      !matrix_ok(d_scale, 4, scale_rows, blocks_of(cols), ld_scale))
+    return RBF_ERR_INVALID_VALUE;
+  if (rows == 0 || cols == 0) return RBF_OK;
+  QuantizeF8Launch a;
+  a.x = d_x;
+  a.dtype = x_dtype;
+  a.ld_x = ld_x;
+  a.rows = rows;
+  a.cols = cols;
+  a.block_rows = block_rows;
+  a.q = d_q;
+  a.q_dtype = q_dtype;
+  a.ld_q = ld_q;
+  a.scale = d_scale;
+  a.ld_scale = ld_scale;
+  OPS_LAUNCH(o, launch_quantize_f8(a, o->num_sms, o->stream));
+  return RBF_OK;
+}
+
+rbf_status matmul_f8_dev(rbf_ops* o, const void* d_a, rbf_dtype a_dtype, int64_t ld_a, const float* d_a_scale,
+                         int64_t ld_a_scale, const void* d_b, rbf_dtype b_dtype, int64_t ld_b, const float* d_b_scale,
+                         int64_t ld_b_scale, int32_t block_rows, const float* d_bias, void* d_out, rbf_dtype out_dtype,
+                         int64_t ld_out, int64_t m, int64_t n, int32_t k) {
+  if (!o || !f8_dtype(a_dtype) || !f8_dtype(b_dtype) || !float_dtype(out_dtype) || (block_rows != 1 && block_rows != 128))
+    return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
+  if (m < 0 || n < 0 || k < 0 || m > o->max_rows || n > INT32_MAX || k > o->max_depth) return RBF_ERR_INVALID_VALUE;
+  const int64_t b_scale_rows = block_rows == 1 ? n : blocks_of(n);
+  if (!matrix_ok(d_a, 1, m, k, ld_a) || !matrix_ok(d_b, 1, n, k, ld_b) ||
+      !matrix_ok(d_out, dtype_bytes(out_dtype), m, n, ld_out) || !matrix_ok(d_a_scale, 4, m, blocks_of(k), ld_a_scale) ||
+      !matrix_ok(d_b_scale, 4, b_scale_rows, blocks_of(k), ld_b_scale) || !floats_ok(d_bias))
+    return RBF_ERR_INVALID_VALUE;
+  if (m == 0 || n == 0) return RBF_OK;
+  MatmulF8Launch a;
+  a.a = static_cast<const uint8_t*>(d_a);
+  a.a_dtype = a_dtype;
+  a.ld_a = ld_a;
+  a.a_scale = d_a_scale;
+  a.ld_a_scale = ld_a_scale;
+  a.b = static_cast<const uint8_t*>(d_b);
+  a.b_dtype = b_dtype;
+  a.ld_b = ld_b;
+  a.b_scale = d_b_scale;
+  a.ld_b_scale = ld_b_scale;
+  a.block_rows = block_rows;
+  a.bias = d_bias;
+  a.out = d_out;
+  a.out_dtype = out_dtype;
+  a.ld_out = ld_out;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  OPS_LAUNCH(o, launch_matmul_f8(a, o->stream));
+  return RBF_OK;
+}
+
+rbf_status verify_dev(rbf_ops* o, const void* d_target, int64_t ld_target_seq, int64_t ld_target, const void* d_draft,
+                      int64_t ld_draft_seq, int64_t ld_draft, rbf_dtype dtype, int64_t seqs, int32_t drafts,
+                      int32_t vocab, const int32_t* d_draft_token, const int32_t* d_draft_count, const float* d_u,
+                      const float* d_temperature, int32_t* d_token, int32_t* d_accepted, float* d_logprob) {
+  if (!o || !float_dtype(dtype) || seqs < 0 || drafts < 0 || drafts > RBF_OPS_MAX_DRAFTS || vocab < 0 ||
+      vocab > RBF_OPS_MAX_VOCAB)
+    return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
+  if (seqs > o->max_rows / (drafts + 1)) return RBF_ERR_INVALID_VALUE;
+  if (seqs == 0) return RBF_OK;
+  const int elem = dtype_bytes(dtype);
+  // Places of a sequence are rows, sequences rows of those.
+  if (!matrix_ok(d_target, elem, drafts + 1, vocab, ld_target) ||
+      !matrix_ok(d_target, elem, seqs, std::min<int64_t>(vocab, 1) * (drafts * ld_target + vocab), ld_target_seq))
+    return RBF_ERR_INVALID_VALUE;
+  if (d_draft && (!matrix_ok(d_draft, elem, drafts, vocab, ld_draft) ||
+                  !matrix_ok(d_draft, elem, seqs, std::min<int64_t>(vocab, 1) * std::min(drafts, 1) * ((drafts - 1) * ld_draft + vocab), ld_draft_seq)))
+    return RBF_ERR_INVALID_VALUE;
+  if ((drafts > 0 && !d_draft_token) || !d_u || !d_token || !d_accepted || !floats_ok(d_draft_token) ||
+      !floats_ok(d_draft_count) || !floats_ok(d_u) || !floats_ok(d_temperature) || !floats_ok(d_token) ||
+      !floats_ok(d_accepted) || !floats_ok(d_logprob))
+    return RBF_ERR_INVALID_VALUE;
+  VerifyLaunch a;
+  a.target = d_target;
+  a.ld_target_seq = ld_target_seq;
+  a.ld_target = ld_target;
+  a.draft = drafts > 0 ? d_draft : nullptr;
+  a.ld_draft_seq = ld_draft_seq;
+  a.ld_draft = ld_draft;
+  a.dtype = dtype;
+  a.seqs = seqs;
+  a.drafts = drafts;
+  a.vocab = vocab;
+  a.draft_token = d_draft_token;
+  a.count = d_draft_count;
+  a.u = d_u;
+  a.temperature = d_temperature;
+  a.token = d_token;
+  a.accepted = d_accepted;
+  a.logprob = d_logprob;
+  OPS_LAUNCH(o, launch_verify_stats(a, o->parts, verify_max_parts(o->max_rows, o->num_sms), o->num_sms, o->stream));
+  OPS_LAUNCH(o, launch_verify_draw(a, o->parts, verify_max_parts(o->max_rows, o->num_sms), o->num_sms, o->stream));
+  return RBF_OK;
+}
+
+rbf_status distill_dev(rbf_ops* o, const void* d_scores, rbf_dtype dtype, int64_t ld_scores, int64_t rows, int32_t vocab,
+                       const int32_t* d_index, int64_t ld_index, const void* d_teacher, rbf_dtype teacher_dtype,
+                       int64_t ld_teacher, int32_t k, const float* d_rest, const float* d_weight, float temperature,
+                       float* d_loss, void* d_grad, int64_t ld_grad) {
+  if (!o || !float_dtype(dtype) || !float_dtype(teacher_dtype) || rows < 0 || rows > INT32_MAX || vocab < 0 ||
+      vocab > RBF_OPS_MAX_VOCAB || k < 0 || k > RBF_OPS_MAX_TEACHER || !(temperature >= 0x1p-20f && temperature <= 0x1p20f))
+    return RBF_ERR_INVALID_VALUE;
+  o->launches = 0;
+  if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
+  const int elem = dtype_bytes(dtype);
+  if (!matrix_ok(d_scores, elem, rows, vocab, ld_scores) || (d_grad && !matrix_ok(d_grad, elem, rows, vocab, ld_grad)) ||
+      !matrix_ok(d_index, 4, rows, k, ld_index) || !matrix_ok(d_teacher, dtype_bytes(teacher_dtype), rows, k, ld_teacher))
+    return RBF_ERR_INVALID_VALUE;
+  if (!floats_ok(d_rest) || !floats_ok(d_weight) || !floats_ok(d_loss)) return RBF_ERR_INVALID_VALUE;
+  if (rows == 0 || (!d_loss && !d_grad)) return RBF_OK;
+  DistillLaunch a;
+  a.scores = d_scores;
+  a.dtype = dtype;
+  a.ld_scores = ld_scores;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.index = d_index;
+  a.ld_index = ld_index;
+  a.teacher = d_teacher;
+  a.teacher_dtype = teacher_dtype;
+  a.ld_teacher = ld_teacher;
+  a.k = k;
+  a.rest = d_rest;
+  a.weight = d_weight;
+  a.temperature = temperature;
+  a.loss = d_loss;
+  a.grad = d_grad;
+  a.ld_grad = ld_grad;
+  OPS_LAUNCH(o, launch_distill(a, o->errw, o->timeout_ns, o->num_sms, o->stream));
   return RBF_OK;
 }
 

@@ -13,6 +13,8 @@ constexpr int kBF16 = 1;
 constexpr int kF16 = 2;
 constexpr int kI32 = 3;
 constexpr int kI8 = 4;  // internal: the tokens of matmul_i8_dev
+constexpr int kE4M3 = 5;
+constexpr int kE5M2 = 6;
 
 inline int dtype_bytes(int dtype) { return dtype == kF32 || dtype == kI32 ? 4 : 2; }
 
@@ -100,5 +102,96 @@ struct SampleLaunch {
   float* logprob = nullptr;
 };
 cudaError_t launch_sample(const SampleLaunch& a, cudaStream_t stream);
+
+// Rows to 8-bit floating point, a scale for each 128 values of block_rows (1 or 128) rows.
+struct QuantizeF8Launch {
+  const void* x = nullptr;
+  int dtype = 0;
+  int64_t ld_x = 0;
+  int64_t rows = 0;
+  int cols = 0;
+  int block_rows = 1;
+  void* q = nullptr;
+  int q_dtype = 0;
+  int64_t ld_q = 0;
+  float* scale = nullptr;
+  int64_t ld_scale = 0;
+};
+cudaError_t launch_quantize_f8(const QuantizeF8Launch& a, int num_sms, cudaStream_t stream);
+
+// out[i, j] = sum_c a_scale[i, c] b_scale[j / block_rows, c] sum_{k in block c} a[i, k] b[j, k] + bias[j].
+struct MatmulF8Launch {
+  const uint8_t* a = nullptr;
+  int a_dtype = 0;
+  int64_t ld_a = 0;
+  const float* a_scale = nullptr;
+  int64_t ld_a_scale = 0;
+  const uint8_t* b = nullptr;
+  int b_dtype = 0;
+  int64_t ld_b = 0;
+  const float* b_scale = nullptr;
+  int64_t ld_b_scale = 0;
+  int block_rows = 1;
+  const float* bias = nullptr;
+  void* out = nullptr;
+  int out_dtype = 0;
+  int64_t ld_out = 0;
+  int64_t m = 0;
+  int64_t n = 0;
+  int k = 0;
+};
+cudaError_t launch_matmul_f8(const MatmulF8Launch& a, cudaStream_t stream);
+
+// Drafted tokens checked against the target's scores, and the answer after them.
+struct VerifyLaunch {
+  const void* target = nullptr;  // [seqs, drafts + 1, vocab]
+  int64_t ld_target_seq = 0, ld_target = 0;
+  const void* draft = nullptr;   // [seqs, drafts, vocab], or none
+  int64_t ld_draft_seq = 0, ld_draft = 0;
+  int dtype = 0;
+  int64_t seqs = 0;
+  int drafts = 0;
+  int vocab = 0;
+  const int32_t* draft_token = nullptr;
+  const int32_t* count = nullptr;
+  const float* u = nullptr;
+  const float* temperature = nullptr;
+  int32_t* token = nullptr;
+  int32_t* accepted = nullptr;
+  float* logprob = nullptr;
+};
+// What a part of a row says: its largest score and the sum of its weights, or
+// the key of its best index.
+struct VerifyPart {
+  float top, z;
+  unsigned long long key;
+};
+int64_t verify_max_parts(int64_t max_rows, int num_sms);  // for up to 2 max_rows rows: at least two each
+// The rows' sums, then the accepted tokens and the draw (enqueued just behind it).
+cudaError_t launch_verify_stats(const VerifyLaunch& a, VerifyPart* parts, int64_t max_parts, int num_sms, cudaStream_t stream);
+cudaError_t launch_verify_draw(const VerifyLaunch& a, const VerifyPart* parts, int64_t max_parts, int num_sms, cudaStream_t stream);
+
+// Distillation from a teacher's best logits.
+struct DistillLaunch {
+  const void* scores = nullptr;
+  int dtype = 0;
+  int64_t ld_scores = 0;
+  int64_t rows = 0;
+  int vocab = 0;
+  const int32_t* index = nullptr;
+  int64_t ld_index = 0;
+  const void* teacher = nullptr;
+  int teacher_dtype = 0;
+  int64_t ld_teacher = 0;
+  int k = 0;
+  const float* rest = nullptr;
+  const float* weight = nullptr;
+  float temperature = 1.0f;
+  float* loss = nullptr;
+  void* grad = nullptr;
+  int64_t ld_grad = 0;
+};
+constexpr int kMaxTeacher = 1024;  // entries of a row
+cudaError_t launch_distill(const DistillLaunch& a, int* err, uint64_t timeout_ns, int num_sms, cudaStream_t stream);
 
 }  // namespace rbf

@@ -1,0 +1,233 @@
+// quantize_f8.cu -- rows to 8-bit floating point with a scale for each block of
+// 128 values of a row, or of 128 x 128 (include/rbf_ops.h, quantize_f8_dev).
+//
+// With t = max |x| over the block and MAX the type's largest number:
+//   scale = t * (1 / MAX),  q = x * ((1 / t) * MAX) rounded to the nearest 8-bit number,
+// in fp32, each step rounded as IEEE says, so that the bytes are the same
+// wherever they are computed. |x| times the factor is at most MAX (1 + 2^-22), which
+// rounds to MAX. A block so small that the factor passes 2^127 takes that and 2^-127.
+//
+// One pass: a block is held in registers between its maximum and its rounding.
+// Blocks of a row: 16 lanes (fp32: 32) a block, 16 bytes a lane, four blocks a
+// lane under way. Blocks of 128 x 128: a CTA each, 32 KB (fp32: 64) in its
+// threads' registers. What bounds it: HBM.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "ops_internal.h"
+#include "rbf_device.cuh"
+
+namespace rbf {
+namespace {
+
+constexpr int kBlock = 128;
+
+template <typename T>
+constexpr int kLen = 16 / sizeof(T);  // values of a lane's 16 bytes
+
+// Magnitudes as their fp32 patterns: ordered as unsigned integers, the
+// infinities and the NaNs on top.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+struct BlockScale {
+  float scale, inv;
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t code, float top) {
+  BlockScale s;
+  if (code >= 0x7F800000u) {  // a NaN or an infinity: zeros, and a scale that makes every product NaN
+    s.scale = __uint_as_float(0x7FC00000u);
+    s.inv = 0.0f;
+  } else if (code == 0) {
+    s.scale = s.inv = 0.0f;
+  } else {
+    const float t = __uint_as_float(code);
+    s.inv = __fmul_rn(__fdiv_rn(1.0f, t), top);
+    s.scale = __fmul_rn(t, __fdiv_rn(1.0f, top));
+    if (s.inv > 0x1p127f) {
+      s.inv = 0x1p127f;
+      s.scale = 0x1p-127f;
+    }
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[kLen<T>]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// kLen values from column c on of a row of `cols` (0 past it).
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T* row, int c, int cols, bool wide) {
+  if (wide && c + kLen<T> <= cols) return __ldcs(reinterpret_cast<const uint4*>(row + c));
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int i = 0; i < kLen<T>; ++i)
+    if (c + i < cols) e[i] = row[c + i];
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t piece_top(const uint4& v) {
+  float x[kLen<T>];
+  unpack<T>(v, x);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kLen<T>; ++i) m = max(m, magnitude(x[i]));
+  return m;
+}
+
+template <typename T, __nv_fp8_interpretation_t F8>
+__device__ __forceinline__ void store_piece(uint8_t* row, int c, int cols, bool wide, const uint4& v, float inv) {
+  float x[kLen<T>];
+  unpack<T>(v, x);
+  uint16_t h[kLen<T> / 2];
+#pragma unroll
+  for (int i = 0; i < kLen<T> / 2; ++i) {
+    const float a = inv != 0.0f ? __fmul_rn(x[2 * i], inv) : 0.0f, b = inv != 0.0f ? __fmul_rn(x[2 * i + 1], inv) : 0.0f;
+    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, F8);
+  }
+  if (wide && c + kLen<T> <= cols) {
+    if constexpr (kLen<T> == 8)
+      *reinterpret_cast<uint2*>(row + c) = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+    else
+      *reinterpret_cast<uint32_t*>(row + c) = h[0] | static_cast<uint32_t>(h[1]) << 16;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kLen<T>; ++i)
+    if (c + i < cols) row[c + i] = static_cast<uint8_t>(h[i / 2] >> (8 * (i & 1)));
+}
+
+// Whether a matrix' rows start on boundaries of `bytes`.
+__device__ __forceinline__ bool rows_on(const void* p, int64_t ld_bytes, int bytes) {
+  return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes)) & static_cast<uintptr_t>(bytes - 1)) == 0;
+}
+
+constexpr int kThreads = 256;
+
+template <typename T, __nv_fp8_interpretation_t F8>
+__global__ void __launch_bounds__(kThreads) quantize_f8_rows_kernel(const QuantizeF8Launch a, float top) {
+  constexpr int kLanes = kBlock / kLen<T>;  // of a block
+  constexpr int kAhead = 4;                 // blocks a lane
+  const T* x = static_cast<const T*>(a.x);
+  uint8_t* q = static_cast<uint8_t*>(a.q);
+  const bool wide_x = rows_on(x, a.ld_x * static_cast<int64_t>(sizeof(T)), 16), wide_q = rows_on(q, a.ld_q, kLen<T>);
+  const int per = (a.cols + kBlock - 1) / kBlock;
+  const int64_t all = a.rows * per;
+  const int sub = threadIdx.x % kLanes;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / kLanes);
+  for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes; b0 - threadIdx.x / kLanes < all;
+       b0 += stride * kAhead) {
+    uint4 v[kAhead];
+    int64_t row[kAhead];
+    int col[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t b = b0 + stride * j;
+      row[j] = b < all ? b / per : -1;
+      col[j] = static_cast<int>(b - row[j] * per) * kBlock + sub * kLen<T>;
+      v[j] = row[j] < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_piece(x + row[j] * a.ld_x, col[j], a.cols, wide_x);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      uint32_t m = piece_top<T>(v[j]);
+#pragma unroll
+      for (int d = kLanes / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, d));
+      const BlockScale s = block_scale(m, top);
+      if (row[j] < 0) continue;
+      store_piece<T, F8>(q + row[j] * a.ld_q, col[j], a.cols, wide_q, v[j], s.inv);
+      if (sub == 0) a.scale[row[j] * a.ld_scale + col[j] / kBlock] = s.scale;
+    }
+  }
+}
+
+template <typename T, __nv_fp8_interpretation_t F8>
+__global__ void __launch_bounds__(kThreads) quantize_f8_blocks_kernel(const QuantizeF8Launch a, float top) {
+  constexpr int kLanes = kBlock / kLen<T>;
+  constexpr int kRows = kThreads / kLanes;    // of a pass
+  constexpr int kPasses = kBlock / kRows;
+  __shared__ uint32_t part[kThreads / 32];
+  const T* x = static_cast<const T*>(a.x);
+  uint8_t* q = static_cast<uint8_t*>(a.q);
+  const bool wide_x = rows_on(x, a.ld_x * static_cast<int64_t>(sizeof(T)), 16), wide_q = rows_on(q, a.ld_q, kLen<T>);
+  const int per = (a.cols + kBlock - 1) / kBlock;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x / per) * kBlock + threadIdx.x / kLanes;
+  const int c = static_cast<int>(blockIdx.x % per) * kBlock + static_cast<int>(threadIdx.x % kLanes) * kLen<T>;
+  uint4 v[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t r = r0 + p * kRows;
+    v[p] = r < a.rows ? load_piece(x + r * a.ld_x, c, a.cols, wide_x) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) m = max(m, piece_top<T>(v[p]));
+  m = __reduce_max_sync(kFullMask, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) m = max(m, part[w]);
+  const BlockScale s = block_scale(m, top);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t r = r0 + p * kRows;
+    if (r < a.rows) store_piece<T, F8>(q + r * a.ld_q, c, a.cols, wide_q, v[p], s.inv);
+  }
+  if (threadIdx.x == 0) a.scale[static_cast<int64_t>(blockIdx.x / per) * a.ld_scale + blockIdx.x % per] = s.scale;
+}
+
+template <typename T, __nv_fp8_interpretation_t F8>
+cudaError_t launch_t(const QuantizeF8Launch& a, int num_sms, cudaStream_t st) {
+  const float top = F8 == __NV_E4M3 ? 448.0f : 57344.0f;
+  const int per = (a.cols + kBlock - 1) / kBlock;
+  if (a.block_rows == 1) {
+    const int64_t of_cta = kThreads / (kBlock / kLen<T>);
+    const int64_t ctas = std::min<int64_t>((a.rows * per + of_cta - 1) / of_cta, int64_t(num_sms) * 8);
+    quantize_f8_rows_kernel<T, F8><<<static_cast<unsigned>(ctas), kThreads, 0, st>>>(a, top);
+  } else {
+    // Rows past what one grid takes go in parts of whole blocks.
+    const int64_t most = (int64_t(1) << 30) / per * kBlock;
+    for (int64_t r = 0; r < a.rows; r += most) {
+      QuantizeF8Launch p = a;
+      p.rows = std::min(most, a.rows - r);
+      p.x = static_cast<const T*>(a.x) + r * a.ld_x;
+      p.q = static_cast<uint8_t*>(a.q) + r * a.ld_q;
+      p.scale = a.scale + r / kBlock * a.ld_scale;
+      quantize_f8_blocks_kernel<T, F8><<<static_cast<unsigned>((p.rows + kBlock - 1) / kBlock * per), kThreads, 0, st>>>(p, top);
+    }
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_f8(const QuantizeF8Launch& a, int num_sms, cudaStream_t st) {
+  return a.q_dtype == kE4M3 ? launch_t<T, __NV_E4M3>(a, num_sms, st) : launch_t<T, __NV_E5M2>(a, num_sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_f8(const QuantizeF8Launch& a, int num_sms, cudaStream_t st) {
+  if (a.dtype == kF32) return launch_f8<float>(a, num_sms, st);
+  if (a.dtype == kBF16) return launch_f8<__nv_bfloat16>(a, num_sms, st);
+  return launch_f8<__half>(a, num_sms, st);
+}
+
+}  // namespace rbf
