@@ -464,7 +464,53 @@ rbf_status matmul_f8_dev(rbf_ops* o, const void* d_a, rbf_dtype a_dtype, int64_t
   a.m = m;
   a.n = n;
   a.k = k;
-  OPS_LAUNCH(o, launch_matmul_f8(a, o->stream));
+  if (k == 0) {
+    MatmulI8Launch none;  // the bias, or zeros
+    none.bias = d_bias;
+    none.out = d_out;
+    none.out_dtype = out_dtype;
+    none.ld_out = ld_out;
+    none.m = m;
+    none.n = n;
+    OPS_LAUNCH(o, launch_matmul_i8_empty(none, o->num_sms, o->stream));
+    return RBF_OK;
+  }
+  MatmulF8Workspace w;
+  w.partial = reinterpret_cast<float*>(o->partial);
+  w.arrived = o->arrived;
+  w.err = o->errw;
+  w.num_sms = o->num_sms;
+  w.timeout_ns = o->timeout_ns;
+  const int pitch = (k + 15) / 16 * 16;
+  if (m == 1) a.ld_a = pitch;
+  if (!aligned(a.a, 16) || a.ld_a % 16 != 0) {
+    // The product's other room for rows of a: max_rows x max_depth 16-bit numbers.
+    OPS_LAUNCH(o, launch_pitch_rows(reinterpret_cast<const int8_t*>(a.a), a.ld_a, m, k, static_cast<int8_t*>(o->rows_f16), pitch,
+                                    o->num_sms, o->stream));
+    a.a = static_cast<const uint8_t*>(o->rows_f16);
+    a.ld_a = pitch;
+  }
+  // As many rows of b as a launch takes and, where they do not start on 16-byte
+  // boundaries, as the room holds in which they are put on them.
+  const bool staged = !aligned(d_b, 16) || (n > 1 && ld_b % 16 != 0);
+  int64_t most = std::min(n, matmul_f8_rows(m, k));
+  if (staged) most = std::min<int64_t>(most, static_cast<int64_t>(kStagedBytes / pitch / 256 * 256));
+  for (int64_t j = 0; j < n; j += most) {
+    MatmulF8Launch part = a;
+    part.n = std::min(most, n - j);
+    part.b = a.b + j * ld_b;
+    part.b_scale = d_b_scale + j / block_rows * ld_b_scale;
+    part.bias = d_bias ? d_bias + j : nullptr;
+    part.out = static_cast<char*>(d_out) + j * dtype_bytes(out_dtype);
+    if (staged) {
+      OPS_LAUNCH(o, launch_pitch_rows(reinterpret_cast<const int8_t*>(part.b), ld_b, part.n, k, o->staged, pitch, o->num_sms, o->stream));
+      part.b = reinterpret_cast<const uint8_t*>(o->staged);
+      part.ld_b = pitch;
+    } else if (n == 1) {
+      part.ld_b = pitch;
+    }
+    OPS_LAUNCH(o, launch_matmul_f8(part, w, o->stream));
+  }
   return RBF_OK;
 }
 

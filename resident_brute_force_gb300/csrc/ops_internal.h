@@ -140,7 +140,16 @@ struct MatmulF8Launch {
   int64_t n = 0;
   int k = 0;
 };
-cudaError_t launch_matmul_f8(const MatmulF8Launch& a, cudaStream_t stream);
+// Both operands' rows start on 16-byte boundaries (one row: any stride).
+struct MatmulF8Workspace {
+  float* partial = nullptr;     // matmul_i8_partial_bytes
+  unsigned* arrived = nullptr;  // num_sms counters, zero between launches
+  int* err = nullptr;
+  int num_sms = 0;
+  uint64_t timeout_ns = 0;
+};
+int64_t matmul_f8_rows(int64_t m, int k);  // most rows of b that one launch takes
+cudaError_t launch_matmul_f8(const MatmulF8Launch& a, const MatmulF8Workspace& w, cudaStream_t stream);
 
 // Drafted tokens checked against the target's scores, and the answer after them.
 struct VerifyLaunch {

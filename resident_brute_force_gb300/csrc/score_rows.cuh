@@ -9,11 +9,10 @@
 
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "rbf_device.cuh"
 
 namespace rbf {
-
-using u64 = unsigned long long;
 
 template <typename T>
 struct Vec;  // 16 bytes of scores
@@ -114,25 +113,6 @@ struct Row {
   }
 };
 
-// Two fp32 numbers in a register pair, one instruction for both, each rounded
-// as the single instruction rounds.
-__device__ __forceinline__ u64 pack2(float a, float b) {
-  u64 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float low2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float high2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float ex2(float z) {  // exp2f where the result is not subnormal, 0 there
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
