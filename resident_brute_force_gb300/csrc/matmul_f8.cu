@@ -55,7 +55,7 @@ constexpr int kSplitCost = NT <= 64 ? 20 : 32;
 // OUT: what is stored: 1 fp32, 2 bf16, 3 fp16.
 template <int NT, int OUT>
 struct Shape {
-  static constexpr int kGroups = NT >= 64 ? 4 : 2;         // of four workers: each takes a part of the tokens
+  static constexpr int kGroups = NT >= 128 ? 4 : 2;        // of four workers: each takes a part of the tokens
   static constexpr int kWorkers = 4 * kGroups;
   static constexpr int kThreads = (kFirstWorker + kWorkers) * 32;
   // A worker with 64 sums needs more than an equal share of the registers: the
@@ -63,12 +63,11 @@ struct Shape {
   static constexpr bool kMoveRegs = NT == 256;
   static constexpr int kLaunchRegs = 96, kControlRegs = 56, kWorkerRegs = 104;
   static_assert(!kMoveRegs || kControlRegs * 128 + kWorkerRegs * kWorkers * 32 <= kLaunchRegs * kThreads, "registers of the launch");
-  static constexpr int kBuffers = NT == 256 ? 1 : 2;       // slabs in registers
   static constexpr int kXBytes = NT / 2 * kDepth;
   static constexpr int kStage = kWBytes + kXBytes;
   static constexpr int kAcc = NT == 256 ? 2 : 4;           // accumulators
   static constexpr int kCols = NT / kGroups;               // tokens of a worker
-  static constexpr int kSlab = 16;                          // of those, read at a time
+  static constexpr int kSlab = 16;                         // of those, read at a time
   static_assert(kCols % kSlab == 0, "whole slabs");
   static constexpr int kOutTokens = kCols < 32 ? kCols : 32;  // 16-bit results in shared memory at a time
   static constexpr int kStageOut = OUT >= 2 ? kOutTokens * 64 : 0;  // of a worker: 32 channels x 16 bits a token
@@ -92,7 +91,6 @@ struct Params {
   int64_t ld_out;
   int64_t m, n;
   uint32_t formats;  // of the instruction descriptor
-  int by_channel;    // 1: every channel has scales of its own
   int stages;        // per tile
   int token_tiles;
   int tiles;         // tiles x stages < 2^31
@@ -115,11 +113,38 @@ __device__ __forceinline__ void umma_pair_f8(uint32_t d_tmem, uint64_t adesc, ui
       : "memory");
 }
 
+// 16 columns of the warp's 32 TMEM lanes, the load and its wait in one: a
+// wait of its own would have to take all registers through itself, a move each.
+// As 8 x 8 blocks: registers 4 j, 4 j + 1 are columns 8 j + 2 (lane % 4) + {0, 1} of TMEM lane lane / 4,
+// 4 j + 2, 4 j + 3 of lane / 4 + 8, and 8 on the same of TMEM lanes 16 on.
+__device__ __forceinline__ void tmem_read_blocks(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      :
+        "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr), "r"(taddr + (16u << 16))
+      : "memory");
+}
+// A register a column.
+__device__ __forceinline__ void tmem_read_columns(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      :
+        "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // A worker's part of a tile: 32 channels from j0 on, tokens i0 .. of which `live`
-// exist. Its sums are in registers as the tensor memory gives them out, in pairs:
-//   OUT 1: lane = channel, pair i = tokens 2 i, 2 i + 1;
-//   OUT 2, 3: as the 8 x 8 blocks of a 16-bit matrix store: of 16 tokens, pair
-//     4 (q / 2) + 2 j + q % 2 is tokens 8 j + 2 (lane % 4) + {0, 1} of channel lane / 4 + 8 q.
+// exist. Its sums are in registers as the tensor memory gives them out:
+//   OUT 1: lane = channel, register = token;
+//   OUT 2, 3: as tmem_read_blocks gives them, the 8 x 8 blocks of a 16-bit matrix store:
+//     tokens 8 j + 2 (lane % 4) + {0, 1} of channels lane / 4 + 8 q.
 template <int NT, int OUT>
 struct Part {
   using S = Shape<NT, OUT>;
@@ -167,7 +192,7 @@ __device__ __forceinline__ void store_tokens(const Params& p, const CUtensorMap*
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float* of = acc + 2 * ((j / 2) * 8 + 4 * (q / 2) + 2 * (j & 1) + (q & 1));
+        const float* of = acc + 8 * j / S::kSlab * S::kSlab + q / 2 * (S::kSlab / 2) + j % (S::kSlab / 8) * 4 + (q & 1) * 2;
         const float v0 = __fadd_rn(of[0], t.add[q]), v1 = __fadd_rn(of[1], t.add[q]);
         if constexpr (OUT == 2) {
           const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
@@ -208,7 +233,8 @@ __device__ __forceinline__ void store_tokens(const Params& p, const CUtensorMap*
   }
 }
 
-template <int NT, int OUT>
+// BY_CHANNEL: every channel has scales of its own.
+template <int NT, int OUT, bool BY_CHANNEL>
 __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
     matmul_f8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                           const __grid_constant__ CUtensorMap tmap_out, const Params p) {
@@ -233,7 +259,7 @@ __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
   __shared__ int abort_flag;
   __shared__ unsigned last_flag[2];
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(kFullMask, static_cast<int>(threadIdx.x >> 5), 0);  // in a uniform register, and what follows from it
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -266,7 +292,7 @@ __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(kFullMask, *tmem_slot, 0);
   pdl_launch_dependents();
 
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&abort_flag) != 0; };
@@ -384,7 +410,7 @@ __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
         const int64_t i0 = static_cast<int64_t>(tile % p.token_tiles) * NT + at;
 #pragma unroll
         for (int t = 0; t < kX; ++t) fetch(p.a_scale + (i0 + 64 * t) * p.ld_a_scale, some && i0 + 64 * t < p.m, k, wide_a, x[t]);
-        if (p.by_channel) {
+        if (BY_CHANNEL) {
 #pragma unroll
           for (int t = 0; t < kW; ++t) fetch(p.b_scale + (j0 + 64 * t + at) * p.ld_b_scale, j0 + 64 * t + at < p.n, k, wide_b, w[t]);
         } else {
@@ -413,8 +439,8 @@ __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
         for (int q = 0; q < kScaleBlocks; ++q) {
 #pragma unroll
           for (int t = 0; t < kX; ++t)
-            if (some) to[q * (NT + kChannels) + 64 * t] = p.by_channel ? x[t][q] : __fmul_rn(x[t][q], w[0][q]);
-          if (p.by_channel) {
+            if (some) to[q * (NT + kChannels) + 64 * t] = BY_CHANNEL ? x[t][q] : __fmul_rn(x[t][q], w[0][q]);
+          if (BY_CHANNEL) {
 #pragma unroll
             for (int t = 0; t < kW; ++t) to[q * (NT + kChannels) + NT + 64 * t] = w[t][q];
           }
@@ -446,14 +472,6 @@ __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
       meet_phase ^= 1u;
       return r;
     };
-    auto ld = [&](uint32_t at, uint32_t* v) {  // kSlab columns of the warp's 32 lanes
-      if constexpr (OUT >= 2) {
-        tmem_ld_blocks2(at, v);
-        tmem_ld_blocks2(at + (16u << 16), v + 8);  // TMEM lanes 16-31 of the warp's
-      } else {
-        tmem_ld16(at, v);
-      }
-    };
     pdl_wait();  // the kernel before it may read `out`, and writes the bias
     Slot<S::kAcc> as;
     Slot<kScaleSlots> ss;
@@ -461,68 +479,59 @@ __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
       float acc[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
-      for (int k = k0; k < k1; ++k) {
-        const int q = k % kScaleBlocks;
-        if (q == 0 || k == k0) {
-          ok = fine(mbar_wait(&sc_full[ss.i], ss.phase, p.timeout_ns));
-          if (!ok) break;
-        }
-        const float* sx = scales + ss.i * S::kScaleFloats + q * (NT + kChannels);
-        // One scale for all channels is in the tokens' already.
-        float sw[4];
-#pragma unroll
-        for (int c = 0; c < (OUT >= 2 ? 4 : 1); ++c) sw[c] = p.by_channel ? sx[NT + quad * 32 + (OUT >= 2 ? 8 * c + lane / 4 : lane)] : 1.0f;
-        sx += group * kCols;
-        ok = fine(mbar_wait(&acc_full[as.i], as.phase, p.timeout_ns));
+      for (int k = k0; k < k1;) {
+        ok = fine(mbar_wait(&sc_full[ss.i], ss.phase, p.timeout_ns));
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t from = lane_base + static_cast<uint32_t>(as.i * NT);
-        auto promote = [&](auto by_channel) {
-          // With room for two slabs the next one's sums are on their way while this one's are added.
-          constexpr int kBuf = S::kBuffers, kF = OUT >= 2 ? 2 : kSlab / 2;
-          uint32_t v[kBuf][kSlab];
-          u64 f[kF];
-          if (kBuf == 2) ld(from, v[0]);
+        const float* sx = scales + ss.i * S::kScaleFloats + k % kScaleBlocks * (NT + kChannels);
+        const int last = min(k1, (k / kScaleBlocks + 1) * kScaleBlocks);
+#pragma unroll 1
+        for (; k < last; ++k, sx += NT + kChannels) {
+          // One scale for all channels is in the tokens' already.
+          float sw[Part<NT, OUT>::kChan];
+          if constexpr (BY_CHANNEL) {
+#pragma unroll
+            for (int c = 0; c < Part<NT, OUT>::kChan; ++c) sw[c] = sx[NT + quad * 32 + (OUT >= 2 ? 8 * c + lane / 4 : lane)];
+          }
+          const float* st = sx + group * kCols + (OUT >= 2 ? 2 * (lane & 3) : 0);
+          ok = fine(mbar_wait(&acc_full[as.i], as.phase, p.timeout_ns));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t from = lane_base + static_cast<uint32_t>(as.i * NT);
+          constexpr int kF = OUT >= 2 ? kSlab / 8 : kSlab / 2;
 #pragma unroll
           for (int i = 0; i < kCols / kSlab; ++i) {
-            uint32_t(&now)[kSlab] = v[i % kBuf];
-            if (kBuf == 1) ld(from + i * kSlab, now);
+            u64 f[kF];
 #pragma unroll
-            for (int j = 0; j < kF; ++j)
-              f[j] = *reinterpret_cast<const u64*>(sx + i * kSlab + (OUT >= 2 ? 8 * j + 2 * (lane & 3) : 2 * j));
-            tmem_wait_ld<kSlab>(now);
+            for (int j = 0; j < kF; ++j) f[j] = *reinterpret_cast<const u64*>(st + i * kSlab + (OUT >= 2 ? 8 * j : 2 * j));
+            float v[kSlab];
+            if constexpr (OUT >= 2)
+              tmem_read_blocks(from + i * kSlab, v);
+            else
+              tmem_read_columns(from + i * kSlab, v);
             if (i + 1 == kCols / kSlab) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_cluster(acc_empty_addr + as.i * 8);
-            } else if (kBuf == 2) {
-              ld(from + (i + 1) * kSlab, v[(i + 1) % kBuf]);
             }
 #pragma unroll
-            for (int e = 0; e < kSlab / 2; ++e) {
-              const u64 s = f[OUT >= 2 ? (e >> 1) & 1 : e];
-              float s0 = low2(s), s1 = high2(s);
-              if constexpr (decltype(by_channel)::value) {
-                const float c = sw[OUT >= 2 ? 2 * (e >> 2) + (e & 1) : 0];
-                s0 = __fmul_rn(s0, c);
-                s1 = __fmul_rn(s1, c);
+            for (int e = 0; e < kSlab; e += 2) {
+              u64 s = f[OUT >= 2 ? (e >> 2) % (kSlab / 8) : e >> 1];
+              if constexpr (BY_CHANNEL) {
+                const float c = sw[OUT >= 2 ? 2 * (e / (kSlab / 2)) + (e >> 1 & 1) : 0];
+                s = mul2(s, pack2(c, c));
               }
-              float* to = acc + i * kSlab + 2 * e;
-              to[0] = __fmaf_rn(__uint_as_float(now[2 * e]), s0, to[0]);
-              to[1] = __fmaf_rn(__uint_as_float(now[2 * e + 1]), s1, to[1]);
+              float* to = acc + i * kSlab + e;
+              const u64 r = fma2(pack2(v[e], v[e + 1]), s, pack2(to[0], to[1]));
+              to[0] = low2(r);
+              to[1] = high2(r);
             }
           }
-        };
-        if (p.by_channel)
-          promote(std::true_type{});
-        else
-          promote(std::false_type{});
-        as.advance();
-        if (q == kScaleBlocks - 1 || k + 1 == k1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_empty[ss.i]);
-          ss.advance();
+          as.advance();
         }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[ss.i]);
+        ss.advance();
       }
       if (!ok) break;
       if (k0 != 0 || k1 != p.stages) {
@@ -587,7 +596,7 @@ __global__ void __launch_bounds__(Shape<NT, OUT>::kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
-template <int NT, int OUT>
+template <int NT, int OUT, bool BY_CHANNEL>
 cudaError_t launch_t(const MatmulF8Launch& a, const MatmulF8Workspace& w, cudaStream_t st) {
   using S = Shape<NT, OUT>;
   CUtensorMap mx, mw, mo;
@@ -609,7 +618,6 @@ cudaError_t launch_t(const MatmulF8Launch& a, const MatmulF8Workspace& w, cudaSt
   p.n = a.n;
   // A is b's rows, B is a's: 0 e4m3, 1 e5m2.
   p.formats = (a.b_dtype == kE5M2 ? 1u << 7 : 0u) | (a.a_dtype == kE5M2 ? 1u << 10 : 0u);
-  p.by_channel = a.block_rows == 1;
   p.stages = (a.k + kDepth - 1) / kDepth;
   p.token_tiles = static_cast<int>((a.m + NT - 1) / NT);
   p.tiles = static_cast<int>((a.n + kPairChannels - 1) / kPairChannels * p.token_tiles);
@@ -626,7 +634,7 @@ cudaError_t launch_t(const MatmulF8Launch& a, const MatmulF8Workspace& w, cudaSt
   p.split = rounds * p.stages > (total + max_pairs - 1) / max_pairs + kSplitCost<NT>;
   const int64_t pairs = p.split ? std::min(max_pairs, total) : std::min<int64_t>(max_pairs, p.tiles);
 
-  auto fn = matmul_f8_pair_kernel<NT, OUT>;
+  auto fn = matmul_f8_pair_kernel<NT, OUT, BY_CHANNEL>;
   static PerDeviceOnce once;
   const cudaError_t limit = once.run([fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem); });
   if (limit != cudaSuccess) return limit;
@@ -654,11 +662,16 @@ cudaError_t launch_t(const MatmulF8Launch& a, const MatmulF8Workspace& w, cudaSt
   return cudaLaunchKernelEx(&cfg, fn, mx, mw, mo, p);
 }
 
+template <int NT, int OUT>
+cudaError_t launch_blocks(const MatmulF8Launch& a, const MatmulF8Workspace& w, cudaStream_t st) {
+  return a.block_rows == 1 ? launch_t<NT, OUT, true>(a, w, st) : launch_t<NT, OUT, false>(a, w, st);
+}
+
 template <int NT>
 cudaError_t launch_out(const MatmulF8Launch& a, const MatmulF8Workspace& w, cudaStream_t st) {
-  if (a.out_dtype == kF32) return launch_t<NT, 1>(a, w, st);
-  if (a.out_dtype == kBF16) return launch_t<NT, 2>(a, w, st);
-  return launch_t<NT, 3>(a, w, st);
+  if (a.out_dtype == kF32) return launch_blocks<NT, 1>(a, w, st);
+  if (a.out_dtype == kBF16) return launch_blocks<NT, 2>(a, w, st);
+  return launch_blocks<NT, 3>(a, w, st);
 }
 
 }  // namespace
