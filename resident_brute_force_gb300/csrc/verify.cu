@@ -19,8 +19,8 @@
 // 64-bit integers, exact and in any order, and each number in them is right to
 // 2^-30 of itself: weights in fp32 would put some draws in a thousand on another
 // index than 64 bits do, where the tail is long. 2^z with z = (x - max) log2(e) / T
-// - log2 Z as the sum of two fp32 numbers, split into whole 32nds (a table of 31-bit
-// integers) and a rest of at most 2^-5 (a polynomial, as a 32-bit fraction).
+// as the sum of two fp32 numbers, split into whole 32nds (a table of 31-bit
+// integers) and a rest of at most 2^-6 (a polynomial, as a 32-bit fraction).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,8 +38,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxSplits = 64;
-constexpr int kMaxHeld = 192 * 1024;  // of two rows in one CTA's shared memory
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);  // what fp32 leaves out
+constexpr int kDrawThreads = 1024;  // an SM, in the draw: 64 registers each
 
 // log2(e) / T as a finite number above 0 (sample_dev's); 0 where the best index is asked for.
 __device__ __forceinline__ float rate_of(const VerifyLaunch& a, int64_t seq) {
@@ -97,74 +98,88 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyLaun
   const int v0 = static_cast<int>(int64_t(row.vecs) * split / splits), v1 = static_cast<int>(int64_t(row.vecs) * (split + 1) / splits);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  Sum s;
-  u64 first = 0;  // the key of the best index
-  for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += 4 * kThreads) {
-    uint4 raw[4];
+  if (rate == 0.0f) {  // the key of the best index
+    u64 first = 0;
+    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads) {
+      float x[E];
+      Vec<T>::unpack(row.load(v), x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i] = v + i * kThreads < v1 ? row.load(v + i * kThreads) : vec_none<T>();
-    float x[4][E];
-    uint4 best = vec_max<T>(vec_max<T>(raw[0], raw[1]), vec_max<T>(raw[2], raw[3]));
-    Vec<T>::unpack(best, x[0]);
-    float top = x[0][0];
-#pragma unroll
-    for (int i = 1; i < E; ++i) top = fmaxf(top, x[0][i]);
-    if (rate == 0.0f) {
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        Vec<T>::unpack(raw[i], x[0]);
-        for (int e = 0; e < E; ++e)
-          if (x[0][e] > -INFINITY) first = umax64(first, make_key(x[0][e], static_cast<uint32_t>((v + i * kThreads) * E - row.lead + e)));
-      }
-      continue;
+      for (int e = 0; e < E; ++e)
+        if (x[e] > -INFINITY) first = umax64(first, make_key(x[e], static_cast<uint32_t>(v * E - row.lead + e)));
     }
-    if (top == -INFINITY) continue;
+    first = warp_max(first);
+    if (lane == 0) part[warp].key = first;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kWarps; ++w) first = umax64(first, part[w].key);
+      parts[row_id * splits + split] = VerifyPart{0.0f, 0.0f, first};
+    }
+    return;
+  }
+
+  Sum s;
+  auto add = [&](auto n, const uint4 (&raw)[4]) {  // the first n vectors
+    constexpr int N = decltype(n)::value;
+    float x[E];
+    uint4 best = raw[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = vec_max<T>(best, raw[i]);
+    Vec<T>::unpack(best, x);
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < E; ++i) top = fmaxf(top, x[i]);
+    if (top == -INFINITY) return;
     if (top > s.top) {
       s.z = s.top == -INFINITY ? 0.0f : s.z * ex2(less_top(s.top, top) * rate);
       s.top = top;
     }
-    if (s.top == INFINITY) {
+    const bool inf = s.top == INFINITY;  // then only the scores that equal it count
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        Vec<T>::unpack(raw[i], x[0]);
+    for (int i = 0; i < N; ++i) {
+      Vec<T>::unpack(raw[i], x);
+      if (inf) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s.z += x[0][e] == INFINITY ? 1.0f : 0.0f;
+        for (int e = 0; e < E; ++e) s.z += x[e] == INFINITY ? 1.0f : 0.0f;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e % 4] += ex2(__fmul_rn(__fsub_rn(x[e], s.top), rate));
       }
-      continue;
-    }
-    const u64 ntop2 = pack2(-s.top, -s.top), rate2 = pack2(rate, rate);
-    float sum[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Vec<T>::unpack(raw[i], x[i]);
-      u64 add = 0;  // two zeros
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const u64 z = mul2(add2(pack2(x[i][e], x[i][e + 1]), ntop2), rate2);
-        add = add2(add, pack2(ex2(low2(z)), ex2(high2(z))));
-      }
-      sum[i] = low2(add) + high2(add);
     }
     s.z += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-  }
-  if (rate == 0.0f) {
-    first = warp_max(first);
-    if (lane == 0) part[warp].key = first;
-  } else {
+  };
+  {
+    const int f0 = max(v0, row.lead > 0 ? 1 : 0), f1 = min(v1, (row.n + row.lead) / E);
+    const uint4* src = reinterpret_cast<const uint4*>(row.p - row.lead);
+    uint4 raw[4];
+    int v = f0 + static_cast<int>(threadIdx.x);
+    for (; v + 3 * kThreads < f1; v += 4 * kThreads) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s.join(__shfl_xor_sync(kFullMask, s.top, d), __shfl_xor_sync(kFullMask, s.z, d), rate);
-    if (lane == 0) part[warp] = VerifyPart{s.top, s.z, 0};
+      for (int i = 0; i < 4; ++i) raw[i] = src[v + i * kThreads];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[i] = vec_max<T>(raw[i], vec_none<T>());
+      add(std::integral_constant<int, 4>{}, raw);
+    }
+#pragma unroll 1
+    for (; v < f1; v += kThreads) {
+      raw[0] = vec_max<T>(src[v], vec_none<T>());
+      add(std::integral_constant<int, 1>{}, raw);
+    }
+    if (threadIdx.x < 2 && v0 < v1) {  // the one or two vectors that reach past the row
+      const int e = threadIdx.x == 0 ? v0 : v1 - 1;
+      if ((e < f0 || e >= f1) && !(threadIdx.x == 1 && e == v0)) {
+        raw[0] = row.load(e);
+        add(std::integral_constant<int, 1>{}, raw);
+      }
+    }
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s.join(__shfl_xor_sync(kFullMask, s.top, d), __shfl_xor_sync(kFullMask, s.z, d), rate);
+  if (lane == 0) part[warp] = VerifyPart{s.top, s.z, 0};
   __syncthreads();
   if (threadIdx.x == 0) {
-    VerifyPart r = part[0];
-    if (rate == 0.0f) {
-      for (int w = 1; w < kWarps; ++w) r.key = umax64(r.key, part[w].key);
-    } else {
-      for (int w = 1; w < kWarps; ++w) s.join(part[w].top, part[w].z, rate);
-      r = VerifyPart{s.top, s.z, 0};
-    }
-    parts[row_id * splits + split] = r;
+    for (int w = 1; w < kWarps; ++w) s.join(part[w].top, part[w].z, rate);
+    parts[row_id * splits + split] = VerifyPart{s.top, s.z, 0};
   }
 }
 
@@ -177,50 +192,67 @@ __constant__ uint32_t kRoots[32] = {
     1518500250u, 1551751076u, 1585730000u, 1620452965u, 1655936265u, 1692196547u, 1729250827u, 1767116489u,
     1805811301u, 1845353420u, 1885761398u, 1927054196u, 1969251188u, 2012372174u, 2056437387u, 2101467502u};
 
-// 2^((x - top) rate - shift) for the scores of a row, in units of 2^-(62 - spare):
-// `shift` is held as whole 32nds and a rest.
+// 2^((x - top) rate) for the scores of a row, each as a whole number of 31 bits
+// and a shift: right to 2^-30 of itself (the polynomial's and the argument's last
+// roundings, 2^-31 each, the table's and the product's, 2^-31 and 2^-30 of it). At
+// `one`, the weight 1 is 2^(30 + one): a sum of weights is set to stay below 2^64.
 struct Weights {
-  float top, rate_hi, rate_lo, rest;
-  int whole, spare;
+  float top;
+  u64 ntop2, rate2, nrate2, lo2;
+  uint32_t factor;        // of a share, in 2^-31, with `one` less its shift
+  int one;
   const uint32_t* roots;  // in shared memory
 
-  __device__ __forceinline__ void set(float t, double rate, double shift, int spare_bits, const uint32_t* table) {
-    top = t;
-    rate_hi = static_cast<float>(rate);
-    rate_lo = rate_hi > 3.0e38f ? 0.0f : static_cast<float>(rate - rate_hi);
-    const double n = rint(shift * 32.0);
-    whole = static_cast<int>(n);
-    rest = static_cast<float>(shift - n * (1.0 / 32.0));
-    spare = spare_bits;
+  __device__ __forceinline__ void set(float t, float rate_hi, float rate_lo, const uint32_t* table) {
+    top = t == INFINITY ? 0.0f : t;
+    ntop2 = pack2(-top, -top);
+    rate2 = pack2(rate_hi, rate_hi);
+    nrate2 = pack2(-rate_hi, -rate_hi);
+    lo2 = pack2(rate_lo, rate_lo);
     roots = table;
   }
-  __device__ __forceinline__ u64 of(float x) const {
-    if (top == INFINITY) return x == INFINITY ? at(0.0f, 0.0f) : 0;
-    // x - top as the sum of two numbers, and their product with the rate.
-    const float d = __fsub_rn(x, top);
-    const float back = __fsub_rn(d, x);  // -top, as far as d has it
-    const float lost = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(top, back));
-    const float hi = __fmul_rn(d, rate_hi);
-    if (!(hi > -64.0f)) return 0;
-    const float lo = __fmaf_rn(lost, rate_hi, __fmaf_rn(d, rate_lo, __fmaf_rn(d, rate_hi, -hi)));
-    return at(hi, lo);
+  // Every weight divided by `all`, a sum of them at the present `one`: shares of 2^62.
+  __device__ __forceinline__ void divide(u64 all) {
+    const int up = __clzll(static_cast<long long>(all));
+    const uint32_t head = static_cast<uint32_t>((all << up) >> 32);  // its first 32 bits
+    const u64 f = (u64(1) << 63) / head;  // 2^31 .. 2^32: 2^(95 - up) / all
+    factor = f > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(f);
+    one += up - 2;  // m f / 2^31 = m 2^(64 - up) / all; a share of 2^62 is m 2^(62 + one) / all
+  }
+  // Of two scores (with a largest score of +infinity: shifted): their weights, or their shares of the sum.
+  template <bool SHARES>
+  __device__ __forceinline__ void of2(float x0, float x1, u64& w0, u64& w1) const {
+    const u64 x = pack2(x0, x1), m1 = pack2(-1.0f, -1.0f);
+    // x - top as the sum of two numbers, and its product with the rate.
+    const u64 d = add2(x, ntop2);
+    const u64 back = fma2(x, m1, d);  // -top, as far as d has it
+    const u64 lost = fma2(fma2(ntop2, m1, back), m1, fma2(fma2(back, m1, d), m1, x));
+    const u64 far = mul2(d, rate2);
+    const u64 hi = pack2(fmaxf(low2(far), -200.0f), fmaxf(high2(far), -200.0f));  // no weight; -infinity among them
+    const u64 lo = fma2(lost, rate2, fma2(d, lo2, fma2(d, rate2, mul2(d, nrate2))));  // any number there
+    // Whole 32nds (1.5 * 2^23 rounds, and leaves them in the low bits) and a rest.
+    const u64 n = fma2(hi, pack2(32.0f, 32.0f), pack2(12582912.0f, 12582912.0f));
+    const u64 whole = add2(n, pack2(-12582912.0f, -12582912.0f));
+    const u64 f = add2(fma2(whole, pack2(-1.0f / 32.0f, -1.0f / 32.0f), hi), lo);
+    // 2^f - 1, |f| < 2^-5: the series of exp(f ln 2).
+    u64 g = fma2(f, pack2(9.6181291e-3f, 9.6181291e-3f), pack2(5.5504109e-2f, 5.5504109e-2f));
+    g = fma2(f, g, pack2(2.4022651e-1f, 2.4022651e-1f));
+    g = fma2(f, g, pack2(6.9314718e-1f, 6.9314718e-1f));
+    g = mul2(mul2(f, g), pack2(4294967296.0f, 4294967296.0f));
+    w0 = place<SHARES>(low2(n), low2(g));
+    w1 = place<SHARES>(high2(n), high2(g));
   }
 
  private:
-  __device__ __forceinline__ u64 at(float hi, float lo) const {
-    const float n = rintf(hi * 32.0f);
-    const float f = __fadd_rn(__fmaf_rn(n, -1.0f / 32.0f, hi), __fsub_rn(lo, rest));
-    const int e = static_cast<int>(n) - whole;
-    // 2^f - 1, |f| < 2^-4: the series of exp(f ln 2).
-    float g = __fmaf_rn(f, 1.3333558e-3f, 9.6181291e-3f);
-    g = __fmaf_rn(f, g, 5.5504109e-2f);
-    g = __fmaf_rn(f, g, 2.4022651e-1f);
-    g = __fmaf_rn(f, g, 6.9314718e-1f);
-    const int frac = __float2int_rn(__fmul_rn(f, g) * 4294967296.0f);
-    const u64 root = roots[e & 31];
-    const u64 w = (root << 32) + static_cast<u64>(static_cast<long long>(root) * frac);
-    const int down = spare - (e >> 5);
-    return down < 64 ? (down > 0 ? w >> down : w) : 0;
+  template <bool SHARES>
+  __device__ __forceinline__ u64 place(float n, float g) const {
+    const int e = static_cast<int>(__float_as_uint(n) - 0x4B400000u);
+    const int root = static_cast<int>(roots[e & 31]);
+    uint32_t m = static_cast<uint32_t>(root + __mulhi(root, __float2int_rn(g)));
+    if (SHARES) m = __umulhi(m << 1, factor);
+    u64 w;  // m 2^(one + e / 32), nothing left of it past 64
+    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(m) << 32), "r"(32 - one - (e >> 5)));
+    return w;
   }
 };
 
@@ -253,11 +285,10 @@ struct Place {  // what one place's parts say
   float top, z;
 };
 
-template <typename T, bool HELD>
-__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyLaunch a, const VerifyPart* parts, int splits, int held_vecs) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw_kernel(const VerifyLaunch a, const VerifyPart* parts, int splits) {
+  constexpr int kWarps = kThreads / 32;
   constexpr int E = Vec<T>::kLen;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  uint4* held = reinterpret_cast<uint4*>(dyn);  // the target's part, then the draft's
   __shared__ uint32_t roots[32];
   __shared__ u64 slot[4][kMaxCluster];  // a word per CTA, written by all of them
   __shared__ u64 kept[kWarps];
@@ -385,16 +416,6 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyLaunc
   const int c0 = static_cast<int>(int64_t(rp.vecs) * rank / size), c1 = static_cast<int>(int64_t(rp.vecs) * (rank + 1) / size);
   auto part_of = [](int lo, int hi, int w) { return lo + static_cast<int>(int64_t(hi - lo) * w / kWarps); };
   const int v0 = part_of(c0, c1, warp), v1 = part_of(c0, c1, warp + 1);
-  auto get_p = [&](int v) -> uint4 { return HELD ? held[v - c0] : rp.load(v); };
-  auto get_q = [&](int v) -> uint4 { return HELD ? held[held_vecs + v - c0] : load_q(v); };
-  if (HELD) {
-    for (int v = v0 + lane; v < v1; v += 32) {
-      held[v - c0] = rp.load(v);
-      if (with_q) held[held_vecs + v - c0] = load_q(v);
-    }
-    __syncwarp();
-  }
-
   int turn = 0;
   // Sum over the cluster of every thread's v; slot[turn - 1] keeps the CTAs' own.
   auto total_of = [&](u64 v) {
@@ -413,40 +434,81 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyLaunc
     return warp_sum(r);
   };
 
-  // The two rows' sums, exactly; `spare` bits keep them within 62.
-  const double rate64 = a.temperature ? fmin(fmax(1.4426950408889634 / static_cast<double>(a.temperature[seq]), 1.4e-45), 3.4e38)
-                                      : 1.4426950408889634;
-  const int spare = 33 - __clz(max(a.vocab, 1));
-  Weights wp, wq;
-  auto sum_of = [&](Weights& w, float top, auto&& get) {
-    w.set(top, rate64, 0.0, spare, roots);
-    u64 sum = 0;
-#pragma unroll 1
-    for (int v = v0 + lane; v < v1; v += 32) {
-      float x[E];
-      Vec<T>::unpack(get(v), x);
+  // log2(e) / T as the sum of two numbers (one, where it is at an end of the range).
+  const float heat = a.temperature ? a.temperature[seq] : 1.0f;
+  const float rest = __fadd_rn(__fmaf_rn(-rate, heat, kLog2e), kLog2eLow);
+  const float rate_lo = rate > 1.4e-45f && rate < 3.4e38f ? __fdiv_rn(rest, heat) : 0.0f;
+  // With a largest score of +infinity only those that equal it count.
+  auto scores = [](uint4 raw, float top, float (&x)[E]) {
+    Vec<T>::unpack(raw, x);
+    if (top == INFINITY) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += w.of(x[e]);
+      for (int e = 0; e < E; ++e) x[e] = x[e] == INFINITY ? 0.0f : -INFINITY;
     }
-    const u64 all = total_of(sum);
-    w.set(top, rate64, log2(static_cast<double>(all)) + spare - 62, 0, roots);
   };
-  sum_of(wp, pp.top, get_p);
-  if (with_q) sum_of(wq, row_q.top, get_q);
-
-  // What a vector's scores leave, from place 2^-62 of the whole on.
+  auto load_p = [&](int v) { return rp.load(v); };
+  const Place qq = row_q;
+  Weights wp, wq;
+  // An fp32 sum bounds the exact one: 2^31 times that, and a bit to spare, stays below 2^64.
+  auto set = [&](Weights& w, const Place& place) {
+    w.set(place.top, rate, rate_lo, roots);
+    w.one = 31 - (static_cast<int>(__float_as_uint(place.z * 1.001f) >> 23) - 127);
+  };
+  set(wp, pp);
+  if (with_q) set(wq, qq);
+  // body(v, p's vector, q's vector) for this warp's part, a vector a lane, the next ones on their way.
+  auto each = [&](bool both, auto&& body) {
+    int v = v0 + lane;
+    uint4 np = v < v1 ? load_p(v) : vec_none<T>(), nq = both && v < v1 ? load_q(v) : vec_none<T>();
+#pragma unroll 1
+    for (; v < v1; v += 32) {
+      const uint4 rp4 = np, rq4 = nq;
+      if (v + 32 < v1) {
+        np = load_p(v + 32);
+        if (both) nq = load_q(v + 32);
+      }
+      body(v, rp4, rq4);
+    }
+  };
+  // With a draft's row: both rows' sums, and then shares of 2^62, whose differences are what is left.
+  if (with_q) {
+    u64 sum_p = 0, sum_q = 0;
+    each(true, [&](int, const uint4& vp, const uint4& vq) {
+      float x[E], y[E];
+      scores(vp, pp.top, x);
+      scores(vq, qq.top, y);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        u64 a0, a1;
+        wp.of2<false>(x[e], x[e + 1], a0, a1);
+        sum_p += a0 + a1;
+        wq.of2<false>(y[e], y[e + 1], a0, a1);
+        sum_q += a0 + a1;
+      }
+    });
+    const u64 all_p = total_of(sum_p);
+    wp.divide(all_p);
+    wq.divide(total_of(sum_q));
+  }
   bool left = with_q || out >= 0;
-  auto weigh = [&](int v, u64 (&w)[E]) {
+  auto weigh = [&](int v, const uint4& vp, const uint4& vq, u64 (&w)[E]) {
     float x[E];
-    Vec<T>::unpack(get_p(v), x);
+    scores(vp, pp.top, x);
+    if (!with_q) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = wp.of(x[e]);
+      for (int e = 0; e < E; e += 2) wp.of2<false>(x[e], x[e + 1], w[e], w[e + 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 2) wp.of2<true>(x[e], x[e + 1], w[e], w[e + 1]);
+    }
     if (left && with_q) {
-      Vec<T>::unpack(get_q(v), x);
+      scores(vq, qq.top, x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const u64 q = wq.of(x[e]);
-        w[e] = w[e] > q ? w[e] - q : 0;
+      for (int e = 0; e < E; e += 2) {
+        u64 q[2];
+        wq.of2<true>(x[e], x[e + 1], q[0], q[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[e + i] = w[e + i] > q[i] ? w[e + i] - q[i] : 0;
       }
     } else if (left) {
 #pragma unroll
@@ -456,13 +518,12 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyLaunc
   };
   auto sum_left = [&]() {
     u64 sum = 0;
-#pragma unroll 1
-    for (int v = v0 + lane; v < v1; v += 32) {
+    each(left && with_q, [&](int v, const uint4& vp, const uint4& vq) {
       u64 w[E];
-      weigh(v, w);
+      weigh(v, vp, vq, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum += w[e];
-    }
+    });
     return total_of(sum);
   };
   u64 total = sum_left();
@@ -481,7 +542,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyLaunc
   for (int v = v0; v < v1; v += 32) {
     u64 w[E], sum = 0;
     if (v + lane < v1) {
-      weigh(v + lane, w);
+      weigh(v + lane, load_p(v + lane), left && with_q ? load_q(v + lane) : vec_none<T>(), w);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum += w[e];
     }
@@ -503,19 +564,19 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyLaunc
   }
 }
 
-template <typename T, bool HELD>
-cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int splits, int cluster, int held_vecs, cudaStream_t st) {
-  auto fn = verify_draw_kernel<T, HELD>;
+template <typename T, int kThreads>
+cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int splits, int num_sms, cudaStream_t st) {
+  auto fn = verify_draw_kernel<T, kThreads>;
   static PerDeviceOnce once;
-  const cudaError_t ready = once.run([fn] {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
+  const cudaError_t ready = once.run([fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
   if (ready != cudaSuccess) return ready;
+  // As many CTAs a row as run at once, of a vector a thread at least.
+  const int64_t vecs = a.vocab * static_cast<int64_t>(sizeof(T)) / 16 + 2;
+  int cluster = 1;
+  while (cluster < kMaxCluster && a.seqs * cluster * 2 <= int64_t(num_sms) * (kDrawThreads / kThreads) && vecs / cluster > kThreads) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.seqs * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = HELD ? static_cast<size_t>(held_vecs) * 32 : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -526,17 +587,32 @@ cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int sp
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fn, a, parts, splits, held_vecs);
+  return cudaLaunchKernelEx(&cfg, fn, a, parts, splits);
 }
 
-// CTAs a row: parts of some 32 KB, fewer bytes where that leaves SMs idle, as
-// many as the workspace has room for.
+// Sixteen CTAs a row of 256 threads where that many run at once, else of 128: smaller
+// ones fill the SMs more evenly, and rows differ in what there is to do.
+template <typename T>
+cudaError_t launch_draw(const VerifyLaunch& a, const VerifyPart* parts, int splits, int num_sms, cudaStream_t st) {
+  return a.seqs * kMaxCluster <= int64_t(num_sms) * (kDrawThreads / 256) ? launch_draw_t<T, 256>(a, parts, splits, num_sms, st)
+                                                                       : launch_draw_t<T, 128>(a, parts, splits, num_sms, st);
+}
+
+// CTAs a row, of 8 KB at least, as many as the workspace has room for: the number
+// whose rounds of CTAs (eight an SM) read the least, a round's own time counted as 4 KB.
 int splits_of(const VerifyLaunch& a, int64_t max_parts, int num_sms) {
   const int64_t rows = a.seqs * (a.drafts + 1 + (a.draft ? a.drafts : 0));
-  const int64_t bytes = a.vocab * static_cast<int64_t>(dtype_bytes(a.dtype));
-  const int64_t fill = std::min((int64_t(num_sms) * 8 + rows - 1) / rows, bytes / 4096);
-  const int64_t s = std::min<int64_t>(std::max((bytes + 32767) / 32768, fill), std::min<int64_t>(kMaxSplits, max_parts / rows));
-  return static_cast<int>(std::max<int64_t>(1, s));
+  const int64_t bytes = a.vocab * static_cast<int64_t>(dtype_bytes(a.dtype)), places = int64_t(num_sms) * 8;
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(kMaxSplits, max_parts / rows), bytes / 8192);
+  int64_t best = 1, least = INT64_MAX;
+  for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
+    const int64_t cost = (rows * s + places - 1) / places * (bytes / s + 4096);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return static_cast<int>(best);
 }
 
 template <typename T>
@@ -544,16 +620,6 @@ cudaError_t launch_stats(const VerifyLaunch& a, VerifyPart* parts, int splits, c
   const int64_t rows = a.seqs * (a.drafts + 1 + (a.draft ? a.drafts : 0));
   verify_stats_kernel<T><<<static_cast<unsigned>(rows * splits), kThreads, 0, st>>>(a, parts, splits);
   return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t launch_draw(const VerifyLaunch& a, const VerifyPart* parts, int splits, cudaStream_t st) {
-  const int64_t vecs = a.vocab * static_cast<int64_t>(sizeof(T)) / 16 + 2;
-  int cluster = 1;
-  while (cluster < kMaxCluster && vecs / cluster > 512) cluster *= 2;
-  const int64_t held = vecs / cluster + 2;
-  return held * 32 <= kMaxHeld ? launch_draw_t<T, true>(a, parts, splits, cluster, static_cast<int>(held), st)
-                               : launch_draw_t<T, false>(a, parts, splits, cluster, 0, st);
 }
 
 }  // namespace
@@ -569,9 +635,9 @@ cudaError_t launch_verify_stats(const VerifyLaunch& a, VerifyPart* parts, int64_
 
 cudaError_t launch_verify_draw(const VerifyLaunch& a, const VerifyPart* parts, int64_t max_parts, int num_sms, cudaStream_t st) {
   const int splits = splits_of(a, max_parts, num_sms);
-  if (a.dtype == kF32) return launch_draw<float>(a, parts, splits, st);
-  if (a.dtype == kBF16) return launch_draw<__nv_bfloat16>(a, parts, splits, st);
-  return launch_draw<__half>(a, parts, splits, st);
+  if (a.dtype == kF32) return launch_draw<float>(a, parts, splits, num_sms, st);
+  if (a.dtype == kBF16) return launch_draw<__nv_bfloat16>(a, parts, splits, num_sms, st);
+  return launch_draw<__half>(a, parts, splits, num_sms, st);
 }
 
 }  // namespace rbf
