@@ -29,10 +29,11 @@
 namespace rbf {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kPiece = 64 * 1024;  // bytes of a row in a CTA's shared memory
+constexpr int kPiece = 64 * 1024;  // bytes of a row in a CTA's shared memory, at most
+constexpr int kAim = 64 * 1024;
+constexpr int kSmallCta = 8192;
+constexpr int kBigThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -63,6 +64,20 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { re
 template <>
 __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
+// The largest score of a vector.
+template <typename T>
+__device__ __forceinline__ float vec_top(const uint4& v) {
+  float x[Vec<T>::kLen];
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t m = Vec<T>::max(Vec<T>::max(v.x, v.y), Vec<T>::max(v.z, v.w));
+    Vec<T>::unpack(make_uint4(m, m, m, m), x);
+    return fmaxf(x[0], x[1]);
+  } else {
+    Vec<T>::unpack(v, x);
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ uint4 pack_vec(const float (&g)[Vec<T>::kLen]) {
   uint4 r;
@@ -72,9 +87,28 @@ __device__ __forceinline__ uint4 pack_vec(const float (&g)[Vec<T>::kLen]) {
   return r;
 }
 
-// What a CTA says of its part to all of its cluster: the largest and the sum of
-// the scores that are not listed, and of the listed ones (a float each, in a
-// word), the sum of p_e ((t_e - largest t) - (s_e - largest of these)), and of p_e.
+// A number as the sum of two fp32 ones: a loss is a small difference of sums, and
+// 64-bit arithmetic runs at a 64th of fp32's rate here.
+struct Pair {
+  float h = 0.0f, l = 0.0f;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ Pair two_product(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  return {s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
+}
+
+// What a CTA says of its part to all of its cluster, two floats a word: the largest
+// and the sum of the scores that are not listed, the same of the listed ones, the sum
+// of p_e ((t_e - largest t) - (s_e - largest of these)) (infinite where a listed
+// score is -infinity), and of p_e.
 constexpr int kWords = 4;
 
 // The weight 2^((x - top) rate), 0 where nothing is left.
@@ -89,39 +123,60 @@ __device__ __forceinline__ V warp_fold(V v, F&& f) {
   return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a, int piece_bytes, int* err, uint64_t timeout_ns) {
+// Shared memory of a CTA behind its piece of the row: five words an entry, and a
+// hash table of two words a slot for the first entry of each index.
+__host__ __device__ constexpr int table_bits(int k) {
+  int b = 5;
+  while ((1 << b) < 2 * k) ++b;
+  return b;
+}
+__host__ __device__ constexpr int list_bytes(int k) { return k ? 20 * k + (8 << table_bits(k)) : 0; }
+
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a, int piece_bytes, int cluster_bits, int bits, float rate, int* err,
+                                                                  uint64_t timeout_ns) {
   constexpr int E = Vec<T>::kLen;
+  constexpr int kWarps = kThreads / 32;
   using B = typename Bits<T>::type;
   extern __shared__ __align__(16) uint8_t dyn[];
   T* piece = reinterpret_cast<T*>(dyn);                                   // piece_bytes
   int* at = reinterpret_cast<int*>(dyn + piece_bytes);                    // [k] index, -1: not in this CTA's part
   float* logit = reinterpret_cast<float*>(at + a.k);                      // [k] the teacher's, -infinity: no entry
-  float* score = logit + a.k;                                             // [k] the student's
+  float* score = logit + a.k;                                             // [k] the student's, at the first entry of an index
   float* prob = score + a.k;                                              // [k] p_e
   int* owner = reinterpret_cast<int*>(prob + a.k);                        // [k] the first entry with the same index
+  int* key = owner + a.k;                                                 // the table: an index, and its first entry
+  int* first = key + (1 << bits);
   __shared__ uint64_t full;
   __shared__ float red[2][kWarps];
+  __shared__ float of_warp[8][32];  // what each warp says of its part; zeros past kWarps
   __shared__ u64 said[kMaxCluster][kWords];
-  __shared__ double part_d[2];
 
-  uint32_t rank, size;
+  uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  const uint32_t size = 1u << cluster_bits;
   if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t r = blockIdx.x / size;
+  const int64_t r = blockIdx.x >> cluster_bits;
+  // The row's first entries and its numbers are on their way from here on.
+  int j_first = -1;
+  float t_first = -INFINITY;
+  if (tid < a.k) {
+    j_first = a.index[r * a.ld_index + tid];
+    t_first = read_float(a.teacher, r * a.ld_teacher + tid, a.teacher_dtype);
+  }
+  const float w_row = a.weight ? a.weight[r] : 1.0f;
+  const float rest_raw = a.rest ? a.rest[r] : -INFINITY;
   const T* row = static_cast<const T*>(a.scores) + r * a.ld_scores;
   const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
   const int vecs = static_cast<int>((int64_t(a.vocab) + lead + E - 1) / E);
-  const int c0 = static_cast<int>(int64_t(vecs) * rank / size), c1 = static_cast<int>(int64_t(vecs) * (rank + 1) / size);
+  const int c0 = static_cast<int>(int64_t(vecs) * rank >> cluster_bits), c1 = static_cast<int>(int64_t(vecs) * (rank + 1) >> cluster_bits);
   const int piece_vecs = piece_bytes / 16;
-  const int pieces = max(1, (c1 - c0 + piece_vecs - 1) / piece_vecs);
+  const int pieces = c1 - c0 <= piece_vecs ? 1 : (c1 - c0 + piece_vecs - 1) / piece_vecs;
   if (tid == 0) {
     mbar_init(&full, 1);
     fence_mbar_init();
   }
-  __syncthreads();
 
   // Vectors [v0, v1) of the row into shared memory, -infinity outside of the row.
   const uint64_t policy = l2_policy_evict_first();
@@ -148,7 +203,9 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     }
   };
   auto arrived = [&]() {
-    if (!mbar_wait(&full, phase, timeout_ns)) {
+    // One thread looks, the others wait at the barrier: all of them looking takes
+    // the issue slots that the SM's other CTAs compute in.
+    if (tid == 0 && !mbar_wait(&full, phase, timeout_ns)) {
       ok = false;
       mbar_wait(&full, phase, timeout_ns);  // no copy may be in flight when the CTA exits
     }
@@ -156,63 +213,62 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     ok = __syncthreads_and(ok) != 0;
     if (!ok && tid == 0) atomicOr(err, kErrConsumerTimeout);
   };
-  fetch(c0, min(c1, c0 + piece_vecs));
+  fetch(c0, min(c1, c0 + piece_vecs));  // its barrier is the issuing thread's own so far
+  if (a.k)
+    for (int s = tid; s < 2 << bits; s += kThreads) key[s] = s < 1 << bits ? -1 : INT32_MAX;
+  for (int i = tid; i < 8 * 32; i += kThreads) of_warp[0][i] = i < 64 ? -INFINITY : 0.0f;  // two largest scores, six sums
+  __syncthreads();
 
-  // ------------------------------------------------------------ the teacher
-  const float rate = kLog2e / a.temperature;
-  const float w_row = a.weight ? a.weight[r] : 1.0f;
-  float rest_t = a.rest ? a.rest[r] * a.temperature : -INFINITY;  // as a logit
+  // ------------------------------------------- the teacher, ahead of the scores
+  const float rest_t = rest_raw * a.temperature;  // as a logit
   float top_t = rest_t;
   for (int e = tid; e < a.k; e += kThreads) {
-    const int j = a.index[r * a.ld_index + e];
-    const float t = j >= 0 && j < a.vocab ? read_float(a.teacher, r * a.ld_teacher + e, a.teacher_dtype) : -INFINITY;
-    const int64_t v = j >= 0 && j < a.vocab ? (int64_t(j) + lead) / E : -1;
-    at[e] = v >= c0 && v < c1 ? j : -1;
+    const int j = e == tid ? j_first : a.index[r * a.ld_index + e];
+    const bool there = j >= 0 && j < a.vocab;
+    float t = e == tid ? t_first : read_float(a.teacher, r * a.ld_teacher + e, a.teacher_dtype);
+    if (!there) t = -INFINITY;
+    const int64_t v = there ? (int64_t(j) + lead) / E : -1;
+    const bool mine = v >= c0 && v < c1;
+    at[e] = mine ? j : -1;
     logit[e] = t;
     top_t = fmaxf(top_t, t);
+    if (mine) {  // a slot of its index: whatever the order, the smallest entry stays
+      const uint32_t mask = (1u << bits) - 1;
+      uint32_t s = (static_cast<uint32_t>(j) * 2654435761u) >> (32 - bits);
+      for (int old; (old = atomicCAS(&key[s], -1, j)) != -1 && old != j;) s = (s + 1) & mask;
+      atomicMin(&first[s], e);
+      owner[e] = static_cast<int>(s);
+    }
   }
-  auto block_max = [&](float v) {
-    v = warp_fold(v, [](float x, float y) { return fmaxf(x, y); });
-    __syncthreads();
-    if (lane == 0) red[0][warp] = v;
-    __syncthreads();
-    v = red[0][0];
+  auto fmax2 = [](float x, float y) { return fmaxf(x, y); };
+  auto plus = [](auto x, auto y) { return x + y; };
+  // Over the CTA, in the warps' order; `slot`: each reduction's own words.
+  auto post = [&](int slot, float v) {
+    if (lane == 0) red[slot][warp] = v;
+  };
+  auto fold = [&](int slot, auto&& f) {
+    float v = red[slot][lane % kWarps];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) v = fmaxf(v, red[0][w]);
+    for (int d = kWarps / 2; d > 0; d >>= 1) v = f(v, __shfl_xor_sync(kFullMask, v, d));
     return v;
   };
-  auto block_sum2 = [&](float& x, float& y) {
-    x = warp_fold(x, [](float p, float q) { return p + q; });
-    y = warp_fold(y, [](float p, float q) { return p + q; });
-    __syncthreads();
-    if (lane == 0) {
-      red[0][warp] = x;
-      red[1][warp] = y;
-    }
-    __syncthreads();
-    x = y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      x += red[0][w];
-      y += red[1][w];
-    }
-  };
-  top_t = block_max(top_t);
-  float z_t = 0.0f, dummy = 0.0f;
+  post(0, warp_fold(top_t, fmax2));
+  __syncthreads();
+  top_t = fold(0, fmax2);
+  float z_t = 0.0f;
   for (int e = tid; e < a.k; e += kThreads) {
     const float p = weight_of(logit[e], top_t, rate);
     prob[e] = p;
     z_t += p;
+    if (at[e] >= 0) owner[e] = first[owner[e]];
   }
-  block_sum2(z_t, dummy);
-  const float z_tr = weight_of(rest_t, top_t, rate);
-  const float inv_t = z_t + z_tr > 0.0f || z_t != z_t || z_tr != z_tr ? 1.0f / (z_t + z_tr) : 0.0f;
-  const float p_in = z_t * inv_t, p_rest = z_tr * inv_t;
+  post(1, warp_fold(z_t, plus));
 
   // ------------------------------------------------------------ the student
+  // Of a thread: the largest of its scores that are not listed, and the sum of
+  // their weights below that.
   float top_rest = -INFINITY, top_in = -INFINITY;
-  float z_rest = 0.0f;  // this thread's
-  double z_all = 0.0;   // and of the pieces before
+  Pair z_rest;
   for (int p = 0; p < pieces; ++p) {
     const int v0 = c0 + p * piece_vecs, v1 = min(c1, v0 + piece_vecs);
     if (p > 0) {
@@ -221,102 +277,129 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     }
     arrived();
     if (!ok) break;
-    // The listed scores are read, then the first entry of each index marks its
-    // place with its number (the smallest stays, whatever the order of the
-    // writes), and in the end the place becomes -infinity.
+    // The listed scores are taken out.
     const int64_t j0 = int64_t(v0) * E - lead, j1 = int64_t(v1) * E - lead;
     for (int e = tid; e < a.k; e += kThreads) {
       const int j = at[e];
-      if (j >= j0 && j < j1) score[e] = Vec<T>::one(piece[j - j0]);
-    }
-    __syncthreads();
-    B* mark = reinterpret_cast<B*>(piece);
-    for (int e = tid; e < a.k; e += kThreads)
-      if (at[e] >= j0 && at[e] < j1) mark[at[e] - j0] = static_cast<B>(e);
-    bool again = true;
-    while (again) {
-      __syncthreads();
-      bool lower = false;
-      for (int e = tid; e < a.k; e += kThreads)
-        lower |= at[e] >= j0 && at[e] < j1 && static_cast<B>(e) < *reinterpret_cast<volatile B*>(&mark[at[e] - j0]);
-      again = __syncthreads_or(lower) != 0;
-      if (lower)
-        for (int e = tid; e < a.k; e += kThreads)
-          if (at[e] >= j0 && at[e] < j1 && static_cast<B>(e) < *reinterpret_cast<volatile B*>(&mark[at[e] - j0]))
-            *reinterpret_cast<volatile B*>(&mark[at[e] - j0]) = static_cast<B>(e);
-    }
-    for (int e = tid; e < a.k; e += kThreads)
-      if (at[e] >= j0 && at[e] < j1) owner[e] = static_cast<int>(mark[at[e] - j0]);
-    __syncthreads();
-    for (int e = tid; e < a.k; e += kThreads)
-      if (at[e] >= j0 && at[e] < j1) mark[at[e] - j0] = Bits<T>::kNone;
-    __syncthreads();
-
-    const uint4* src = reinterpret_cast<const uint4*>(piece);
-    float top = -INFINITY;
-    for (int v = tid; v < v1 - v0; v += kThreads) {
-      float x[E];
-      Vec<T>::unpack(src[v], x);
-#pragma unroll
-      for (int i = 0; i < E; ++i) top = fmaxf(top, x[i]);
-    }
-    top = fmaxf(block_max(top), top_rest);
-    if (p > 0) z_all *= static_cast<double>(weight_of(top_rest, top, rate));
-    top_rest = top;
-    z_rest = 0.0f;
-    const float base = top == -INFINITY ? 0.0f : top;
-    for (int v = tid; v < v1 - v0; v += kThreads) {
-      float x[E];
-      Vec<T>::unpack(src[v], x);
-      const u64 nb = pack2(-base, -base), r2 = pack2(rate, rate);
-      u64 add = 0;
-#pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const u64 z = mul2(add2(pack2(x[i], x[i + 1]), nb), r2);
-        add = add2(add, pack2(ex2(low2(z)), ex2(high2(z))));
+      if (j >= j0 && j < j1 && owner[e] == e) {
+        const float s = Vec<T>::one(piece[j - j0]);
+        reinterpret_cast<B*>(piece)[j - j0] = Bits<T>::kNone;
+        score[e] = s;
       }
-      z_rest += low2(add) + high2(add);
     }
-    if (pieces > 1) {
-      z_all += static_cast<double>(z_rest);
-      z_rest = 0.0f;
+    __syncthreads();
+    const uint4* src = reinterpret_cast<const uint4*>(piece);
+    // Of a thread's first scores the largest is found at once, then that of
+    // four vectors at a time (a NaN loses: the sum finds it).
+#pragma unroll 1
+    for (int v = tid; v < v1 - v0; v += 4 * kThreads) {
+      uint4 raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[i] = v + i * kThreads < v1 - v0 ? src[v + i * kThreads] : vec_none<T>();
+      float x[E];
+      const float top = vec_top<T>(vec_max<T>(vec_max<T>(raw[0], raw[1]), vec_max<T>(raw[2], raw[3])));
+      if (top > top_rest) {
+        const float less = weight_of(top_rest, top, rate);
+        z_rest = {z_rest.h * less, z_rest.l * less};
+        top_rest = top;
+      }
+      const float base = top_rest == -INFINITY ? 0.0f : top_rest;
+      const u64 nbase2 = pack2(-base, -base), rate2 = pack2(rate, rate);
+      u64 sum[2] = {0, 0};  // two zeros each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        Vec<T>::unpack(raw[i], x);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const u64 z = mul2(add2(pack2(x[e], x[e + 1]), nbase2), rate2);
+          sum[e / 2 % 2] = add2(sum[e / 2 % 2], pack2(ex2(low2(z)), ex2(high2(z))));
+        }
+      }
+      sum[0] = add2(sum[0], sum[1]);
+      z_rest = z_rest + Pair{low2(sum[0]) + high2(sum[0]), 0.0f};
     }
   }
-  if (pieces > 1) z_rest = static_cast<float>(z_all);
 
-  // Of this CTA's listed scores: the largest, the sum, and the products.
-  for (int e = tid; e < a.k; e += kThreads)
-    if (at[e] >= 0) top_in = fmaxf(top_in, score[e]);
-  top_in = block_max(top_in);
-  float z_in = 0.0f;
-  for (int e = tid; e < a.k; e += kThreads)
-    if (at[e] >= 0 && owner[e] == e) z_in += weight_of(score[e], top_in, rate);
-  block_sum2(z_rest, z_in);
-  if (warp == 0) {
-    // Each below its own largest: beside scores at the type's lowest value a teacher's logit would vanish.
-    double d = 0.0;
-    float m = 0.0f;
-    for (int e = lane; e < a.k; e += 32) {
-      if (at[e] < 0 || !(prob[e] > 0.0f)) continue;
-      const float p = prob[e] * inv_t;
-      d += score[e] == -INFINITY ? INFINITY : static_cast<double>(p) * static_cast<double>((logit[e] - top_t) - (score[e] - top_in));
-      m += p;
-    }
-    d = warp_fold(d, [](double x, double y) { return x + y; });
-    m = warp_fold(m, [](float x, float y) { return x + y; });
+  const float rest_w = weight_of(rest_t, top_t, rate);
+  z_t = fold(1, plus);
+  const float all_t = z_t + rest_w;
+  const float inv_t = all_t == 0.0f ? 0.0f : 1.0f / all_t;
+  const float p_in = z_t * inv_t, p_rest = rest_w * inv_t;
+  {
+    // The warp's, below its own largest.
+    const float top = warp_fold(top_rest, fmax2);
+    const float z = warp_fold(z_rest.h * weight_of(top_rest, top, rate), plus);  // of a thread's own -infinity: 0, or NaN
+    const float bad = top_rest == -INFINITY ? z_rest.h : 0.0f;                   // a NaN alone has no largest
     if (lane == 0) {
-      part_d[0] = d;
-      part_d[1] = static_cast<double>(m);
+      of_warp[0][warp] = top;
+      of_warp[2][warp] = z;
+    }
+    if (bad != bad) of_warp[2][warp] = bad;
+  }
+  if (warp * 32 < a.k) {
+    // The warp's listed scores: the sum, and the products, each below their
+    // largest: beside scores at the type's lowest value a teacher's logit would vanish.
+    for (int e = tid; e < a.k; e += kThreads)
+      if (at[e] >= 0) top_in = fmaxf(top_in, score[owner[e]]);
+    top_in = warp_fold(top_in, fmax2);
+    float z_in = 0.0f, mass = 0.0f, missed = 0.0f;
+    Pair diff;
+    for (int e = tid; e < a.k; e += kThreads) {
+      if (at[e] < 0) continue;
+      const float s = score[owner[e]];
+      if (owner[e] == e) z_in += weight_of(s, top_in, rate);
+      if (prob[e] > 0.0f) {
+        const float p = prob[e] * inv_t;
+        if (s == -INFINITY)
+          missed = 1.0f;
+        else
+          diff = diff + two_product(p, (logit[e] - top_t) - (s - top_in));
+        mass += p;
+      }
+    }
+    z_in = warp_fold(z_in, plus);
+    mass = warp_fold(mass, plus);
+    missed = warp_fold(missed, fmax2);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) diff = diff + Pair{__shfl_xor_sync(kFullMask, diff.h, d), __shfl_xor_sync(kFullMask, diff.l, d)};
+    if (lane == 0) {
+      of_warp[1][warp] = top_in;
+      of_warp[3][warp] = z_in;
+      of_warp[4][warp] = mass;
+      of_warp[5][warp] = missed;
+      of_warp[6][warp] = diff.h;
+      of_warp[7][warp] = diff.l;
     }
   }
   if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
-  if (tid < kWords * static_cast<int>(size)) {
-    const int word = tid % kWords;
-    const u64 v = word == 0   ? (static_cast<u64>(__float_as_uint(z_rest)) << 32 | __float_as_uint(top_rest))
-                  : word == 1 ? (static_cast<u64>(__float_as_uint(z_in)) << 32 | __float_as_uint(top_in))
-                              : static_cast<u64>(__double_as_longlong(part_d[word - 2]));
-    remote_store(remote(&said[rank][word], static_cast<uint32_t>(tid / kWords)), v);
+  if (warp == 0) {
+    // The warps' below the CTA's largest, and their sums, a warp a lane.
+    auto among = [&](float v, auto&& f) {
+#pragma unroll
+      for (int d = kWarps / 2; d > 0; d >>= 1) v = f(v, __shfl_xor_sync(kFullMask, v, d));
+      return __shfl_sync(kFullMask, v, 0);
+    };
+    const float wr = of_warp[0][lane], wi = of_warp[1][lane], m = of_warp[4][lane];
+    const float tr = among(wr, fmax2), ti = among(wi, fmax2);
+    const float zr = among(wr == -INFINITY ? of_warp[2][lane] : of_warp[2][lane] * weight_of(wr, tr, rate), plus);
+    const float zi = among(wi == -INFINITY ? of_warp[3][lane] : of_warp[3][lane] * weight_of(wi, ti, rate), plus);
+    Pair d{of_warp[6][lane], of_warp[7][lane]};
+    if (m > 0.0f && wi > -INFINITY) {
+      const Pair apart = two_sum(ti, -wi), part = two_product(m, apart.h);
+      d = d + Pair{part.h, __fmaf_rn(m, apart.l, part.l)};
+    }
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) d = d + Pair{__shfl_xor_sync(kFullMask, d.h, o), __shfl_xor_sync(kFullMask, d.l, o)};
+    d = {__shfl_sync(kFullMask, d.h, 0), __shfl_sync(kFullMask, d.l, 0)};
+    if (among(of_warp[5][lane], fmax2) > 0.0f) d = {INFINITY, 0.0f};
+    const float mass = among(m, plus);
+    for (int i = lane; i < kWords * static_cast<int>(size); i += 32) {
+      const int word = i % kWords;
+      const float lo = word == 0 ? tr : word == 1 ? ti : word == 2 ? d.h : mass;
+      const float hi = word == 0 ? zr : word == 1 ? zi : word == 2 ? d.l : 0.0f;
+      remote_store(remote(&said[rank][word], static_cast<uint32_t>(i / kWords)), static_cast<u64>(__float_as_uint(hi)) << 32 | __float_as_uint(lo));
+    }
   }
   if (size > 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -324,22 +407,25 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     __syncthreads();
   if (!ok) return;
 
-  // Every thread joins what the CTAs have said, in their order.
+  // Every thread joins what the CTAs have said, in their order (one warp's word to
+  // the others would take a barrier more); a loss alone is for rank 0's first one.
+  if (!a.grad && (rank != 0 || warp != 0)) return;
+  auto low = [&](uint32_t c, int word) { return __uint_as_float(static_cast<uint32_t>(said[c][word])); };
+  auto high = [&](uint32_t c, int word) { return __uint_as_float(static_cast<uint32_t>(said[c][word] >> 32)); };
   float tr = -INFINITY, ti = -INFINITY, zr = 0.0f, zi = 0.0f;
   for (uint32_t c = 0; c < size; ++c) {
-    tr = fmaxf(tr, __uint_as_float(static_cast<uint32_t>(said[c][0])));
-    ti = fmaxf(ti, __uint_as_float(static_cast<uint32_t>(said[c][1])));
+    tr = fmaxf(tr, low(c, 0));
+    ti = fmaxf(ti, low(c, 1));
   }
   for (uint32_t c = 0; c < size; ++c) {
-    const float cr = __uint_as_float(static_cast<uint32_t>(said[c][0])), ci = __uint_as_float(static_cast<uint32_t>(said[c][1]));
-    zr += __uint_as_float(static_cast<uint32_t>(said[c][0] >> 32)) * weight_of(cr, tr, rate);
-    zi += __uint_as_float(static_cast<uint32_t>(said[c][1] >> 32)) * weight_of(ci, ti, rate);
+    zr += low(c, 0) == -INFINITY ? high(c, 0) : high(c, 0) * weight_of(low(c, 0), tr, rate);  // 0, or a NaN that is alone
+    zi += low(c, 1) == -INFINITY ? high(c, 1) : high(c, 1) * weight_of(low(c, 1), ti, rate);
   }
   // Both below one score: what is left of the other's weight is a factor.
   const float top_s = fmaxf(tr, ti);
-  const float fr = weight_of(tr, top_s, rate), fi = weight_of(ti, top_s, rate);
+  const float fr = weight_of(tr, top_s, rate), fi = weight_of(ti, top_s, rate);  // one of them 1
   const float zr_s = zr * fr, zi_s = zi * fi, z_s = zr_s + zi_s;
-  const bool no_teacher = z_t + z_tr == 0.0f, no_student = z_s == 0.0f;
+  const bool no_teacher = all_t == 0.0f, no_student = z_s == 0.0f;
   const bool live = !no_teacher && !no_student && w_row != 0.0f;
   const float inv_s = 1.0f / z_s;
   const float q_in = zi_s * inv_s, q_rest = zr_s * inv_s;
@@ -347,27 +433,48 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
   if (a.loss && rank == 0 && tid == 0) {
     float loss = 0.0f;
     if (live) {
-      double d = 0.0;
       // sum p_e (log p_e - log q_e) = sum p_e ((t_e - largest t) - (s_e - largest s)) / T - P log(Z_t / Z_s)
+      Pair l;
+      bool missed = false;
       for (uint32_t c = 0; c < size; ++c) {
-        const double m = __longlong_as_double(static_cast<long long>(said[c][3]));
-        d += __longlong_as_double(static_cast<long long>(said[c][2]));
-        if (m > 0.0) d += m * (static_cast<double>(top_s) - static_cast<double>(__uint_as_float(static_cast<uint32_t>(said[c][1]))));
+        const float m = low(c, 3);
+        missed |= low(c, 2) == INFINITY;
+        l = l + Pair{low(c, 2), high(c, 2)};
+        if (m > 0.0f && low(c, 1) > -INFINITY) {
+          const Pair apart = two_sum(top_s, -low(c, 1)), part = two_product(m, apart.h);
+          l = l + Pair{part.h, __fmaf_rn(m, apart.l, part.l)};
+        }
       }
-      double l = d / static_cast<double>(a.temperature);
-      if (p_in > 0.0f) l -= static_cast<double>(p_in) * static_cast<double>(logf((z_t + z_tr) * inv_s));
+      const float inv_heat = 1.0f / a.temperature, off = __fmaf_rn(-inv_heat, a.temperature, 1.0f) * inv_heat;
+      const Pair of_t = two_product(l.h, inv_heat);
+      l = {of_t.h, of_t.l + __fmaf_rn(l.h, off, l.l * inv_heat)};
+      if (p_in > 0.0f) {
+        // The sums with what their last addition and the division leave out.
+        const Pair zt = two_sum(z_t, rest_w), zs = two_sum(zr_s, zi_s);
+        const float r = zt.h / zs.h;
+        const float left = (__fmaf_rn(-r, zs.h, zt.h) + zt.l - r * zs.l) / zt.h;
+        const float log_r = logf(r);
+        const Pair part = two_product(-p_in, log_r);
+        l = l + Pair{part.h, __fmaf_rn(-p_in, left, part.l)};
+      }
       // p_r / q_r as (1 + listed / others) of both
       if (p_rest > 0.0f) {
-        const float others = zr > 0.0f ? zi / zr : INFINITY;
-        const float gap = (ti == -INFINITY || zr == 0.0f) ? 0.0f : (ti - tr) * rate;
-        const float ratio = ti == -INFINITY ? 0.0f : others * exp2f(gap);
-        const float ls = ratio < 3.0e38f ? log1pf(ratio) : (zr > 0.0f ? logf(others) + gap * kLn2 : INFINITY);
-        const float ratio_t = z_t / z_tr;
-        const float lt = ratio_t < 1.0e30f ? log1pf(ratio_t) : logf(z_t) - logf(z_tr);
-        l += static_cast<double>(p_rest) * (static_cast<double>(ls) - static_cast<double>(lt));
+        float ls;
+        if (zr_s > 1.0e-30f) {
+          ls = log1pf(zi_s / zr_s);
+        } else if (zr > 0.0f) {
+          ls = logf(zi / zr) + (ti - tr) * rate * kLn2;
+        } else {
+          ls = INFINITY;
+        }
+        const float ratio_t = z_t / rest_w;
+        const float lt = ratio_t < 1.0e30f ? log1pf(ratio_t) : logf(z_t) - logf(rest_w);
+        l = ls == INFINITY ? Pair{INFINITY, 0.0f} : l + two_product(p_rest, ls - lt);
       }
-      if (p_in != p_in || z_s != z_s) l = static_cast<double>(p_in + z_s);
-      loss = static_cast<float>(l * static_cast<double>(a.temperature) * static_cast<double>(a.temperature) * static_cast<double>(w_row));
+      loss = missed ? INFINITY : l.h + l.l;
+      if (l.h == INFINITY) loss = INFINITY;
+      if (p_in != p_in || z_s != z_s) loss = p_in + z_s;
+      loss = loss * a.temperature * a.temperature * w_row;
     }
     a.loss[r] = loss;
   }
@@ -393,22 +500,33 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
       __syncthreads();
     }
     const uint4* src = reinterpret_cast<const uint4*>(piece);
+    const u64 nbase2 = pack2(-base, -base), rate2 = pack2(rate, rate), factor2 = pack2(factor, factor);
     auto grad_of = [&](float x) { return live ? ex2(__fmul_rn(__fsub_rn(x, base), rate)) * factor : 0.0f; };
     if (same) {
-      for (int v = tid; v < v1 - v0; v += kThreads) {
-        float x[E];
-        Vec<T>::unpack(src[v], x);
-        float g[E];
+      // The vectors inside of the row, then the one or two that reach past it.
+      const int f0 = max(v0, lead > 0 ? 1 : 0) - v0, f1 = min(v1, static_cast<int>((int64_t(a.vocab) + lead) / E)) - v0;
+      uint4* to = reinterpret_cast<uint4*>(out + j0);
+      if (live) {
+#pragma unroll 2
+        for (int v = f0 + tid; v < f1; v += kThreads) {
+          float x[E], g[E];
+          Vec<T>::unpack(src[v], x);
 #pragma unroll
-        for (int i = 0; i < E; ++i) g[i] = grad_of(x[i]);
-        const int64_t j = j0 + int64_t(v) * E;
-        if (j >= 0 && j + E <= a.vocab) {
-          __stcs(reinterpret_cast<uint4*>(out + j), pack_vec<T>(g));
-        } else {
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (j + i >= 0 && j + i < a.vocab) out[j + i] = from_float<T>(g[i]);
+          for (int i = 0; i < E; i += 2) {
+            const u64 z = mul2(add2(pack2(x[i], x[i + 1]), nbase2), rate2);
+            const u64 w = mul2(pack2(ex2(low2(z)), ex2(high2(z))), factor2);
+            g[i] = low2(w);
+            g[i + 1] = high2(w);
+          }
+          __stcs(to + v, pack_vec<T>(g));
         }
+      } else {
+        for (int v = f0 + tid; v < f1; v += kThreads) __stcs(to + v, make_uint4(0u, 0u, 0u, 0u));
+      }
+      if (tid < 2 * E && v0 < v1) {
+        const int v = tid < E ? 0 : v1 - v0 - 1;
+        const int64_t j = j0 + int64_t(v) * E + tid % E;
+        if ((v < f0 || v >= f1) && j >= 0 && j < a.vocab) out[j] = from_float<T>(grad_of(Vec<T>::one(piece[j - j0])));
       }
     } else {
       for (int64_t j = max(j0, int64_t(0)) + tid; j < min(j1, int64_t(a.vocab)); j += kThreads) out[j] = from_float<T>(grad_of(Vec<T>::one(piece[j - j0])));
@@ -422,26 +540,21 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     float p = prob[e];
     for (int o = e + 1; o < a.k; ++o)
       if (at[o] == at[e]) p += prob[o];
-    const float q = weight_of(score[e], top_s, rate) * inv_s;
+    const float q = weight_of(score[e], top_s, rate) * inv_s;  // at its first entry
     out[at[e]] = from_float<T>(scale * (q - p * inv_t));
   }
 }
 
-template <typename T>
-cudaError_t launch_t(const DistillLaunch& a, int* err, uint64_t timeout_ns, int num_sms, cudaStream_t st) {
-  auto fn = distill_kernel<T>;
-  constexpr int kMost = kPiece + 5 * 4 * kMaxTeacher;
+template <typename T, int kThreads>
+cudaError_t launch_t(const DistillLaunch& a, int cluster_bits, int piece, int* err, uint64_t timeout_ns, cudaStream_t st) {
+  const int cluster = 1 << cluster_bits;
+  auto fn = distill_kernel<T, kThreads>;
   static PerDeviceOnce once;
   const cudaError_t ready = once.run([fn] {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPiece + list_bytes(kMaxTeacher));
     return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (ready != cudaSuccess) return ready;
-  const int64_t bytes = (int64_t(a.vocab) * static_cast<int64_t>(sizeof(T)) / 16 + 2) * 16;
-  int cluster = 1;
-  while (cluster < kMaxCluster && bytes / cluster + 16 > kPiece) cluster *= 2;
-  while (cluster < kMaxCluster && a.rows * cluster < 2 * num_sms && bytes / cluster > 8192) cluster *= 2;
-  const int64_t piece = std::min<int64_t>(kPiece, (bytes / 16 / cluster + 1) * 16);
   // A grid has 2^31 - 1 CTAs: more rows go in parts.
   for (int64_t r = 0; r < a.rows; r += int64_t(1) << 26) {
     DistillLaunch p = a;
@@ -456,7 +569,7 @@ cudaError_t launch_t(const DistillLaunch& a, int* err, uint64_t timeout_ns, int 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows * cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(piece) + 5 * 4 * static_cast<size_t>(a.k);
+    cfg.dynamicSmemBytes = static_cast<size_t>(piece + list_bytes(a.k));
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -464,19 +577,30 @@ cudaError_t launch_t(const DistillLaunch& a, int* err, uint64_t timeout_ns, int 
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p, static_cast<int>(piece), err, timeout_ns);
+    cfg.numAttrs = cluster > 1;  // a launch with clusters starts its CTAs more slowly
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p, piece, cluster_bits, table_bits(a.k), kLog2e / a.temperature, err, timeout_ns);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
+template <typename T>
+cudaError_t launch_rows(const DistillLaunch& a, int* err, uint64_t timeout_ns, int num_sms, cudaStream_t st) {
+  const int64_t bytes = (int64_t(a.vocab) * static_cast<int64_t>(sizeof(T)) / 16 + 2) * 16;
+  int bits = 0;  // of the cluster's size
+  while (1 << bits < kMaxCluster && (bytes >> bits) + 16 > kAim) ++bits;
+  while (1 << bits < kMaxCluster && a.rows << bits < 2 * num_sms && bytes >> bits > 8192) ++bits;
+  const int piece = static_cast<int>(std::min<int64_t>(kPiece, ((bytes / 16 >> bits) + 1) * 16));
+  if (piece <= kSmallCta) return launch_t<T, 64>(a, bits, piece, err, timeout_ns, st);
+  return launch_t<T, kBigThreads>(a, bits, piece, err, timeout_ns, st);
+}
+
 }  // namespace
 
 cudaError_t launch_distill(const DistillLaunch& a, int* err, uint64_t timeout_ns, int num_sms, cudaStream_t st) {
-  if (a.dtype == kF32) return launch_t<float>(a, err, timeout_ns, num_sms, st);
-  if (a.dtype == kBF16) return launch_t<__nv_bfloat16>(a, err, timeout_ns, num_sms, st);
-  return launch_t<__half>(a, err, timeout_ns, num_sms, st);
+  if (a.dtype == kF32) return launch_rows<float>(a, err, timeout_ns, num_sms, st);
+  if (a.dtype == kBF16) return launch_rows<__nv_bfloat16>(a, err, timeout_ns, num_sms, st);
+  return launch_rows<__half>(a, err, timeout_ns, num_sms, st);
 }
 
 }  // namespace rbf

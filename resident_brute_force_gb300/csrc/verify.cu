@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyLaun
   }
 
   Sum s;
-  auto add = [&](auto n, const uint4 (&raw)[4]) {  // the first n vectors
+  auto add = [&](auto n, uint4 (&raw)[4]) {  // the first n vectors
     constexpr int N = decltype(n)::value;
     float x[E];
     uint4 best = raw[0];
@@ -134,19 +134,30 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyLaun
       s.top = top;
     }
     const bool inf = s.top == INFINITY;  // then only the scores that equal it count
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (inf) {
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        Vec<T>::unpack(raw[0], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.z += x[e] == INFINITY ? 1.0f : 0.0f;
+#pragma unroll
+        for (int o = 0; o < 3; ++o) raw[o] = raw[o + 1];
+      }
+      return;
+    }
+    const u64 ntop2 = pack2(-s.top, -s.top), rate2 = pack2(rate, rate);
+    u64 sum[2] = {0, 0};  // two zeros each
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       Vec<T>::unpack(raw[i], x);
-      if (inf) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s.z += x[e] == INFINITY ? 1.0f : 0.0f;
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[e % 4] += ex2(__fmul_rn(__fsub_rn(x[e], s.top), rate));
+      for (int e = 0; e < E; e += 2) {
+        const u64 z = mul2(add2(pack2(x[e], x[e + 1]), ntop2), rate2);
+        sum[e / 2 % 2] = add2(sum[e / 2 % 2], pack2(ex2(low2(z)), ex2(high2(z))));
       }
     }
-    s.z += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    sum[0] = add2(sum[0], sum[1]);
+    s.z += low2(sum[0]) + high2(sum[0]);
   };
   {
     const int f0 = max(v0, row.lead > 0 ? 1 : 0), f1 = min(v1, (row.n + row.lead) / E);
