@@ -64,20 +64,6 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { re
 template <>
 __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
-// The largest score of a vector.
-template <typename T>
-__device__ __forceinline__ float vec_top(const uint4& v) {
-  float x[Vec<T>::kLen];
-  if constexpr (sizeof(T) == 2) {
-    const uint32_t m = Vec<T>::max(Vec<T>::max(v.x, v.y), Vec<T>::max(v.z, v.w));
-    Vec<T>::unpack(make_uint4(m, m, m, m), x);
-    return fmaxf(x[0], x[1]);
-  } else {
-    Vec<T>::unpack(v, x);
-    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ uint4 pack_vec(const float (&g)[Vec<T>::kLen]) {
   uint4 r;

@@ -82,6 +82,20 @@ __device__ __forceinline__ uint4 vec_none() {
   return make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
 }
 
+// The largest score of a vector.
+template <typename T>
+__device__ __forceinline__ float vec_top(const uint4& v) {
+  float x[Vec<T>::kLen];
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t m = Vec<T>::max(Vec<T>::max(v.x, v.y), Vec<T>::max(v.z, v.w));
+    Vec<T>::unpack(make_uint4(m, m, m, m), x);
+    return fmaxf(x[0], x[1]);
+  } else {
+    Vec<T>::unpack(v, x);
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  }
+}
+
 // Scores i0 .. i0 + kLen - 1 of a row of n, -infinity where there are none; out
 // of line, for the one or two vectors of a row that reach past it.
 template <typename T>

@@ -38,6 +38,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxSplits = 64;
+constexpr int kStatsCtas = 6;  // an SM, in the rows' sums: 40 registers a thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);  // what fp32 leaves out
 constexpr int kDrawThreads = 1024;  // an SM, in the draw: 64 registers each
@@ -80,22 +81,22 @@ struct Sum {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyLaunch a, VerifyPart* parts, int splits) {
+__global__ void __launch_bounds__(kThreads, kStatsCtas) verify_stats_kernel(const VerifyLaunch a, VerifyPart* parts, int part_vecs) {
   constexpr int E = Vec<T>::kLen;
   __shared__ VerifyPart part[kWarps];
   pdl_launch_dependents();
   const int places = a.drafts + 1;
   const int rows = places + (a.draft ? a.drafts : 0);  // of a sequence: the target's, then the draft's
-  const int64_t row_id = blockIdx.x / splits;
-  const int split = static_cast<int>(blockIdx.x % splits);
-  const int64_t seq = row_id / rows;
-  const int in = static_cast<int>(row_id % rows);
+  // A sequence, its row, and the row's part.
+  const int64_t seq = blockIdx.x;
+  const int in = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z), splits = static_cast<int>(gridDim.z);
+  const int64_t row_id = seq * rows + in;
   const float rate = rate_of(a, seq);
   const int count = count_of(a, seq);
   const bool of_target = in < places;
   if (of_target ? in > count : (in - places >= count || rate == 0.0f)) return;
   const Row<T> row(of_target ? target_row<T>(a, seq, in) : draft_row<T>(a, seq, in - places), a.vocab);
-  const int v0 = static_cast<int>(int64_t(row.vecs) * split / splits), v1 = static_cast<int>(int64_t(row.vecs) * (split + 1) / splits);
+  const int v0 = min(row.vecs, split * part_vecs), v1 = min(row.vecs, v0 + part_vecs);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   if (rate == 0.0f) {  // the key of the best index
@@ -124,10 +125,7 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyLaun
     uint4 best = raw[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) best = vec_max<T>(best, raw[i]);
-    Vec<T>::unpack(best, x);
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < E; ++i) top = fmaxf(top, x[i]);
+    const float top = vec_top<T>(best);
     if (top == -INFINITY) return;
     if (top > s.top) {
       s.z = s.top == -INFINITY ? 0.0f : s.z * ex2(less_top(s.top, top) * rate);
@@ -184,13 +182,22 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyLaun
       }
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s.join(__shfl_xor_sync(kFullMask, s.top, d), __shfl_xor_sync(kFullMask, s.z, d), rate);
+  // Each below the largest of the warp, and then of the CTA.
+  auto below = [&](Sum& v, int lanes) {
+    float top = v.top;
+    for (int d = lanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, d));
+    v.z = v.top == -INFINITY ? 0.0f : v.z * ex2(less_top(v.top, top) * rate);
+    v.top = top;
+    for (int d = lanes / 2; d > 0; d >>= 1) v.z += __shfl_xor_sync(kFullMask, v.z, d);
+  };
+  below(s, 32);
   if (lane == 0) part[warp] = VerifyPart{s.top, s.z, 0};
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) s.join(part[w].top, part[w].z, rate);
-    parts[row_id * splits + split] = VerifyPart{s.top, s.z, 0};
+  if (warp == 0) {
+    s.top = part[lane % kWarps].top;
+    s.z = part[lane % kWarps].z;
+    below(s, kWarps);
+    if (lane == 0) parts[row_id * splits + split] = VerifyPart{s.top, s.z, 0};
   }
 }
 
@@ -297,7 +304,7 @@ struct Place {  // what one place's parts say
 };
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw_kernel(const VerifyLaunch a, const VerifyPart* parts, int splits) {
+__global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw_kernel(const VerifyLaunch a, const VerifyPart* parts, int splits, int cluster_bits) {
   constexpr int kWarps = kThreads / 32;
   constexpr int E = Vec<T>::kLen;
   __shared__ uint32_t roots[32];
@@ -306,11 +313,11 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   __shared__ int first_no;
   __shared__ Place row_p, row_q;
 
-  uint32_t rank, size;
+  uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  const uint32_t size = 1u << cluster_bits;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t seq = blockIdx.x / size;
+  const int64_t seq = blockIdx.x >> cluster_bits;
   const int places = a.drafts + 1, rows = places + (a.draft ? a.drafts : 0);
   // A CTA's shared memory may be written by others once it has started: all
   // arrive here and wait ahead of the first remote store.
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   // the target's vectors.
   const T* dq = with_q ? draft_row<T>(a, seq, accepted) : nullptr;
   auto load_q = [&](int v) { return vec_max<T>(load_shifted(dq, v * E - rp.lead, a.vocab), vec_none<T>()); };
-  const int c0 = static_cast<int>(int64_t(rp.vecs) * rank / size), c1 = static_cast<int>(int64_t(rp.vecs) * (rank + 1) / size);
+  const int c0 = static_cast<int>(int64_t(rp.vecs) * rank >> cluster_bits), c1 = static_cast<int>(int64_t(rp.vecs) * (rank + 1) >> cluster_bits);
   auto part_of = [](int lo, int hi, int w) { return lo + static_cast<int>(int64_t(hi - lo) * w / kWarps); };
   const int v0 = part_of(c0, c1, warp), v1 = part_of(c0, c1, warp + 1);
   int turn = 0;
@@ -583,8 +590,9 @@ cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int sp
   if (ready != cudaSuccess) return ready;
   // As many CTAs a row as run at once, of a vector a thread at least.
   const int64_t vecs = a.vocab * static_cast<int64_t>(sizeof(T)) / 16 + 2;
-  int cluster = 1;
-  while (cluster < kMaxCluster && a.seqs * cluster * 2 <= int64_t(num_sms) * (kDrawThreads / kThreads) && vecs / cluster > kThreads) cluster *= 2;
+  int bits = 0;
+  while (1 << bits < kMaxCluster && a.seqs << (bits + 1) <= int64_t(num_sms) * (kDrawThreads / kThreads) && vecs >> bits > kThreads) ++bits;
+  const int cluster = 1 << bits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.seqs * cluster));
   cfg.blockDim = dim3(kThreads);
@@ -598,7 +606,7 @@ cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int sp
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fn, a, parts, splits);
+  return cudaLaunchKernelEx(&cfg, fn, a, parts, splits, bits);
 }
 
 // Sixteen CTAs a row of 256 threads where that many run at once, else of 128: smaller
@@ -610,14 +618,14 @@ cudaError_t launch_draw(const VerifyLaunch& a, const VerifyPart* parts, int spli
 }
 
 // CTAs a row, of 8 KB at least, as many as the workspace has room for: the number
-// whose rounds of CTAs (eight an SM) read the least, a round's own time counted as 4 KB.
+// whose rounds of CTAs read the least, a CTA's own instructions counted as 16 KB.
 int splits_of(const VerifyLaunch& a, int64_t max_parts, int num_sms) {
   const int64_t rows = a.seqs * (a.drafts + 1 + (a.draft ? a.drafts : 0));
-  const int64_t bytes = a.vocab * static_cast<int64_t>(dtype_bytes(a.dtype)), places = int64_t(num_sms) * 8;
+  const int64_t bytes = a.vocab * static_cast<int64_t>(dtype_bytes(a.dtype)), places = int64_t(num_sms) * kStatsCtas;
   const int64_t most = std::min<int64_t>(std::min<int64_t>(kMaxSplits, max_parts / rows), bytes / 8192);
   int64_t best = 1, least = INT64_MAX;
   for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
-    const int64_t cost = (rows * s + places - 1) / places * (bytes / s + 4096);
+    const int64_t cost = (rows * s + places - 1) / places * (bytes / s + 16384);
     if (cost < least) {
       least = cost;
       best = s;
@@ -628,8 +636,10 @@ int splits_of(const VerifyLaunch& a, int64_t max_parts, int num_sms) {
 
 template <typename T>
 cudaError_t launch_stats(const VerifyLaunch& a, VerifyPart* parts, int splits, cudaStream_t st) {
-  const int64_t rows = a.seqs * (a.drafts + 1 + (a.draft ? a.drafts : 0));
-  verify_stats_kernel<T><<<static_cast<unsigned>(rows * splits), kThreads, 0, st>>>(a, parts, splits);
+  const unsigned rows = static_cast<unsigned>(a.drafts + 1 + (a.draft ? a.drafts : 0));
+  const int vecs = static_cast<int>(a.vocab * static_cast<int64_t>(sizeof(T)) / 16) + 2;  // wherever a row starts
+  verify_stats_kernel<T><<<dim3(static_cast<unsigned>(a.seqs), rows, static_cast<unsigned>(splits)), kThreads, 0, st>>>(
+      a, parts, (vecs + splits - 1) / splits);
   return cudaGetLastError();
 }
 
