@@ -67,6 +67,13 @@ __device__ __forceinline__ float less_top(float x, float top) {
   return top == INFINITY ? (x == INFINITY ? 0.0f : -INFINITY) : __fsub_rn(x, top);
 }
 
+// What fp32 leaves out of x - top = d.
+__device__ __forceinline__ float less_rest(float x, float top, float d) {
+  if (top == INFINITY || !(d > -INFINITY)) return 0.0f;
+  const float back = __fsub_rn(d, x);
+  return __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(top, back));
+}
+
 // ------------------------------------------------------------------- sums
 
 // Parts of a row in fp32: the largest score and the sum of weights below it.
@@ -233,7 +240,12 @@ struct Weights {
   __device__ __forceinline__ void divide(u64 all) {
     const int up = __clzll(static_cast<long long>(all));
     const uint32_t head = static_cast<uint32_t>((all << up) >> 32);  // its first 32 bits
-    const u64 f = (u64(1) << 63) / head;  // 2^31 .. 2^32: 2^(95 - up) / all
+    // 2^63 / head = 2^(95 - up) / all, in 2^31 .. 2^32: by fp32's reciprocal, and
+    // what that leaves of 2^63.
+    const float inv = __frcp_rn(static_cast<float>(head));
+    const u64 near = static_cast<u64>(inv * 0x1p63f);
+    const long long rest = static_cast<long long>((u64(1) << 63) - near * head);
+    const u64 f = near + static_cast<u64>(static_cast<long long>(rintf(static_cast<float>(rest) * inv)));
     factor = f > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(f);
     one += up - 2;  // m f / 2^31 = m 2^(64 - up) / all; a share of 2^62 is m 2^(62 + one) / all
   }
@@ -252,11 +264,12 @@ struct Weights {
     const u64 n = fma2(hi, pack2(32.0f, 32.0f), pack2(12582912.0f, 12582912.0f));
     const u64 whole = add2(n, pack2(-12582912.0f, -12582912.0f));
     const u64 f = add2(fma2(whole, pack2(-1.0f / 32.0f, -1.0f / 32.0f), hi), lo);
-    // 2^f - 1, |f| < 2^-5: the series of exp(f ln 2).
-    u64 g = fma2(f, pack2(9.6181291e-3f, 9.6181291e-3f), pack2(5.5504109e-2f, 5.5504109e-2f));
-    g = fma2(f, g, pack2(2.4022651e-1f, 2.4022651e-1f));
-    g = fma2(f, g, pack2(6.9314718e-1f, 6.9314718e-1f));
-    g = mul2(mul2(f, g), pack2(4294967296.0f, 4294967296.0f));
+    // 2^32 (2^f - 1), |f| < 2^-5: the series of exp(f ln 2).
+    constexpr float c1 = 0x1p32f * 6.9314718e-1f, c2 = 0x1p32f * 2.4022651e-1f, c3 = 0x1p32f * 5.5504109e-2f, c4 = 0x1p32f * 9.6181291e-3f;
+    u64 g = fma2(f, pack2(c4, c4), pack2(c3, c3));
+    g = fma2(f, g, pack2(c2, c2));
+    g = fma2(f, g, pack2(c1, c1));
+    g = mul2(f, g);
     w0 = place<SHARES>(low2(n), low2(g));
     w1 = place<SHARES>(high2(n), high2(g));
   }
@@ -264,12 +277,12 @@ struct Weights {
  private:
   template <bool SHARES>
   __device__ __forceinline__ u64 place(float n, float g) const {
-    const int e = static_cast<int>(__float_as_uint(n) - 0x4B400000u);
-    const int root = static_cast<int>(roots[e & 31]);
+    const uint32_t e = __float_as_uint(n);  // 0x4B400000 and the 32nds
+    const int root = static_cast<int>(roots[e & 31u]);
     uint32_t m = static_cast<uint32_t>(root + __mulhi(root, __float2int_rn(g)));
     if (SHARES) m = __umulhi(m << 1, factor);
     u64 w;  // m 2^(one + e / 32), nothing left of it past 64
-    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(m) << 32), "r"(32 - one - (e >> 5)));
+    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(m) << 32), "r"(32 + (0x4B400000 >> 5) - one - static_cast<int>(e >> 5)));
     return w;
   }
 };
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   constexpr int E = Vec<T>::kLen;
   __shared__ uint32_t roots[32];
   __shared__ u64 slot[4][kMaxCluster];  // a word per CTA, written by all of them
-  __shared__ u64 kept[kWarps];
+  __shared__ u64 kept[kWarps], kept_too[kWarps];
   __shared__ int first_no;
   __shared__ Place row_p, row_q;
 
@@ -319,14 +332,17 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t seq = blockIdx.x >> cluster_bits;
   const int places = a.drafts + 1, rows = places + (a.draft ? a.drafts : 0);
-  // A CTA's shared memory may be written by others once it has started: all
-  // arrive here and wait ahead of the first remote store.
-  if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  auto cluster_meets = [&]() {
+    if (size > 1)
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+      __syncthreads();
+  };
   const float rate = rate_of(a, seq);
   const int count = count_of(a, seq);
   if (threadIdx.x < 32) roots[threadIdx.x] = kRoots[threadIdx.x];
   if (threadIdx.x == 0) first_no = count;
-  __syncthreads();
+  cluster_meets();  // a CTA's shared memory may be written by others now
   pdl_wait();
 
   // The sums of a row, from its parts (every lane of a warp).
@@ -354,43 +370,41 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
 
   int32_t* token = a.token + seq * places;
   float* logprob = a.logprob ? a.logprob + seq * places : nullptr;
-  for (int i = warp; i < count; i += kWarps) {
+  // A place a warp of the cluster; all that it needs is read at once.
+  for (int i = static_cast<int>(rank) * kWarps + warp; i < count; i += kWarps << cluster_bits) {
     const int x = a.draft_token[seq * a.drafts + i];
-    bool ok = x >= 0 && x < a.vocab;
+    const float u = a.u[seq * places + i];
+    const bool inside = x >= 0 && x < a.vocab;
+    bool ok;
     float lp = 0.0f;
     if (rate == 0.0f) {
-      const int best = best_of(i);
-      ok = ok && best == x;
-    } else if (ok) {
-      const Place p = join(i);
-      const float xp = score(target_row<T>(a, seq, i), x);
+      ok = inside && best_of(i) == x;
+    } else {
+      const float xp = inside ? score(target_row<T>(a, seq, i), x) : -INFINITY;
+      const float xq = inside && a.draft ? score(draft_row<T>(a, seq, i), x) : 0.0f;
+      const Place p = join(i), q = a.draft ? join(places + i) : Place{0.0f, 1.0f};
       ok = xp > -INFINITY;
       lp = log_p(xp, p);
-      if (ok) {
-        // u q / p < 1, with the exponents' difference in 64 bits.
-        double diff = -static_cast<double>(less_top(xp, p.top));
-        float ratio = p.z;
-        if (a.draft) {
-          const Place q = join(places + i);
-          const float xq = score(draft_row<T>(a, seq, i), x);
-          diff += xq > -INFINITY ? static_cast<double>(less_top(xq, q.top)) : -INFINITY;
-          ratio = xq > -INFINITY ? __fdiv_rn(p.z, q.z) : 0.0f;
-        }
-        const double e = diff * static_cast<double>(rate), n = rint(e);
-        const float m = exp2f(static_cast<float>(e - n));
-        ok = ratio == 0.0f ? a.u[seq * places + i] == a.u[seq * places + i]
-                           : a.u[seq * places + i] * (ratio * m) * exp2f(static_cast<float>(fmin(fmax(n, -1000.0), 1000.0))) < 1.0f;
-      }
+      // u q / p < 1, with the difference of the exponents as the sum of two numbers
+      // (64-bit arithmetic runs at a 64th of fp32's rate).
+      const float dp = less_top(xp, p.top), up = less_rest(xp, p.top, dp), dq = less_top(xq, q.top), uq = less_rest(xq, q.top, dq);
+      const float d = __fsub_rn(dq, dp), back = __fsub_rn(d, dq);
+      const float lost = __fadd_rn(__fsub_rn(__fsub_rn(dq, __fsub_rn(d, back)), __fadd_rn(dp, back)), __fsub_rn(uq, up));
+      const float e = __fmul_rn(d, rate), n = rintf(fminf(fmaxf(e, -1000.0f), 1000.0f));
+      const float f = fabsf(e) < 1000.0f ? __fadd_rn(__fsub_rn(e, n), __fmaf_rn(lost, rate, __fmaf_rn(d, rate, -e))) : 0.0f;
+      if (xq > -INFINITY)
+        ok = ok && u * (__fdiv_rn(p.z, q.z) * exp2f(f)) * exp2f(0.5f * n) * exp2f(0.5f * n) < 1.0f;
+      else  // no mass of the draft's
+        ok = ok && u == u;
     }
+    if (!ok && lane < static_cast<int>(size))
+      asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(remote(&first_no, lane)), "r"(i) : "memory");
     if (lane == 0) {
-      if (!ok) atomicMin(&first_no, i);
-      if (rank == 0) {
-        token[i] = x;
-        if (logprob) logprob[i] = lp;
-      }
+      token[i] = x;
+      if (logprob) logprob[i] = lp;
     }
   }
-  __syncthreads();
+  cluster_meets();
   const int accepted = first_no;
   const bool late = accepted < count;  // a token was refused
   if (rank == 0) {
@@ -408,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
         if (logprob) logprob[accepted] = 0.0f;
       }
     }
-    if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     return;
   }
   if (warp == 0) {
@@ -419,7 +432,6 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
     if (lane == 0) row_q = q;
   }
   __syncthreads();
-  if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const Place pp = row_p;
   if (pp.top == -INFINITY) return;  // nothing is left of the row: -1 stays
   const bool with_q = late && a.draft && row_q.top > -INFINITY;
@@ -435,21 +447,28 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   auto part_of = [](int lo, int hi, int w) { return lo + static_cast<int>(int64_t(hi - lo) * w / kWarps); };
   const int v0 = part_of(c0, c1, warp), v1 = part_of(c0, c1, warp + 1);
   int turn = 0;
-  // Sum over the cluster of every thread's v; slot[turn - 1] keeps the CTAs' own.
-  auto total_of = [&](u64 v) {
+  // Sum over the cluster of every thread's v (and w); slot[turn - 1] keeps the CTAs' own.
+  auto total_of = [&](u64 v, u64* w) {
     v = warp_sum(v);
-    if (lane == 0) kept[warp] = v;
+    if (w) *w = warp_sum(*w);
+    if (lane == 0) {
+      kept[warp] = v;
+      if (w) kept_too[warp] = *w;
+    }
     __syncthreads();
-    u64 r = lane < kWarps ? kept[lane] : 0ull;
-    r = warp_sum(r);
-    if (threadIdx.x < size) remote_store(remote(&slot[turn][rank], threadIdx.x), r);
-    if (size > 1)
-      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    else
-      __syncthreads();
-    r = lane < static_cast<int>(size) ? slot[turn][lane] : 0ull;
-    ++turn;
-    return warp_sum(r);
+    if (warp == 0) {
+      v = warp_sum(lane < kWarps ? kept[lane] : 0ull);
+      if (lane < static_cast<int>(size)) remote_store(remote(&slot[turn][rank], lane), v);
+      if (w) {
+        *w = warp_sum(lane < kWarps ? kept_too[lane] : 0ull);
+        if (lane < static_cast<int>(size)) remote_store(remote(&slot[turn + 1][rank], lane), *w);
+      }
+    }
+    cluster_meets();
+    if (w) *w = warp_sum(lane < static_cast<int>(size) ? slot[turn + 1][lane] : 0ull);
+    v = warp_sum(lane < static_cast<int>(size) ? slot[turn][lane] : 0ull);
+    turn += w ? 2 : 1;
+    return v;
   };
 
   // log2(e) / T as the sum of two numbers (one, where it is at an end of the range).
@@ -504,9 +523,8 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
         sum_q += a0 + a1;
       }
     });
-    const u64 all_p = total_of(sum_p);
-    wp.divide(all_p);
-    wq.divide(total_of(sum_q));
+    wp.divide(total_of(sum_p, &sum_q));
+    wq.divide(sum_q);
   }
   bool left = with_q || out >= 0;
   auto weigh = [&](int v, const uint4& vp, const uint4& vq, u64 (&w)[E]) {
@@ -542,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
 #pragma unroll
       for (int e = 0; e < E; ++e) sum += w[e];
     });
-    return total_of(sum);
+    return total_of(sum, nullptr);
   };
   u64 total = sum_left();
   if (left && total == 0) {  // p and q agree (or p is all on the refused token): what is left is rounding
