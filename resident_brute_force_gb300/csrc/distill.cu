@@ -36,6 +36,7 @@ constexpr int kSmallCta = 8192;
 constexpr int kBigThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2Low = 0.6931471805599453 - static_cast<double>(kLn2);  // what fp32 leaves out
 
 // The number of a score in shared memory that is not one of the types', as its bits.
 template <typename T>
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
   int* first = key + (1 << bits);
   __shared__ uint64_t full;
   __shared__ float red[2][kWarps];
-  __shared__ float of_warp[8][32];  // what each warp says of its part; zeros past kWarps
+  __shared__ float of_warp[9][32];  // what each warp says of its part; zeros past kWarps
   __shared__ u64 said[kMaxCluster][kWords];
 
   uint32_t rank;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
   fetch(c0, min(c1, c0 + piece_vecs));  // its barrier is the issuing thread's own so far
   if (a.k)
     for (int s = tid; s < 2 << bits; s += kThreads) key[s] = s < 1 << bits ? -1 : INT32_MAX;
-  for (int i = tid; i < 8 * 32; i += kThreads) of_warp[0][i] = i < 64 ? -INFINITY : 0.0f;  // two largest scores, six sums
+  for (int i = tid; i < 9 * 32; i += kThreads) of_warp[0][i] = i < 64 ? -INFINITY : 0.0f;  // two largest scores, seven sums
   __syncthreads();
 
   // ------------------------------------------- the teacher, ahead of the scores
@@ -306,7 +307,9 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     }
   }
 
-  const float rest_w = weight_of(rest_t, top_t, rate);
+  // With what fp32 leaves out of rest * T.
+  const float rest_low = fabsf(rest_t) < 1.0e30f ? __fmaf_rn(rest_raw, a.temperature, -rest_t) : 0.0f;
+  const float rest_w = __fmaf_rn(weight_of(rest_t, top_t, rate), rest_low * rate * kLn2, weight_of(rest_t, top_t, rate));
   z_t = fold(1, plus);
   const float all_t = z_t + rest_w;
   const float inv_t = all_t == 0.0f ? 0.0f : 1.0f / all_t;
@@ -328,8 +331,8 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     for (int e = tid; e < a.k; e += kThreads)
       if (at[e] >= 0) top_in = fmaxf(top_in, score[owner[e]]);
     top_in = warp_fold(top_in, fmax2);
-    float z_in = 0.0f, mass = 0.0f, missed = 0.0f;
-    Pair diff;
+    float z_in = 0.0f, missed = 0.0f;
+    Pair diff, mass;
     for (int e = tid; e < a.k; e += kThreads) {
       if (at[e] < 0) continue;
       const float s = score[owner[e]];
@@ -340,18 +343,21 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
           missed = 1.0f;
         else
           diff = diff + two_product(p, (logit[e] - top_t) - (s - top_in));
-        mass += p;
+        mass = mass + Pair{p, 0.0f};
       }
     }
     z_in = warp_fold(z_in, plus);
-    mass = warp_fold(mass, plus);
     missed = warp_fold(missed, fmax2);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) diff = diff + Pair{__shfl_xor_sync(kFullMask, diff.h, d), __shfl_xor_sync(kFullMask, diff.l, d)};
+    for (int d = 16; d > 0; d >>= 1) {
+      diff = diff + Pair{__shfl_xor_sync(kFullMask, diff.h, d), __shfl_xor_sync(kFullMask, diff.l, d)};
+      mass = mass + Pair{__shfl_xor_sync(kFullMask, mass.h, d), __shfl_xor_sync(kFullMask, mass.l, d)};
+    }
     if (lane == 0) {
       of_warp[1][warp] = top_in;
       of_warp[3][warp] = z_in;
-      of_warp[4][warp] = mass;
+      of_warp[4][warp] = mass.h;
+      of_warp[8][warp] = mass.l;
       of_warp[5][warp] = missed;
       of_warp[6][warp] = diff.h;
       of_warp[7][warp] = diff.l;
@@ -379,11 +385,14 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     for (int o = kWarps / 2; o > 0; o >>= 1) d = d + Pair{__shfl_xor_sync(kFullMask, d.h, o), __shfl_xor_sync(kFullMask, d.l, o)};
     d = {__shfl_sync(kFullMask, d.h, 0), __shfl_sync(kFullMask, d.l, 0)};
     if (among(of_warp[5][lane], fmax2) > 0.0f) d = {INFINITY, 0.0f};
-    const float mass = among(m, plus);
+    Pair mass{m, of_warp[8][lane]};
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) mass = mass + Pair{__shfl_xor_sync(kFullMask, mass.h, o), __shfl_xor_sync(kFullMask, mass.l, o)};
+    mass = {__shfl_sync(kFullMask, mass.h, 0), __shfl_sync(kFullMask, mass.l, 0)};
     for (int i = lane; i < kWords * static_cast<int>(size); i += 32) {
       const int word = i % kWords;
-      const float lo = word == 0 ? tr : word == 1 ? ti : word == 2 ? d.h : mass;
-      const float hi = word == 0 ? zr : word == 1 ? zi : word == 2 ? d.l : 0.0f;
+      const float lo = word == 0 ? tr : word == 1 ? ti : word == 2 ? d.h : mass.h;
+      const float hi = word == 0 ? zr : word == 1 ? zi : word == 2 ? d.l : mass.l;
       remote_store(remote(&said[rank][word], static_cast<uint32_t>(i / kWords)), static_cast<u64>(__float_as_uint(hi)) << 32 | __float_as_uint(lo));
     }
   }
@@ -420,28 +429,36 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     float loss = 0.0f;
     if (live) {
       // sum p_e (log p_e - log q_e) = sum p_e ((t_e - largest t) - (s_e - largest s)) / T - P log(Z_t / Z_s)
-      Pair l;
+      // with P the sum of the very numbers p_e that stand in the first sum.
+      Pair l, mass;
       bool missed = false;
       for (uint32_t c = 0; c < size; ++c) {
         const float m = low(c, 3);
         missed |= low(c, 2) == INFINITY;
         l = l + Pair{low(c, 2), high(c, 2)};
+        mass = mass + Pair{m, high(c, 3)};
         if (m > 0.0f && low(c, 1) > -INFINITY) {
           const Pair apart = two_sum(top_s, -low(c, 1)), part = two_product(m, apart.h);
           l = l + Pair{part.h, __fmaf_rn(m, apart.l, part.l)};
         }
       }
-      const float inv_heat = 1.0f / a.temperature, off = __fmaf_rn(-inv_heat, a.temperature, 1.0f) * inv_heat;
-      const Pair of_t = two_product(l.h, inv_heat);
-      l = {of_t.h, of_t.l + __fmaf_rn(l.h, off, l.l * inv_heat)};
+      // Over the very T of the weights, log2(e) / rate: its 2^-25 would stand against logarithms of their sums.
+      Pair of_t = two_product(rate, kLn2);
+      of_t.l = __fmaf_rn(rate, kLn2Low, of_t.l);
+      const Pair by_t = two_product(l.h, of_t.h);
+      l = {by_t.h, by_t.l + __fmaf_rn(l.h, of_t.l, l.l * of_t.h)};
       if (p_in > 0.0f) {
         // The sums with what their last addition and the division leave out.
         const Pair zt = two_sum(z_t, rest_w), zs = two_sum(zr_s, zi_s);
         const float r = zt.h / zs.h;
         const float left = (__fmaf_rn(-r, zs.h, zt.h) + zt.l - r * zs.l) / zt.h;
-        const float log_r = logf(r);
-        const Pair part = two_product(-p_in, log_r);
-        l = l + Pair{part.h, __fmaf_rn(-p_in, left, part.l)};
+        // log r = n log 2 + the logarithm of a number near 1, which keeps its last bits.
+        const int bits_r = __float_as_int(r), n = (bits_r - 0x3F3504F3) >> 23;
+        const float of_n = static_cast<float>(n);
+        const Pair whole = two_product(of_n, kLn2), near = two_sum(whole.h, logf(__int_as_float(bits_r - (n << 23))));
+        const Pair log_r{near.h, near.l + whole.l + of_n * kLn2Low + left};
+        const Pair part = two_product(-mass.h, log_r.h);
+        l = l + Pair{part.h, __fmaf_rn(-mass.h, log_r.l, __fmaf_rn(-mass.l, log_r.h, part.l))};
       }
       // p_r / q_r as (1 + listed / others) of both
       if (p_rest > 0.0f) {
