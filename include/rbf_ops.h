@@ -56,7 +56,7 @@ typedef enum rbf_dtype {
 /* Largest depth (values of one row) of an 8-bit matrix: every sum of that
  * many products fits 32 bits. */
 #define RBF_OPS_MAX_DEPTH 65536
-/* Largest row that sample_dev draws from. */
+/* Largest row that sample_dev draws from, and of verify_dev and distill_dev. */
 #define RBF_OPS_MAX_VOCAB (1 << 26)
 /* Most drafted tokens of a sequence of verify_dev. */
 #define RBF_OPS_MAX_DRAFTS 1024
@@ -67,7 +67,8 @@ typedef enum rbf_dtype {
  * values (1 .. 2^20 and 1 .. RBF_OPS_MAX_DEPTH; max_rows counts the rows of
  * the first operand, the queries or tokens; the second operand's rows are not
  * limited). Its workspace is max_rows x max_depth 16-bit numbers, and up to
- * 40 MB for partial sums and 32 MB for rows that are put on 16-byte boundaries.
+ * 40 MB for partial sums, 32 MB for rows that are put on 16-byte boundaries and
+ * 0.3 MB (64 bytes a row more) for verify_dev's sums.
  *   cuda_stream  stream of every call (NULL: the handle creates its own;
  *                cudaStreamLegacy names the default stream)
  * Errors: INVALID_VALUE, OUT_OF_MEMORY, CUDA. */
@@ -191,7 +192,10 @@ rbf_status quantize_f8_dev(rbf_ops* ops, const void* d_x, rbf_dtype x_dtype, int
 /* out[i, j] = sum_c a_scale[i, c] * b_scale[j / block_rows, c] * sum_{k in block c} a[i, k] b[j, k] + bias[j],
  * block c being the values 128 c .. 128 c + 127 of a row. A block's products are
  * summed in fp32, and the blocks' sums with their scales too; the result is
- * rounded once to out_dtype. It is the same for every replay.
+ * rounded once to out_dtype. It is the same for every replay. Rows of a and b are
+ * read fastest from a 16-byte boundary with a stride that is a multiple of 16: others
+ * are first put on such boundaries in the handle's workspace, a's with one more
+ * launch, b's up to 32 MB at a time with one more launch each.
  *   d_a        [m, k] of a_dtype (E4M3 or E5M2), stride ld_a; m <= max_rows
  *   d_a_scale  [m, ceil(k / 128)] fp32, stride ld_a_scale
  *   d_b        [n, k] of b_dtype (E4M3 or E5M2), stride ld_b
@@ -223,8 +227,9 @@ rbf_status matmul_f8_dev(rbf_ops* ops, const void* d_a, rbf_dtype a_dtype, int64
  * target's own. A NaN score counts as -infinity, which has no probability; where
  * +infinity is a row's largest score only the scores that equal it have any. A
  * place whose scores are all -infinity accepts no token and answers -1. At an
- * infinite T every finite score has the same probability. At a T not above 0, or NaN, p has all of it on the first of the best indices, a token
- * is accepted if it is that one, and log-probabilities are 0.
+ * infinite T every finite score has the same probability. At a T not above 0, or
+ * NaN, p has all of it on the first of the best indices, a token is accepted if it
+ * is that one, and log-probabilities are 0.
  * Scores that were masked to -infinity stand for any filter of either side.
  *   d_target       [seqs, drafts + 1, vocab] of dtype (F32, BF16 or F16): ld_target
  *                  from place to place, ld_target_seq from sequence to sequence
@@ -260,8 +265,8 @@ rbf_status verify_dev(rbf_ops* ops, const void* d_target, int64_t ld_target_seq,
  * search's list) does not count; entries with the same index add up in the
  * gradient. A listed score of -infinity with p_e above 0 makes the loss infinite.
  * A row of weight 0, without any entry or remaining mass, or whose scores are all
- * -infinity has loss 0 and gradient 0; else a NaN, or +infinity, among its scores,
- * logits or weight makes both NaN.
+ * -infinity has loss 0 and gradient 0; else a NaN, or +infinity, among its scores
+ * or logits makes both NaN. (The weight multiplies both.)
  *   d_scores   [rows, vocab] of dtype (F32, BF16 or F16), stride ld_scores
  *   d_index    [rows, k] int32, stride ld_index
  *   d_teacher  [rows, k] of teacher_dtype (F32, BF16 or F16), stride ld_teacher
@@ -269,7 +274,8 @@ rbf_status verify_dev(rbf_ops* ops, const void* d_target, int64_t ld_target_seq,
  *   d_weight   [rows] fp32 (NULL: 1): of a mean 1 / rows, of a backward pass the
  *              loss' gradient
  *   d_loss     [rows] fp32 (NULL: not wanted)
- *   d_grad     [rows, vocab] of dtype, stride ld_grad (NULL: not wanted)
+ *   d_grad     [rows, vocab] of dtype, stride ld_grad (NULL: not wanted); d_scores
+ *              itself, with its stride, is fine: a score is read before its place is written
  * T = temperature, 2^-20 .. 2^20. k <= RBF_OPS_MAX_TEACHER, vocab <=
  * RBF_OPS_MAX_VOCAB. Errors: INVALID_VALUE, CUDA; a device-side timeout through
  * rbf_ops_check_device_error. */

@@ -75,9 +75,10 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[kLen<T>]) {
 }
 
 // kLen values from column c on of a row of `cols` (0 past it).
-// WHOLE: every piece lies within the row and on its boundary.
+// WHOLE: every piece lies within the row and on its boundary. (Column numbers are
+// unsigned: a row's last block may reach past 2^31.)
 template <bool WHOLE, typename T>
-__device__ __forceinline__ uint4 load_piece(const T* row, int c, int cols, bool wide) {
+__device__ __forceinline__ uint4 load_piece(const T* row, uint32_t c, uint32_t cols, bool wide) {
   if (WHOLE || (wide && c + kLen<T> <= cols)) return __ldcs(reinterpret_cast<const uint4*>(row + c));
   uint4 r = make_uint4(0u, 0u, 0u, 0u);
   T* e = reinterpret_cast<T*>(&r);
@@ -98,7 +99,7 @@ __device__ __forceinline__ uint32_t piece_top(const uint4& v) {
 }
 
 template <bool WHOLE, typename T, __nv_fp8_interpretation_t F8>
-__device__ __forceinline__ void store_piece(uint8_t* row, int c, int cols, bool wide, const uint4& v, float inv) {
+__device__ __forceinline__ void store_piece(uint8_t* row, uint32_t c, uint32_t cols, bool wide, const uint4& v, float inv) {
   float x[kLen<T>];
   unpack<T>(v, x);
   uint16_t h[kLen<T> / 2];
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) quantize_f8_rows_kernel(const Quanti
   const T* x = static_cast<const T*>(a.x);
   uint8_t* q = static_cast<uint8_t*>(a.q);
   const bool wide_x = rows_on(x, a.ld_x * static_cast<int64_t>(sizeof(T)), 16), wide_q = rows_on(q, a.ld_q, kLen<T>);
-  const int per = (a.cols + kBlock - 1) / kBlock;
+  const int per = (a.cols - 1) / kBlock + 1;
   const int lane = threadIdx.x & 31, sub = lane % kLanes;
   const int64_t all = a.rows << bits, step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
   struct Group {
@@ -152,19 +153,19 @@ __global__ void __launch_bounds__(kThreads) quantize_f8_rows_kernel(const Quanti
     g.r = u >> bits;
     const int b0 = static_cast<int>(u & ((int64_t(1) << bits) - 1)) * kGroup<T>;
     g.b0 = b0 + lane / kLanes;
-    g.whole = wide_x && wide_q && (b0 + kGroup<T>) * kBlock <= a.cols;
+    g.whole = wide_x && wide_q && static_cast<uint32_t>(b0 + kGroup<T>) * kBlock <= static_cast<uint32_t>(a.cols);
     return g;
   };
   auto load = [&](const Group& g, uint4 (&v)[kAhead]) {
     const T* row = x + g.r * a.ld_x;
     if (g.whole) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) v[j] = load_piece<true>(row, (g.b0 + j * (32 / kLanes)) * kBlock + sub * kLen<T>, a.cols, true);
+      for (int j = 0; j < kAhead; ++j) v[j] = load_piece<true>(row, static_cast<uint32_t>(g.b0 + j * (32 / kLanes)) * kBlock + sub * kLen<T>, a.cols, true);
     } else {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int b = g.b0 + j * (32 / kLanes);
-        v[j] = b < per ? load_piece<false>(row, b * kBlock + sub * kLen<T>, a.cols, wide_x) : make_uint4(0u, 0u, 0u, 0u);
+        v[j] = b < per ? load_piece<false>(row, static_cast<uint32_t>(b) * kBlock + sub * kLen<T>, a.cols, wide_x) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
   };
@@ -184,7 +185,8 @@ __global__ void __launch_bounds__(kThreads) quantize_f8_rows_kernel(const Quanti
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int b = g.b0 + j * (32 / kLanes), c = b * kBlock + sub * kLen<T>;
+      const int b = g.b0 + j * (32 / kLanes);
+      const uint32_t c = static_cast<uint32_t>(b) * kBlock + sub * kLen<T>;
       uint32_t m = piece_top<T>(v[j]);
 #pragma unroll
       for (int d = kLanes / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, d));
@@ -214,11 +216,11 @@ __global__ void __launch_bounds__(kTileThreads<T>, sizeof(T) == 2 ? 6 : 2) quant
   const T* x = static_cast<const T*>(a.x);
   uint8_t* q = static_cast<uint8_t*>(a.q);
   const bool wide_x = rows_on(x, a.ld_x * static_cast<int64_t>(sizeof(T)), 16), wide_q = rows_on(q, a.ld_q, kLen<T>);
-  const int per = (a.cols + kBlock - 1) / kBlock;
+  const int per = (a.cols - 1) / kBlock + 1;
   const int bi = static_cast<int>(blockIdx.x) / per, bj = static_cast<int>(blockIdx.x) - bi * per;
-  const bool whole = wide_x && wide_q && (bj + 1) * kBlock <= a.cols && int64_t(bi + 1) * kBlock <= a.rows;
+  const bool whole = wide_x && wide_q && static_cast<uint32_t>(bj + 1) * kBlock <= static_cast<uint32_t>(a.cols) && int64_t(bi + 1) * kBlock <= a.rows;
   const int64_t r0 = static_cast<int64_t>(bi) * kBlock + threadIdx.x / kLanes;
-  const int c = bj * kBlock + static_cast<int>(threadIdx.x % kLanes) * kLen<T>;
+  const uint32_t c = static_cast<uint32_t>(bj) * kBlock + threadIdx.x % kLanes * kLen<T>;
   auto tile = [&](auto is_whole) {
     constexpr bool kWhole = decltype(is_whole)::value;
     uint4 v[kPasses];
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kTileThreads<T>, sizeof(T) == 2 ? 6 : 2) quant
 
 template <typename T, __nv_fp8_interpretation_t F8>
 cudaError_t launch_t(const QuantizeF8Launch& a, int num_sms, cudaStream_t st) {
-  const int per = (a.cols + kBlock - 1) / kBlock;
+  const int per = (a.cols - 1) / kBlock + 1;
   if (a.block_rows == 1) {
     int bits = 0;
     while (int64_t(kGroup<T>) << bits < per) ++bits;
