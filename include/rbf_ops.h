@@ -246,7 +246,7 @@ rbf_status matmul_f8_dev(rbf_ops* ops, const void* d_a, rbf_dtype a_dtype, int64
  *   d_logprob      [seqs, drafts + 1] fp32 (may be NULL): log p of each of
  *                  d_token's entries, -infinity where that is -1
  * The sums that a token's acceptance depends on are fp32 ones; the drawn
- * index is decided by 64-bit integers that hold each probability to 2^-30 of itself.
+ * index is decided by 64-bit integers that hold each probability to 2^-29 of itself.
  * seqs * (drafts + 1) <= max_rows, drafts <= RBF_OPS_MAX_DRAFTS,
  * vocab <= RBF_OPS_MAX_VOCAB. Errors: INVALID_VALUE, CUDA. */
 rbf_status verify_dev(rbf_ops* ops, const void* d_target, int64_t ld_target_seq, int64_t ld_target, const void* d_draft,

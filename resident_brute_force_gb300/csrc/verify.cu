@@ -17,10 +17,10 @@
 //
 // The draw lies between running sums of up to 2^26 numbers, so its sums are of
 // 64-bit integers, exact and in any order, and each number in them is right to
-// 2^-30 of itself: weights in fp32 would put some draws in a thousand on another
-// index than 64 bits do, where the tail is long. 2^z with z = (x - max) log2(e) / T
-// as the sum of two fp32 numbers, split into whole 32nds (a table of 31-bit
-// integers) and a rest of at most 2^-6 (a polynomial, as a 32-bit fraction).
+// 2^-29 of itself: weights in fp32 would put some draws in a thousand on another
+// index than 64 bits do, where the tail is long. 2^z is taken by z's whole 32nds (a
+// table of 31-bit integers, a lane of the warp each) and a rest of at most 2^-6 (a
+// polynomial, as a 32-bit fraction).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,6 +38,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxSplits = 64;
+constexpr int kGroupVecs = 4 * kThreads;  // vectors that a CTA of the rows' sums takes at a time
 constexpr int kStatsCtas = 6;  // an SM, in the rows' sums: 40 registers a thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);  // what fp32 leaves out
@@ -169,17 +170,13 @@ __global__ void __launch_bounds__(kThreads, kStatsCtas) verify_stats_kernel(cons
     const uint4* src = reinterpret_cast<const uint4*>(row.p - row.lead);
     uint4 raw[4];
     int v = f0 + static_cast<int>(threadIdx.x);
-    for (; v + 3 * kThreads < f1; v += 4 * kThreads) {
+#pragma unroll 1
+    for (; v < f1; v += kGroupVecs) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) raw[i] = src[v + i * kThreads];
+      for (int i = 0; i < 4; ++i) raw[i] = v + i * kThreads < f1 ? src[v + i * kThreads] : vec_none<T>();
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw[i] = vec_max<T>(raw[i], vec_none<T>());
       add(std::integral_constant<int, 4>{}, raw);
-    }
-#pragma unroll 1
-    for (; v < f1; v += kThreads) {
-      raw[0] = vec_max<T>(src[v], vec_none<T>());
-      add(std::integral_constant<int, 1>{}, raw);
     }
     if (threadIdx.x < 2 && v0 < v1) {  // the one or two vectors that reach past the row
       const int e = threadIdx.x == 0 ? v0 : v1 - 1;
@@ -210,6 +207,10 @@ __global__ void __launch_bounds__(kThreads, kStatsCtas) verify_stats_kernel(cons
 
 // -------------------------------------------------------------- exact draw
 
+struct Place {  // what one place's parts say
+  float top, z;
+};
+
 // 2^(i / 32) in units of 2^-30.
 __constant__ uint32_t kRoots[32] = {
     1073741824u, 1097253708u, 1121280436u, 1145833280u, 1170923762u, 1196563654u, 1222764986u, 1249540052u,
@@ -217,27 +218,42 @@ __constant__ uint32_t kRoots[32] = {
     1518500250u, 1551751076u, 1585730000u, 1620452965u, 1655936265u, 1692196547u, 1729250827u, 1767116489u,
     1805811301u, 1845353420u, 1885761398u, 1927054196u, 1969251188u, 2012372174u, 2056437387u, 2101467502u};
 
-// 2^((x - top) rate) for the scores of a row, each as a whole number of 31 bits
-// and a shift: right to 2^-30 of itself (the polynomial's and the argument's last
-// roundings, 2^-31 each, the table's and the product's, 2^-31 and 2^-30 of it). At
-// `one`, the weight 1 is 2^(30 + one): a sum of weights is set to stay below 2^64.
+// 2^((x - top) rate) for the scores of a row, each as a whole number of 31 bits and a
+// shift, times a factor near 1 that all of them have. x rate, exact in a fused
+// multiplication, is split into whole 32nds (1.5 * 2^18 rounds to them, and
+// leaves their number in the low bits) and a rest of at most 2^-6: no difference
+// x - top is formed, whose rounding would have to be followed. Where top * rate
+// passes 2^16 it is, and exact: scores that have any weight are within 2^-8 of top then.
+// A weight is right to 2^-29 of itself: 2^-31 each for the rest's two roundings,
+// the polynomial's last one and the table's, 2^-30 for the product with it.
+// At `one`, the weight 1 is 2^(30 + one): a sum of weights is set to stay below 2^64.
+// The 32 roots are a warp's own in shared memory (as a register of each lane they
+// would cost a shuffle, and a convergence check, a weight).
 struct Weights {
-  float top;
-  u64 ntop2, rate2, nrate2, lo2;
-  uint32_t factor;        // of a share, in 2^-31, with `one` less its shift
+  u64 nbase2, rate2, lo2, round2;
+  uint32_t roots;  // in shared memory, on 128 bytes: in 2^-30
   int one;
-  const uint32_t* roots;  // in shared memory
 
-  __device__ __forceinline__ void set(float t, float rate_hi, float rate_lo, const uint32_t* table) {
-    top = t == INFINITY ? 0.0f : t;
-    ntop2 = pack2(-top, -top);
+  static constexpr float kRound = 393216.0f, kNone = kRound - 200.0f;  // no weight below that
+
+  __device__ __forceinline__ void set(const Place& place, float rate_hi, float rate_lo, uint32_t* table, int lane) {
+    const float top = place.top == INFINITY ? 0.0f : place.top;
+    const float whole = fabsf(__fmul_rn(top, rate_hi)) < 65536.0f ? __fsub_rn(__fmaf_rn(top, rate_hi, kRound), kRound) : 0.0f;
+    const float base = fabsf(__fmul_rn(top, rate_hi)) < 65536.0f ? 0.0f : top;
+    nbase2 = pack2(-base, -base);
     rate2 = pack2(rate_hi, rate_hi);
-    nrate2 = pack2(-rate_hi, -rate_hi);
     lo2 = pack2(rate_lo, rate_lo);
-    roots = table;
+    round2 = pack2(kRound - whole, kRound - whole);
+    __syncwarp();
+    table[lane] = kRoots[lane];
+    __syncwarp();
+    roots = smem_addr(table);
+    // An fp32 sum bounds the exact one: 2^31 times that, and a bit to spare, stays below 2^64.
+    one = 31 - (static_cast<int>(__float_as_uint(place.z * 1.02f) >> 23) - 127);
   }
   // Every weight divided by `all`, a sum of them at the present `one`: shares of 2^62.
-  __device__ __forceinline__ void divide(u64 all) {
+  __device__ __forceinline__ void divide(u64 all, uint32_t* table, int lane) {
+    const uint32_t root = table[lane];
     const int up = __clzll(static_cast<long long>(all));
     const uint32_t head = static_cast<uint32_t>((all << up) >> 32);  // its first 32 bits
     // 2^63 / head = 2^(95 - up) / all, in 2^31 .. 2^32: by fp32's reciprocal, and
@@ -246,58 +262,49 @@ struct Weights {
     const u64 near = static_cast<u64>(inv * 0x1p63f);
     const long long rest = static_cast<long long>((u64(1) << 63) - near * head);
     const u64 f = near + static_cast<u64>(static_cast<long long>(rintf(static_cast<float>(rest) * inv)));
-    factor = f > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(f);
+    const uint32_t factor = f > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(f);
     one += up - 2;  // m f / 2^31 = m 2^(64 - up) / all; a share of 2^62 is m 2^(62 + one) / all
+    // Of the factor, 1 .. 2 in 2^-31, whole 32nds of an octave go with the
+    // scores' and what is left, below 2^(1/32), into the roots: those stay below 2^31.
+    const int i0 = __popc(__ballot_sync(kFullMask, root <= factor >> 1)) - 1;
+    const u64 less = static_cast<u64>(factor) * __shfl_sync(kFullMask, root, (32 - i0) & 31);
+    const u64 scaled = (static_cast<u64>(root) * (less >> (i0 ? 31 : 30)) + (u64(1) << 30)) >> 31;
+    __syncwarp();
+    table[lane] = static_cast<uint32_t>(scaled < 0x7FFFFFFFull ? scaled : 0x7FFFFFFFull);
+    __syncwarp();
+    const float round = __fadd_rn(low2(round2), static_cast<float>(i0) * 0.03125f);
+    round2 = pack2(round, round);
   }
   // Of two scores (with a largest score of +infinity: shifted): their weights, or their shares of the sum.
-  template <bool SHARES>
   __device__ __forceinline__ void of2(float x0, float x1, u64& w0, u64& w1) const {
-    const u64 x = pack2(x0, x1), m1 = pack2(-1.0f, -1.0f);
-    // x - top as the sum of two numbers, and its product with the rate.
-    const u64 d = add2(x, ntop2);
-    const u64 back = fma2(x, m1, d);  // -top, as far as d has it
-    const u64 lost = fma2(fma2(ntop2, m1, back), m1, fma2(fma2(back, m1, d), m1, x));
-    const u64 far = mul2(d, rate2);
-    const u64 hi = pack2(fmaxf(low2(far), -200.0f), fmaxf(high2(far), -200.0f));  // no weight; -infinity among them
-    const u64 lo = fma2(lost, rate2, fma2(d, lo2, fma2(d, rate2, mul2(d, nrate2))));  // any number there
-    // Whole 32nds (1.5 * 2^23 rounds, and leaves them in the low bits) and a rest.
-    const u64 n = fma2(hi, pack2(32.0f, 32.0f), pack2(12582912.0f, 12582912.0f));
-    const u64 whole = add2(n, pack2(-12582912.0f, -12582912.0f));
-    const u64 f = add2(fma2(whole, pack2(-1.0f / 32.0f, -1.0f / 32.0f), hi), lo);
+    const u64 x = add2(pack2(x0, x1), nbase2);
+    const u64 near = fma2(x, rate2, round2);
+    const u64 n = pack2(fmaxf(low2(near), kNone), fmaxf(high2(near), kNone));  // -infinity among them
+    const u64 f = fma2(x, lo2, fma2(x, rate2, fma2(n, pack2(-1.0f, -1.0f), round2)));  // any number where there is no weight
     // 2^32 (2^f - 1), |f| < 2^-5: the series of exp(f ln 2).
     constexpr float c1 = 0x1p32f * 6.9314718e-1f, c2 = 0x1p32f * 2.4022651e-1f, c3 = 0x1p32f * 5.5504109e-2f, c4 = 0x1p32f * 9.6181291e-3f;
     u64 g = fma2(f, pack2(c4, c4), pack2(c3, c3));
     g = fma2(f, g, pack2(c2, c2));
     g = fma2(f, g, pack2(c1, c1));
     g = mul2(f, g);
-    w0 = place<SHARES>(low2(n), low2(g));
-    w1 = place<SHARES>(high2(n), high2(g));
+    w0 = place(low2(n), low2(g));
+    w1 = place(high2(n), high2(g));
   }
 
  private:
-  template <bool SHARES>
   __device__ __forceinline__ u64 place(float n, float g) const {
-    const uint32_t e = __float_as_uint(n);  // 0x4B400000 and the 32nds
-    const int root = static_cast<int>(roots[e & 31u]);
-    uint32_t m = static_cast<uint32_t>(root + __mulhi(root, __float2int_rn(g)));
-    if (SHARES) m = __umulhi(m << 1, factor);
+    const uint32_t e = __float_as_uint(n);  // kRound's and the 32nds
+    uint32_t r, m;  // e % 32's
+    asm("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(roots | (e << 2 & 124u)) : "memory");
+    asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(m) : "r"(r), "r"(__float2int_rn(g)));
     u64 w;  // m 2^(one + e / 32), nothing left of it past 64
-    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(m) << 32), "r"(32 + (0x4B400000 >> 5) - one - static_cast<int>(e >> 5)));
+    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(m) << 32), "r"(32 + (0x48C00000 >> 5) - one - static_cast<int>(e >> 5)));
     return w;
   }
 };
 
-// Scores i0 .. i0 + kLen - 1 of a row of n that starts anywhere, -infinity where
-// there are none: from the two aligned vectors that hold them.
-template <typename T>
-__device__ __forceinline__ uint4 load_shifted(const T* row, int i0, int n) {
-  constexpr int E = Vec<T>::kLen;
-  if (i0 < E || i0 + 2 * E > n) return load_edge(row, i0, n);
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row + i0);
-  const uint4* src = reinterpret_cast<const uint4*>(at & ~uintptr_t(15));
-  const uint4 a = src[0];
-  if ((at & 15) == 0) return a;
-  const uint4 b = src[1];
+// Sixteen bytes from byte `at` on of two vectors.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int at) {
   uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   if (at & 8) {
 #pragma unroll
@@ -307,24 +314,20 @@ __device__ __forceinline__ uint4 load_shifted(const T* row, int i0, int n) {
 #pragma unroll
     for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
   }
-  const int bits = static_cast<int>(at & 3) * 8;
+  const int bits = (at & 3) * 8;
   return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
                     __funnelshift_r(w[3], w[4], bits));
 }
-
-struct Place {  // what one place's parts say
-  float top, z;
-};
 
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw_kernel(const VerifyLaunch a, const VerifyPart* parts, int splits, int cluster_bits) {
   constexpr int kWarps = kThreads / 32;
   constexpr int E = Vec<T>::kLen;
-  __shared__ uint32_t roots[32];
   __shared__ u64 slot[4][kMaxCluster];  // a word per CTA, written by all of them
   __shared__ u64 kept[kWarps], kept_too[kWarps];
   __shared__ int first_no;
   __shared__ Place row_p, row_q;
+  __shared__ __align__(128) uint32_t tables[kWarps][2][32];
 
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -340,18 +343,44 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   };
   const float rate = rate_of(a, seq);
   const int count = count_of(a, seq);
-  if (threadIdx.x < 32) roots[threadIdx.x] = kRoots[threadIdx.x];
   if (threadIdx.x == 0) first_no = count;
-  cluster_meets();  // a CTA's shared memory may be written by others now
+  if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // What a place needs and no kernel before this one writes: on its way ahead of the
+  // wait for the sums. A token's score: a NaN counts as -infinity.
+  auto score = [&](const T* row, int x) {
+    const float v = Vec<T>::one(row[x]);
+    return v == v ? v : -INFINITY;
+  };
+  struct Drafted {
+    int x = -1;
+    float u = 0.0f, xp = -INFINITY, xq = -INFINITY;
+  };
+  auto look = [&](int i) {
+    Drafted d;
+    if (i >= count) return d;
+    d.x = a.draft_token[seq * a.drafts + i];
+    d.u = a.u[seq * places + i];
+    if (d.x >= 0 && d.x < a.vocab) {
+      d.xp = score(target_row<T>(a, seq, i), d.x);
+      d.xq = a.draft ? score(draft_row<T>(a, seq, i), d.x) : 0.0f;
+    }
+    return d;
+  };
+  const int first_place = static_cast<int>(rank) * kWarps + warp;
+  Drafted drafted = look(first_place);
   pdl_wait();
+  if (size > 1)  // a CTA's shared memory may be written by others now
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
 
   // The sums of a row, from its parts (every lane of a warp).
   auto join = [&](int row) {
     Sum s;
     const VerifyPart* from = parts + (seq * rows + row) * splits;
     for (int i = lane; i < splits; i += 32) s.join(__ldcg(&from[i].top), __ldcg(&from[i].z), rate);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s.join(__shfl_xor_sync(kFullMask, s.top, d), __shfl_xor_sync(kFullMask, s.z, d), rate);
+#pragma unroll 1
+    for (int d = 1; d < min(splits, 32); d <<= 1) s.join(__shfl_xor_sync(kFullMask, s.top, d), __shfl_xor_sync(kFullMask, s.z, d), rate);
     return Place{__shfl_sync(kFullMask, s.top, 0), __shfl_sync(kFullMask, s.z, 0)};
   };
   auto best_of = [&](int row) {  // its index, -1 where nothing is left
@@ -361,27 +390,19 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
     k = warp_max(k);
     return k ? static_cast<int>(key_index(k)) : -1;
   };
-  // A token's score; a NaN counts as -infinity.
-  auto score = [&](const T* row, int x) {
-    const float v = Vec<T>::one(row[x]);
-    return v == v ? v : -INFINITY;
-  };
   auto log_p = [&](float x, const Place& p) { return __fsub_rn(less_top(x, p.top) * (rate * 0.69314718f), logf(p.z)); };
 
   int32_t* token = a.token + seq * places;
   float* logprob = a.logprob ? a.logprob + seq * places : nullptr;
-  // A place a warp of the cluster; all that it needs is read at once.
-  for (int i = static_cast<int>(rank) * kWarps + warp; i < count; i += kWarps << cluster_bits) {
-    const int x = a.draft_token[seq * a.drafts + i];
-    const float u = a.u[seq * places + i];
-    const bool inside = x >= 0 && x < a.vocab;
+  // A place a warp of the cluster.
+  for (int i = first_place; i < count; i += kWarps << cluster_bits) {
+    const int x = drafted.x;
+    const float u = drafted.u, xp = drafted.xp, xq = drafted.xq;
     bool ok;
     float lp = 0.0f;
     if (rate == 0.0f) {
-      ok = inside && best_of(i) == x;
+      ok = x >= 0 && best_of(i) == x;
     } else {
-      const float xp = inside ? score(target_row<T>(a, seq, i), x) : -INFINITY;
-      const float xq = inside && a.draft ? score(draft_row<T>(a, seq, i), x) : 0.0f;
       const Place p = join(i), q = a.draft ? join(places + i) : Place{0.0f, 1.0f};
       ok = xp > -INFINITY;
       lp = log_p(xp, p);
@@ -403,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
       token[i] = x;
       if (logprob) logprob[i] = lp;
     }
+    drafted = look(i + (kWarps << cluster_bits));
   }
   cluster_meets();
   const int accepted = first_no;
@@ -439,13 +461,35 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   const int out = late && !a.draft ? a.draft_token[seq * a.drafts + accepted] : -1;
 
   const Row<T> rp(target_row<T>(a, seq, accepted), a.vocab);
-  // The draft's row may lie otherwise on its 16-byte boundaries: it is taken by
-  // the target's vectors.
-  const T* dq = with_q ? draft_row<T>(a, seq, accepted) : nullptr;
-  auto load_q = [&](int v) { return vec_max<T>(load_shifted(dq, v * E - rp.lead, a.vocab), vec_none<T>()); };
   const int c0 = static_cast<int>(int64_t(rp.vecs) * rank >> cluster_bits), c1 = static_cast<int>(int64_t(rp.vecs) * (rank + 1) >> cluster_bits);
   auto part_of = [](int lo, int hi, int w) { return lo + static_cast<int>(int64_t(hi - lo) * w / kWarps); };
   const int v0 = part_of(c0, c1, warp), v1 = part_of(c0, c1, warp + 1);
+  // The draft's row may lie otherwise on its 16-byte boundaries: a vector of the
+  // target's scores has its draft's in vectors v - behind and the one after that.
+  const Row<T> rq(with_q ? draft_row<T>(a, seq, accepted) : target_row<T>(a, seq, accepted), a.vocab);
+  const int behind = rq.lead < rp.lead ? 1 : 0, shift = (rq.lead - rp.lead + behind * E) * static_cast<int>(sizeof(T));
+  // A lane's vectors of a round as they are in memory: nothing waits for them before the round is due.
+  const int fp0 = rp.lead > 0 ? 1 : 0, fp1 = (rp.n + rp.lead) / E, fq0 = rq.lead > 0 ? 1 : 0, fq1 = (rq.n + rq.lead) / E;
+  const uint4* src_p = reinterpret_cast<const uint4*>(rp.p - rp.lead);
+  const uint4* src_q = reinterpret_cast<const uint4*>(rq.p - rq.lead);
+  struct Round {
+    uint4 p, q, q_next;
+  };
+  auto load_q = [&](int w) { return w >= fq0 && w < fq1 ? src_q[w] : load_edge(rq.p, w * E - rq.lead, rq.n); };
+  auto fetch = [&](int v, bool both, Round& r) {
+    if (v >= v1) return;
+    r.p = v >= fp0 && v < fp1 ? src_p[v] : load_edge(rp.p, v * E - rp.lead, rp.n);
+    if (both) {
+      r.q = load_q(v - behind);
+      if (shift > 0) r.q_next = load_q(v - behind + 1);
+    }
+  };
+  // What they hold, none past this warp's part; a NaN becomes -infinity.
+  auto take = [&](int v, bool both, const Round& r, uint4& vp, uint4& vq) {
+    vp = v < v1 ? vec_max<T>(r.p, vec_none<T>()) : vec_none<T>();
+    vq = vec_none<T>();
+    if (both && v < v1) vq = vec_max<T>(shift > 0 ? shifted(r.q, r.q_next, shift) : r.q, vec_none<T>());
+  };
   int turn = 0;
   // Sum over the cluster of every thread's v (and w); slot[turn - 1] keeps the CTAs' own.
   auto total_of = [&](u64 v, u64* w) {
@@ -483,28 +527,21 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
       for (int e = 0; e < E; ++e) x[e] = x[e] == INFINITY ? 0.0f : -INFINITY;
     }
   };
-  auto load_p = [&](int v) { return rp.load(v); };
   const Place qq = row_q;
   Weights wp, wq;
-  // An fp32 sum bounds the exact one: 2^31 times that, and a bit to spare, stays below 2^64.
-  auto set = [&](Weights& w, const Place& place) {
-    w.set(place.top, rate, rate_lo, roots);
-    w.one = 31 - (static_cast<int>(__float_as_uint(place.z * 1.001f) >> 23) - 127);
-  };
-  set(wp, pp);
-  if (with_q) set(wq, qq);
-  // body(v, p's vector, q's vector) for this warp's part, a vector a lane, the next ones on their way.
+  wp.set(pp, rate, rate_lo, tables[warp][0], lane);
+  if (with_q) wq.set(qq, rate, rate_lo, tables[warp][1], lane);
+  // body(v, p's vector, q's vector) for this warp's part, a vector a lane (none past
+  // the end: the whole warp takes part).
   auto each = [&](bool both, auto&& body) {
-    int v = v0 + lane;
-    uint4 np = v < v1 ? load_p(v) : vec_none<T>(), nq = both && v < v1 ? load_q(v) : vec_none<T>();
+    Round next{};
+    fetch(v0 + lane, both, next);
 #pragma unroll 1
-    for (; v < v1; v += 32) {
-      const uint4 rp4 = np, rq4 = nq;
-      if (v + 32 < v1) {
-        np = load_p(v + 32);
-        if (both) nq = load_q(v + 32);
-      }
-      body(v, rp4, rq4);
+    for (int v = v0 + lane; v - lane < v1; v += 32) {
+      uint4 vp, vq;
+      take(v, both, next, vp, vq);
+      fetch(v + 32, both, next);
+      body(v, vp, vq);
     }
   };
   // With a draft's row: both rows' sums, and then shares of 2^62, whose differences are what is left.
@@ -517,32 +554,27 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         u64 a0, a1;
-        wp.of2<false>(x[e], x[e + 1], a0, a1);
+        wp.of2(x[e], x[e + 1], a0, a1);
         sum_p += a0 + a1;
-        wq.of2<false>(y[e], y[e + 1], a0, a1);
+        wq.of2(y[e], y[e + 1], a0, a1);
         sum_q += a0 + a1;
       }
     });
-    wp.divide(total_of(sum_p, &sum_q));
-    wq.divide(sum_q);
+    wp.divide(total_of(sum_p, &sum_q), tables[warp][0], lane);
+    wq.divide(sum_q, tables[warp][1], lane);
   }
   bool left = with_q || out >= 0;
   auto weigh = [&](int v, const uint4& vp, const uint4& vq, u64 (&w)[E]) {
     float x[E];
     scores(vp, pp.top, x);
-    if (!with_q) {
 #pragma unroll
-      for (int e = 0; e < E; e += 2) wp.of2<false>(x[e], x[e + 1], w[e], w[e + 1]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; e += 2) wp.of2<true>(x[e], x[e + 1], w[e], w[e + 1]);
-    }
+    for (int e = 0; e < E; e += 2) wp.of2(x[e], x[e + 1], w[e], w[e + 1]);
     if (left && with_q) {
       scores(vq, qq.top, x);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         u64 q[2];
-        wq.of2<true>(x[e], x[e + 1], q[0], q[1]);
+        wq.of2(x[e], x[e + 1], q[0], q[1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) w[e + i] = w[e + i] > q[i] ? w[e + i] - q[i] : 0;
       }
@@ -552,15 +584,29 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
         if (v * E - rp.lead + e == out) w[e] = 0;
     }
   };
+  // A warp's part as 32 stretches, of which each lane keeps one's sum: the draw goes through one of them again.
+  const int stretch = max(1, (v1 - v0 + 1023) / 1024);  // rounds of 32 vectors
+  u64 of_stretch = 0;
   auto sum_left = [&]() {
     u64 sum = 0;
+    int rounds = 0, who = 0;
+    of_stretch = 0;
+    auto close = [&]() {
+      const u64 all = warp_sum(sum);
+      if (lane == who) of_stretch = all;
+      ++who;
+      sum = 0;
+      rounds = 0;
+    };
     each(left && with_q, [&](int v, const uint4& vp, const uint4& vq) {
       u64 w[E];
       weigh(v, vp, vq, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum += w[e];
+      if (++rounds == stretch) close();
     });
-    return total_of(sum, nullptr);
+    if (rounds > 0) close();
+    return total_of(of_stretch, nullptr);
   };
   u64 total = sum_left();
   if (left && total == 0) {  // p and q agree (or p is all on the refused token): what is left is rounding
@@ -575,13 +621,19 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   // This CTA's warps, in order.
   for (int w = 0; w < warp; ++w) before += kept[w];
   if (aim < before || aim >= before + kept[warp]) return;
-  for (int v = v0; v < v1; v += 32) {
+  const u64 to_here = before + warp_scan(of_stretch, lane);
+  const int which = __ffs(__ballot_sync(kFullMask, aim < to_here)) - 1;
+  before = __shfl_sync(kFullMask, to_here - of_stretch, which);
+#pragma unroll 1
+  for (int v = v0 + which * stretch * 32; v < v1; v += 32) {
+    Round here{};
+    fetch(v + lane, left && with_q, here);
+    uint4 vp, vq;
+    take(v + lane, left && with_q, here, vp, vq);
     u64 w[E], sum = 0;
-    if (v + lane < v1) {
-      weigh(v + lane, load_p(v + lane), left && with_q ? load_q(v + lane) : vec_none<T>(), w);
+    weigh(v + lane, vp, vq, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += w[e];
-    }
+    for (int e = 0; e < E; ++e) sum += w[e];
     const u64 upto = before + warp_scan(sum, lane);
     u64 run = upto - sum;
     if (sum > 0 && run <= aim && aim < upto) {
@@ -600,6 +652,13 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   }
 }
 
+// A row's vectors, wherever it starts, and those of one of its parts: as many for each thread.
+int vecs_of(const VerifyLaunch& a) { return static_cast<int>(a.vocab * static_cast<int64_t>(dtype_bytes(a.dtype)) / 16) + 2; }
+int part_vecs_of(int vecs, int splits) {
+  const int p = (vecs + splits - 1) / splits;
+  return (p + kThreads - 1) / kThreads * kThreads;
+}
+
 template <typename T, int kThreads>
 cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int splits, int num_sms, cudaStream_t st) {
   auto fn = verify_draw_kernel<T, kThreads>;
@@ -607,7 +666,7 @@ cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int sp
   const cudaError_t ready = once.run([fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
   if (ready != cudaSuccess) return ready;
   // As many CTAs a row as run at once, of a vector a thread at least.
-  const int64_t vecs = a.vocab * static_cast<int64_t>(sizeof(T)) / 16 + 2;
+  const int64_t vecs = vecs_of(a);
   int bits = 0;
   while (1 << bits < kMaxCluster && a.seqs << (bits + 1) <= int64_t(num_sms) * (kDrawThreads / kThreads) && vecs >> bits > kThreads) ++bits;
   const int cluster = 1 << bits;
@@ -637,14 +696,16 @@ cudaError_t launch_draw(const VerifyLaunch& a, const VerifyPart* parts, int spli
 
 // CTAs a row, of 8 KB at least, as many as the workspace has room for: the number
 // whose rounds of CTAs read the least, a CTA's own instructions counted as 16 KB.
+// 960 rows of 128000 bf16 scores: 43 us as 4 parts each, which this chooses, 52 whole,
+// 46 as 3, 44 as 8, 52 as 12, 66 as 24; 671 of 100003: 28 as 4, 54 whole, 26 as 6 to 16, 33 as 24.
 int splits_of(const VerifyLaunch& a, int64_t max_parts, int num_sms) {
-  const int64_t rows = a.seqs * (a.drafts + 1 + (a.draft ? a.drafts : 0));
-  const int64_t bytes = a.vocab * static_cast<int64_t>(dtype_bytes(a.dtype)), places = int64_t(num_sms) * kStatsCtas;
-  const int64_t most = std::min<int64_t>(std::min<int64_t>(kMaxSplits, max_parts / rows), bytes / 8192);
+  const int64_t rows = a.seqs * (a.drafts + 1 + (a.draft ? a.drafts : 0)), places = int64_t(num_sms) * kStatsCtas;
+  const int vecs = vecs_of(a);
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(kMaxSplits, max_parts / rows), vecs / 512);
   int64_t best = 1, least = INT64_MAX;
   for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
-    const int64_t cost = (rows * s + places - 1) / places * (bytes / s + 16384);
-    if (cost < least) {
+    const int64_t cost = (rows * s + places - 1) / places * (part_vecs_of(vecs, static_cast<int>(s)) * int64_t(16) + 16384);
+    if (cost <= least) {
       least = cost;
       best = s;
     }
@@ -655,9 +716,8 @@ int splits_of(const VerifyLaunch& a, int64_t max_parts, int num_sms) {
 template <typename T>
 cudaError_t launch_stats(const VerifyLaunch& a, VerifyPart* parts, int splits, cudaStream_t st) {
   const unsigned rows = static_cast<unsigned>(a.drafts + 1 + (a.draft ? a.drafts : 0));
-  const int vecs = static_cast<int>(a.vocab * static_cast<int64_t>(sizeof(T)) / 16) + 2;  // wherever a row starts
   verify_stats_kernel<T><<<dim3(static_cast<unsigned>(a.seqs), rows, static_cast<unsigned>(splits)), kThreads, 0, st>>>(
-      a, parts, (vecs + splits - 1) / splits);
+      a, parts, part_vecs_of(vecs_of(a), splits));
   return cudaGetLastError();
 }
 

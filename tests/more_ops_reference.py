@@ -89,7 +89,7 @@ def shares(x, temperature):
 # Of a probability ratio: sums of weights that are off by 2^-22 (the exponential) and by 2^-24 for each of |z| (its
 # argument) with |z| below 60 where it matters.
 RATIO_ERROR = 2.0 ** -20
-# Of a draw's running sum, in shares of p's whole: each probability is held to 2^-30, and p - q has two of them.
+# Of a draw's running sum, in shares of p's whole: each probability is held to 2^-29, and p - q has two of them.
 DRAW_ERROR = 2.0 ** -28
 
 
