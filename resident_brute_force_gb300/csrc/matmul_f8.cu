@@ -15,15 +15,23 @@
 //   warp 0      loads its channels and its tokens of a stage (TMA, 128-byte swizzle);
 //   warp 1      one thread of the even CTA issues the pair's MMAs, each stage's into
 //               the next of kAcc accumulators;
-//   warps 4-11  read an accumulator (32 channels and half of the tokens each) and add
-//               it, times its scales, to their running sums, two numbers an
-//               instruction; at a tile's end they add the bias, round and store;
-//   warp 2      puts the scales of four blocks at a time into shared memory (with one
-//               scale for 128 channels: the products of both).
+//   warps 2, 3  put the scales of four blocks at a time into shared memory (with one
+//               scale for 128 channels: the products of both);
+//   warps 4 on  (sixteen from 128 tokens on, else eight) read an accumulator, 32
+//               channels and a part of the tokens each, and add it, times its
+//               scales, to their running sums, two numbers an instruction; at a
+//               tile's end they add the bias, round and store.
 // Work is dealt out in tiles, or, where there are few tiles per pair, in equal
 // shares of all stages: a tile that several pairs share is summed from their
 // partial sums, in the pairs' order, by the one that finishes last. No CTA waits
 // for another pair.
+//
+// What bounds it. Few tokens: HBM, which b passes through once (1 x 1M x 768 at 6.7
+// TB/s). Many: a stage of 256 tokens is 512 clocks of MMAs at the nominal rate, in which
+// each of 16 warps reads 64 columns of sums and adds them; 4096 x 8192 x 4096 runs at 2.0 PFLOP/s,
+// 137 us, of which 111 to 117 without the FMAs and 99 without the reads too, at the
+// power limit by then. Tried there without gain: two accumulators of 128 tokens (135),
+// tiles of 128 tokens (164), eight warps of 128 sums, suspending waits (208).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -48,7 +56,9 @@ constexpr int kFirstWorker = 4;  // from the second warpgroup on
 constexpr int kScaleBlocks = 4;  // blocks whose scales are in a slot
 constexpr int kScaleSlots = 2;
 constexpr int kMaxSmem = 227 * 1024;
-// Stages' time that an exchange of partial sums takes.
+// Stages' time that an exchange of partial sums takes. With it, and never / always
+// sharing, in us: 1 x 4096 x 4096 11.1 / 12.3, 1 x 8192 x 8192 16.4 / 21.0, 128 x 1024 x 8192
+// 18.6 / 25.9 (it shares); 100 x 8192 x 4096 15.7, 17.8 shared, 256 x 4096 x 4096 14.6, 16.9 shared (it does not).
 template <int NT>
 constexpr int kSplitCost = NT <= 64 ? 20 : 32;
 
@@ -686,6 +696,9 @@ cudaError_t launch_matmul_f8(const MatmulF8Launch& a, const MatmulF8Workspace& w
   if (a.m <= 32) return launch_out<32>(a, w, st);
   if (a.m <= 64) return launch_out<64>(a, w, st);
   if (a.m <= 128) return launch_out<128>(a, w, st);
+  // A round of tiles of 256 tokens takes 7/4 of one of 128 (it has twice the MMAs, and
+  // the scales and its start once). In us, as 128 / 256: 256 x 8192 x 4096 16.0 / 25.6,
+  // 1000 x 8192 x 4096 50.0 / 47.5, 384 x 8192 x 4096 25.4 / 22.7, 700 x 4096 x 4096 25.5 / 22.5, 2048 x 8192 x 4096 78 / 78.
   const int64_t pairs = w.num_sms / 2, channels = (a.n + kPairChannels - 1) / kPairChannels;
   const int64_t rounds_128 = ((a.m + 127) / 128 * channels + pairs - 1) / pairs;
   const int64_t rounds_256 = ((a.m + 255) / 256 * channels + pairs - 1) / pairs;

@@ -9,8 +9,10 @@
 //
 // One pass: a block is held in registers between its maximum and its rounding.
 // Blocks of a row: 16 lanes (fp32: 32) a block, 16 bytes a lane, four blocks a
-// lane under way, and no division but the scales'. Blocks of 128 x 128: a CTA each, 32 KB (fp32: 64) in its
-// threads' registers. What bounds it: HBM.
+// lane under way, and no division but the scales'. Blocks of 128 x 128: a CTA each,
+// 32 KB (fp32: 64) in its threads' registers.
+// What bounds it: HBM. 8192 x 8192 bf16: 40.5 us by rows, 38.5 by blocks (30 for the
+// bytes at the copy rate); fp32 4096 x 8192 33.8 and 29.8 (25).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -87,6 +87,17 @@ def test_counts_temperatures_and_masks(ops):
     check(ops, c)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("base,heat", [(3e4, 0.7), (-3e4, 0.7), (45000.0, 1.0), (46000.0, 1.0), (-46000.0, 1.0), (1e6, 1.0), (3.0, 1e-5), (-1e30, 1e25),
+                                       (0.0, 1e-20), (0.0, 1e20), (0.0, 1e-36)])
+def test_scores_far_from_zero(ops, dtype, base, heat):
+    """Largest scores over T on either side of 2^16, where weights are taken without a difference of scores and with one."""
+    c = case(9, 3, 1003, seed=int(abs(base)) % 97)
+    c["target"], c["draft"] = ((base + heat * c[k].double()).to(dtype) for k in ("target", "draft"))
+    c["temperature"] = torch.full((9,), heat)
+    check(ops, c)
+
+
 def test_what_is_not_needed_is_not_looked_at(ops):
     """Places behind a sequence's drafted tokens hold anything, and so do the draft's scores of a greedy one."""
     c = case(6, 4, 500, seed=5)
