@@ -22,12 +22,11 @@
 // table of 31-bit integers) and a rest of at most 2^-6 (a polynomial, as a 32-bit fraction).
 //
 // What bounds it: of 64 sequences of 7 tokens over 128000 bf16 scores the rows' sums take
-// 43 us (246 MB, 36 at the copy rate), the draws 57: some 5 for the accepted tokens,
-// about 20 for either pass over the drawn rows (18 instructions a weight, 4 weights an index,
-// and as much again around them, at half of the issue slots), 3 for the index itself. Without
-// the weights the same passes take 33 in all. Tried without gain: the rows kept in shared
-// memory between the passes, or copied there ahead (cp.async), four scores at a time,
-// the roots by shuffles, 128 registers a thread.
+// 43 us (246 MB, 36 at the copy rate), the draws 45: some 5 for the accepted tokens,
+// about 18 for either pass over the drawn rows (18 instructions a weight, 4 weights an index,
+// and as much again around them), 3 for the index itself. Tried without gain: the rows
+// kept in shared memory between the passes, or copied there ahead (cp.async), vectors
+// fetched two rounds ahead, four scores at a time, the roots by shuffles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -49,7 +48,11 @@ constexpr int kGroupVecs = 4 * kThreads;  // vectors that a CTA of the rows' sum
 constexpr int kStatsCtas = 6;  // an SM, in the rows' sums: 40 registers a thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);  // what fp32 leaves out
-constexpr int kDrawThreads = 1024;  // an SM, in the draw: 64 registers each
+// Of the draw, an SM: 512 threads, so that one has 128 registers for weights side by
+// side. 64 x 7 x 128000 and 61 x 5 x 100003 in all: 90 and 65 us, with 640 threads 102 and 70, with 1024
+// 107 and 69 (as CTAs of 256 99 and 72), with 256 104 and 75; CTAs of 256 and 512 threads 92 and 68, 89 and 67.
+constexpr int kDrawThreads = 512;
+constexpr int kDrawCta = 128;
 
 // log2(e) / T as a finite number above 0 (sample_dev's); 0 where the best index is asked for.
 __device__ __forceinline__ float rate_of(const VerifyLaunch& a, int64_t seq) {
@@ -326,9 +329,9 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int at)
                     __funnelshift_r(w[3], w[4], bits));
 }
 
-template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw_kernel(const VerifyLaunch a, const VerifyPart* parts, int splits, int cluster_bits) {
-  constexpr int kWarps = kThreads / 32;
+template <typename T>
+__global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw_kernel(const VerifyLaunch a, const VerifyPart* parts, int splits, int cluster_bits) {
+  constexpr int kWarps = kDrawCta / 32;
   constexpr int E = Vec<T>::kLen;
   __shared__ u64 slot[4][kMaxCluster];  // a word per CTA, written by all of them
   __shared__ u64 kept[kWarps], kept_too[kWarps];
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, kDrawThreads / kThreads) verify_draw
   const bool late = accepted < count;  // a token was refused
   if (rank == 0) {
     if (threadIdx.x == 0) a.accepted[seq] = accepted;
-    for (int i = accepted + static_cast<int>(threadIdx.x); i < places; i += kThreads) {
+    for (int i = accepted + static_cast<int>(threadIdx.x); i < places; i += kDrawCta) {
       token[i] = -1;
       if (logprob) logprob[i] = -INFINITY;
     }
@@ -666,20 +669,20 @@ int part_vecs_of(int vecs, int splits) {
   return (p + kThreads - 1) / kThreads * kThreads;
 }
 
-template <typename T, int kThreads>
-cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int splits, int num_sms, cudaStream_t st) {
-  auto fn = verify_draw_kernel<T, kThreads>;
+template <typename T>
+cudaError_t launch_draw(const VerifyLaunch& a, const VerifyPart* parts, int splits, int num_sms, cudaStream_t st) {
+  auto fn = verify_draw_kernel<T>;
   static PerDeviceOnce once;
   const cudaError_t ready = once.run([fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
   if (ready != cudaSuccess) return ready;
   // As many CTAs a row as run at once, of a vector a thread at least.
   const int64_t vecs = vecs_of(a);
   int bits = 0;
-  while (1 << bits < kMaxCluster && a.seqs << (bits + 1) <= int64_t(num_sms) * (kDrawThreads / kThreads) && vecs >> bits > kThreads) ++bits;
+  while (1 << bits < kMaxCluster && a.seqs << (bits + 1) <= int64_t(num_sms) * (kDrawThreads / kDrawCta) && vecs >> bits > kDrawCta) ++bits;
   const int cluster = 1 << bits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.seqs * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kDrawCta);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -691,14 +694,6 @@ cudaError_t launch_draw_t(const VerifyLaunch& a, const VerifyPart* parts, int sp
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fn, a, parts, splits, bits);
-}
-
-// Sixteen CTAs a row of 256 threads where that many run at once, else of 128: smaller
-// ones fill the SMs more evenly, and rows differ in what there is to do.
-template <typename T>
-cudaError_t launch_draw(const VerifyLaunch& a, const VerifyPart* parts, int splits, int num_sms, cudaStream_t st) {
-  return a.seqs * kMaxCluster <= int64_t(num_sms) * (kDrawThreads / 256) ? launch_draw_t<T, 256>(a, parts, splits, num_sms, st)
-                                                                       : launch_draw_t<T, 128>(a, parts, splits, num_sms, st);
 }
 
 // CTAs a row, of 8 KB at least, as many as the workspace has room for: the number
