@@ -10,10 +10,10 @@
 //    score and the sum of 2^((x - max) log2(e) / T), in fp32, of a part of the row
 //    a CTA. (Not above 0, T asks for the best index: then the first one at the
 //    largest score, of the target's rows alone.)
-// 2. verify_draw_kernel, a cluster of CTAs a sequence: every CTA joins the parts
-//    and finds the number of accepted tokens from 2 count + 1 sums; the cluster
-//    then draws from the one row (with no accepted count known ahead, every
-//    place's sums are needed; which row is drawn from is only known here).
+// 2. verify_draw_kernel, a cluster of CTAs a sequence: a warp a place joins its parts
+//    and decides on its token, the first refusal of all is the answer's length, and the
+//    cluster draws from that one row (every place's sums are needed ahead of it; which
+//    row is drawn from is only known here).
 //
 // The draw lies between running sums of up to 2^26 numbers, so its sums are of
 // 64-bit integers, exact and in any order, and each number in them is right to
