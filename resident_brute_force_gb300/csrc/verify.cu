@@ -414,16 +414,16 @@ __global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw
       ok = x >= 0 && best_of(i) == x;
     } else {
       const Place p = join(i), q = a.draft ? join(places + i) : Place{0.0f, 1.0f};
-      ok = xp > -INFINITY;
       lp = log_p(xp, p);
       // u q / p < 1, with the difference of the exponents as the sum of two numbers
       // (64-bit arithmetic runs at a 64th of fp32's rate).
       const float dp = less_top(xp, p.top), up = less_rest(xp, p.top, dp), dq = less_top(xq, q.top), uq = less_rest(xq, q.top, dq);
+      ok = dp > -INFINITY;  // p(x) > 0: not for a finite score beside +infinity
       const float d = __fsub_rn(dq, dp), back = __fsub_rn(d, dq);
       const float lost = __fadd_rn(__fsub_rn(__fsub_rn(dq, __fsub_rn(d, back)), __fadd_rn(dp, back)), __fsub_rn(uq, up));
       const float e = __fmul_rn(d, rate), n = rintf(fminf(fmaxf(e, -1000.0f), 1000.0f));
       const float f = fabsf(e) < 1000.0f ? __fadd_rn(__fsub_rn(e, n), __fmaf_rn(lost, rate, __fmaf_rn(d, rate, -e))) : 0.0f;
-      if (xq > -INFINITY)
+      if (dq > -INFINITY)
         ok = ok && u * (__fdiv_rn(p.z, q.z) * exp2f(f)) * exp2f(0.5f * n) * exp2f(0.5f * n) < 1.0f;
       else  // no mass of the draft's
         ok = ok && u == u;

@@ -1,0 +1,42 @@
+"""Verification of drafted tokens (include/rbf_ops.h, verify_dev) at the ends of its range: rows with +infinity, random
+numbers of 0, scores further apart than the largest fp32 number, rows that agree but for rounding."""
+import math
+
+import pytest
+import torch
+
+import resident_brute_force_gb300 as rbf
+from tests.test_gpu_ops_verify import case, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    with rbf.Ops(4096, 64, stream=torch.cuda.current_stream()) as o:
+        yield o
+        assert o.check_device_error() == rbf.RBF_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab", [50, 20011])
+@pytest.mark.parametrize("u", [0.25, 0.999])
+def test_tokens_beside_an_infinite_score_have_no_mass(ops, dtype, vocab, u):
+    """Where a target's row holds +infinity a token with a finite score is refused, whatever the draft says of it."""
+    c = case(8, 2, vocab, dtype, seed=20)
+    c["u"][:, :2] = u
+    c["tokens"][:, 0] = 3
+    c["target"][:7, 0, 7] = math.inf
+    c["draft"][0, 0, 3] = -math.inf                  # the draft has no mass on the token
+    c["draft"][1, 0, 3] = math.nan
+    c["draft"][2, 0, 9] = math.inf                   # nor here, beside its own +infinity
+    c["draft"][3, 0, 3] = math.inf                   # all of it
+    c["draft"][4, 0] = -math.inf                     # its row is empty
+    c["tokens"][5, 0] = 7                            # the one score that counts: accepted
+    c["tokens"][6, 0], c["draft"][6, 0, 7] = 7, -math.inf
+    c["target"][7, 0], c["draft"][7, 0, 3] = -math.inf, -math.inf  # an empty row accepts nothing
+    token, accepted, _ = check(ops, c)
+    assert accepted[[0, 1, 2, 3, 4, 7]].tolist() == [0] * 6 and int(accepted[5]) > 0 and int(accepted[6]) > 0
+    assert token[:5, 0].tolist() == [7] * 5 and int(token[7, 0]) == -1
+    _, accepted, _ = check(ops, dict(c, draft=None))
+    assert accepted[[0, 1, 2, 3, 4, 7]].tolist() == [0] * 6
