@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw
       const float lost = __fadd_rn(__fsub_rn(__fsub_rn(dq, __fsub_rn(d, back)), __fadd_rn(dp, back)), __fsub_rn(uq, up));
       const float e = __fmul_rn(d, rate), n = rintf(fminf(fmaxf(e, -1000.0f), 1000.0f));
       const float f = fabsf(e) < 1000.0f ? __fadd_rn(__fsub_rn(e, n), __fmaf_rn(lost, rate, __fmaf_rn(d, rate, -e))) : 0.0f;
-      if (dq > -INFINITY)
-        ok = ok && u * (__fdiv_rn(p.z, q.z) * exp2f(f)) * exp2f(0.5f * n) * exp2f(0.5f * n) < 1.0f;
+      if (dq > -INFINITY)  // at u = 0 the powers may be infinite: 0 < p(x) is all that is asked
+        ok = ok && (u <= 0.0f || u * (__fdiv_rn(p.z, q.z) * exp2f(f)) * exp2f(0.5f * n) * exp2f(0.5f * n) < 1.0f);
       else  // no mass of the draft's
         ok = ok && u == u;
     }

@@ -40,3 +40,25 @@ def test_tokens_beside_an_infinite_score_have_no_mass(ops, dtype, vocab, u):
     assert token[:5, 0].tolist() == [7] * 5 and int(token[7, 0]) == -1
     _, accepted, _ = check(ops, dict(c, draft=None))
     assert accepted[[0, 1, 2, 3, 4, 7]].tolist() == [0] * 6
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_random_number_of_zero_accepts_any_probability(ops, dtype):
+    """0 < p(x) however far p(x) lies below q(x); where p(x) is 0 the token is refused."""
+    c = case(9, 2, 300, dtype, seed=21)
+    c["tokens"][:, 0] = 11
+    c["u"][:, 0] = 0.0
+    c["u"][8, 0] = -0.0
+    c["temperature"] = torch.full((9,), 0.02)
+    c["target"][:, 0].clamp_(-9.0, 2.0)
+    c["draft"][:, 0].clamp_(-9.0, 2.0)
+    c["draft"][:, 0, 11] = 2.0
+    for i, gap in enumerate((1.0, 3.0, 3.6, 5.0, 9.0, 12.0)):  # over T: 50 to 600, 2^-72 to 2^-866
+        c["target"][i, 0, 5], c["target"][i, 0, 11] = 2.0, 2.0 - gap
+    c["target"][6, 0, 11] = -math.inf
+    c["target"][7, 0, 5] = math.inf
+    _, accepted, _ = check(ops, c)
+    assert bool((accepted[:6] > 0).all()) and accepted[6:8].tolist() == [0, 0] and int(accepted[8]) > 0
+    c["u"][:, 0] = 2.0 ** -126  # above 0: refused from about there on
+    _, accepted, _ = check(ops, c)
+    assert int(accepted[0]) > 0 and accepted[1:8].tolist() == [0] * 7
