@@ -54,10 +54,22 @@ constexpr float kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);  /
 constexpr int kDrawThreads = 512;
 constexpr int kDrawCta = 128;
 
-// log2(e) / T as a finite number above 0 (sample_dev's); 0 where the best index is asked for.
-__device__ __forceinline__ float rate_of(const VerifyLaunch& a, int64_t seq) {
-  const float t = a.temperature ? a.temperature[seq] : 1.0f;
-  return t > 0.0f ? fminf(fmaxf(__fdiv_rn(kLog2e, t), 1.4e-45f), 3.40282347e38f) : 0.0f;
+// A sequence's temperature. From 2^100 on scores and T are taken 2^-64 times as large,
+// exactly: there scores whose difference passes fp32's range have weight, and log2(e) / T
+// falls out of the range in which it has all its bits. Below, such a difference is
+// one of 2^28 octaves at least, and its weight 0.
+struct Heat {
+  float rate;   // log2(e) / T as a finite number above 0 (sample_dev's); 0 where the best index is asked for
+  float t;      // T as the scores are taken
+  float scale;  // of the scores, 1 or 2^-64
+};
+__device__ __forceinline__ Heat heat_of(const VerifyLaunch& a, int64_t seq) {
+  Heat h;
+  h.t = a.temperature ? a.temperature[seq] : 1.0f;
+  h.scale = h.t >= 0x1p100f ? 0x1p-64f : 1.0f;
+  h.t *= h.scale;
+  h.rate = h.t > 0.0f ? fminf(fmaxf(__fdiv_rn(kLog2e, h.t), 1.4e-45f), 3.40282347e38f) : 0.0f;
+  return h;
 }
 
 __device__ __forceinline__ int count_of(const VerifyLaunch& a, int64_t seq) {
@@ -109,7 +121,8 @@ __global__ void __launch_bounds__(kThreads, kStatsCtas) verify_stats_kernel(cons
   const int64_t seq = blockIdx.x;
   const int in = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z), splits = static_cast<int>(gridDim.z);
   const int64_t row_id = seq * rows + in;
-  const float rate = rate_of(a, seq);
+  const Heat heat = heat_of(a, seq);
+  const float rate = heat.rate, scale = heat.scale;
   const int count = count_of(a, seq);
   const bool of_target = in < places;
   if (of_target ? in > count : (in - places >= count || rate == 0.0f)) return;
@@ -146,16 +159,15 @@ __global__ void __launch_bounds__(kThreads, kStatsCtas) verify_stats_kernel(cons
     const float top = vec_top<T>(best);
     if (top == -INFINITY) return;
     if (top > s.top) {
-      s.z = s.top == -INFINITY ? 0.0f : s.z * ex2(less_top(s.top, top) * rate);
+      s.z = s.top == -INFINITY ? 0.0f : s.z * ex2(less_top(s.top * scale, top * scale) * rate);
       s.top = top;
     }
-    const bool inf = s.top == INFINITY;  // then only the scores that equal it count
-    if (inf) {
+    if (s.top == INFINITY || scale != 1.0f) {  // of the former only the scores that equal it count
 #pragma unroll 1
       for (int i = 0; i < N; ++i) {
         Vec<T>::unpack(raw[0], x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s.z += x[e] == INFINITY ? 1.0f : 0.0f;
+        for (int e = 0; e < E; ++e) s.z += ex2(less_top(x[e] * scale, s.top * scale) * rate);
 #pragma unroll
         for (int o = 0; o < 3; ++o) raw[o] = raw[o + 1];
       }
@@ -196,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, kStatsCtas) verify_stats_kernel(cons
       }
     }
   }
+  s.top *= scale;
   // Each below the largest of the warp, and then of the CTA.
   auto below = [&](Sum& v, int lanes) {
     float top = v.top;
@@ -351,7 +364,8 @@ __global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw
     else
       __syncthreads();
   };
-  const float rate = rate_of(a, seq);
+  const Heat heat = heat_of(a, seq);
+  const float rate = heat.rate;
   const int count = count_of(a, seq);
   if (threadIdx.x == 0) first_no = count;
   if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -359,7 +373,7 @@ __global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw
   // wait for the sums. A token's score: a NaN counts as -infinity.
   auto score = [&](const T* row, int x) {
     const float v = Vec<T>::one(row[x]);
-    return v == v ? v : -INFINITY;
+    return v == v ? v * heat.scale : -INFINITY;
   };
   struct Drafted {
     int x = -1;
@@ -526,15 +540,14 @@ __global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw
   };
 
   // log2(e) / T as the sum of two numbers (one, where it is at an end of the range).
-  const float heat = a.temperature ? a.temperature[seq] : 1.0f;
-  const float rest = __fadd_rn(__fmaf_rn(-rate, heat, kLog2e), kLog2eLow);
-  const float rate_lo = rate > 1.4e-45f && rate < 3.4e38f ? __fdiv_rn(rest, heat) : 0.0f;
+  const float rest = __fadd_rn(__fmaf_rn(-rate, heat.t, kLog2e), kLog2eLow);
+  const float rate_lo = rate > 1.4e-45f && rate < 3.4e38f ? __fdiv_rn(rest, heat.t) : 0.0f;
   // With a largest score of +infinity only those that equal it count.
-  auto scores = [](uint4 raw, float top, float (&x)[E]) {
+  auto scores = [&](uint4 raw, float top, float (&x)[E]) {
     Vec<T>::unpack(raw, x);
-    if (top == INFINITY) {
+    if (top == INFINITY || heat.scale != 1.0f) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = x[e] == INFINITY ? 0.0f : -INFINITY;
+      for (int e = 0; e < E; ++e) x[e] = top == INFINITY ? (x[e] == INFINITY ? 0.0f : -INFINITY) : x[e] * heat.scale;
     }
   };
   const Place qq = row_q;

@@ -62,3 +62,24 @@ def test_a_random_number_of_zero_accepts_any_probability(ops, dtype):
     c["u"][:, 0] = 2.0 ** -126  # above 0: refused from about there on
     _, accepted, _ = check(ops, c)
     assert int(accepted[0]) > 0 and accepted[1:8].tolist() == [0] * 7
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heat", [2e36, 1e37, 1e38, 3e38, math.inf])
+@pytest.mark.parametrize("vocab", [9, 40, 3001])
+def test_scores_further_apart_than_the_largest_number(ops, dtype, heat, vocab):
+    """x - max passes fp32's range, x / T - max / T does not: those scores have their weight."""
+    c = case(12, 3, vocab, dtype, seed=22)
+    for k in ("target", "draft"):
+        c[k] = (c[k].double() / 2.5 * 1.5e38).clamp(-3.38e38, 3.38e38).to(dtype)  # a good part of them at either end
+    c["target"][0, 0, 2:] = -math.inf
+    c["target"][0, 0, 0], c["target"][0, 0, 1] = torch.finfo(dtype).max, torch.finfo(dtype).min
+    c["target"][1, 0, ::3] = torch.finfo(dtype).min
+    c["draft"][2, 0, 1::3] = torch.finfo(dtype).max
+    c["target"][3, 1, 4] = math.inf
+    c["temperature"] = torch.full((12,), heat)
+    check(ops, c)
+    check(ops, dict(c, draft=None))
+    for u in (0.0, 0.3, 0.9, 1 - 2.0 ** -24):
+        c["u"][:, -1] = u
+        check(ops, c)
