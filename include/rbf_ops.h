@@ -221,7 +221,8 @@ rbf_status matmul_f8_dev(rbf_ops* ops, const void* d_a, rbf_dtype a_dtype, int64
  * all of it on the drafted token), drafted token x_i is accepted if all before
  * it are and u_i q_i(x_i) < p_i(x_i); one outside of [0, vocab) is not. The answer
  * goes on with one more token: at the first place r whose token is not accepted
- * drawn from max(0, p_r - q_r) (from p_r where that is 0 throughout), behind the
+ * drawn from max(0, p_r - q_r) (from p_r where that is no more than 2^-28 in all, to
+ * which the two probabilities are held together), behind the
  * last accepted one from p. It is the first index, in index order, at which the
  * running sum exceeds u times the total. So the tokens are distributed as the
  * target's own. A NaN score counts as -infinity, which has no probability; where

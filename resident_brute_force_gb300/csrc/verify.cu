@@ -53,6 +53,7 @@ constexpr float kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);  /
 // 107 and 69 (as CTAs of 256 99 and 72), with 256 104 and 75; CTAs of 256 and 512 threads 92 and 68, 89 and 67.
 constexpr int kDrawThreads = 512;
 constexpr int kDrawCta = 128;
+constexpr unsigned long long kRounding = 1ull << 34;  // of shares of 2^62: 2^-28
 
 // A sequence's temperature. From 2^100 on scores and T are taken 2^-64 times as large,
 // exactly: there scores whose difference passes fp32's range have weight, and log2(e) / T
@@ -632,7 +633,9 @@ __global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw
     return total_of(of_stretch, nullptr);
   };
   u64 total = sum_left();
-  if (left && total == 0) {  // p and q agree (or p is all on the refused token): what is left is rounding
+  // p and q agree to the 2^-29 to which either's shares hold, so that what is left is
+  // rounding; or p is all on the refused token, which is taken out exactly.
+  if (left && total <= (with_q ? kRounding : 0)) {
     left = false;
     total = sum_left();
   }

@@ -83,3 +83,20 @@ def test_scores_further_apart_than_the_largest_number(ops, dtype, heat, vocab):
     for u in (0.0, 0.3, 0.9, 1 - 2.0 ** -24):
         c["u"][:, -1] = u
         check(ops, c)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0.0, 0.5, 3.0, -20.0, 96.0])
+def test_rows_that_agree_but_for_rounding(ops, dtype, shift):
+    """A draft's row that is the target's plus a constant has the same probabilities: behind a token outside of the
+    vocabulary the answer is drawn from p, not from what rounding leaves of p - q."""
+    c = case(40, 1, 4001, torch.float32, seed=23)
+    c["target"] = ((c["target"] * 8).round() / 8).to(dtype)  # eighths: the sum below is exact in fp32
+    c["draft"] = (c["target"][:, :1].double() + shift).to(dtype)
+    if dtype == torch.bfloat16 and shift:
+        same = c["draft"].double() == c["target"][:, :1].double() + shift
+        c["draft"][~same], c["target"][:, :1][~same] = -math.inf, -math.inf
+    c["tokens"][:, 0] = -1
+    c["temperature"] = torch.linspace(0.3, 2.0, 40)
+    _, accepted, _ = check(ops, c)
+    assert bool((accepted == 0).all())
