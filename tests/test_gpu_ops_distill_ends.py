@@ -1,0 +1,48 @@
+"""Distillation (include/rbf_ops.h, distill_dev) at the ends of its range: long rows of like scores, listed scores at the
+type's lowest value, NaN beside nothing but masked scores."""
+import math
+
+import pytest
+import torch
+
+import resident_brute_force_gb300 as rbf
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    with rbf.Ops(64, 64, stream=torch.cuda.current_stream()) as o:
+        yield o
+        assert o.check_device_error() == rbf.RBF_OK
+
+
+@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 2 ** 26), (torch.float32, 9_000_001), (torch.bfloat16, 2 ** 26 - 5), (torch.float16, 1_100_003)])
+@pytest.mark.parametrize("gap", [0.0625, 0.15625, 0.34375, 0.8125, 1.28125])
+def test_sums_of_long_rows(ops, dtype, vocab, gap):
+    """A quarter of the scores at 0 and three quarters at -gap, so that every thread adds the same number over and over and
+    its roundings do not cancel; one listed score that has about a quarter of the mass. In 2^-20 of itself the mass of the others
+    is off by 0.25 and 0.13 (the exponential; its argument's two roundings, |z| < 2), 0.57 (six additions of four vectors, three
+    of those in a piece), 0.75 (twelve joins of threads' sums by half a step of 2^-23), 0.25 and 0.69 (the factor below the listed
+    score: the exponential; half a step of its argument, |z| < 32) and 0.2 (log2(e) in fp32): less than 2.9 in all, of which the
+    loss takes three quarters. A gradient has 0.38 of its own weight, 1.7 of the others' sum, a quarter of 2.9 and five
+    roundings, 0.31: less than 3.2."""
+    a = torch.full((vocab,), -gap, dtype=dtype, device="cuda")
+    a[::4] = 0.0
+    n0 = -(-vocab // 4)
+    at = 4 * (n0 // 2)
+    others = (n0 - 1) + (vocab - n0) * math.exp(-gap)
+    a[at] = math.log(others / 3)
+    listed = float(a[at].double())
+    whole = others + math.exp(listed)
+    index, teacher = torch.tensor([[at]], dtype=torch.int32, device="cuda"), torch.zeros(1, 1, device="cuda")
+    loss, grad = torch.empty(1, device="cuda"), torch.empty(1, vocab, dtype=dtype, device="cuda")
+    ops.distill_dev(a[None], index, teacher, d_loss=loss, d_grad=grad)
+    want = math.log(whole) - listed
+    assert abs(float(loss[0]) - want) <= 0.75 * 2.9 * 2.0 ** -20 + want * 2.0 ** -23, (float(loss[0]), want)
+    half = torch.finfo(dtype).eps / 2 + 3.2 * 2.0 ** -20
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    for j, e in ((0, 1.0), (1, math.exp(-gap)), (vocab - 1, 1.0 if (vocab - 1) % 4 == 0 else math.exp(-gap))):
+        assert abs(float(grad[0, j]) - e / whole) <= e / whole * half + tiny, j
+    want = math.exp(listed) / whole - 1
+    assert abs(float(grad[0, at]) - want) <= abs(want) * half
