@@ -106,10 +106,15 @@ __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   return {s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
 }
 
+// A loss is summed in units of 2^34: T is 2^-20 at least, so that nothing on the way to
+// T^2 weight times it passes fp32's range where the loss itself does not (a listed score at its
+// type's lowest value is 3.4e38 away). Powers of two change no bit.
+constexpr float kUnit = 0x1p34f, kPerUnit = 0x1p-34f;
+
 // What a CTA says of its part to all of its cluster, two floats a word: the largest
 // and the sum of the scores that are not listed, the same of the listed ones, the sum
-// of p_e ((t_e - largest t) - (s_e - largest of these)) (infinite where a listed
-// score is -infinity), and of p_e.
+// of p_e ((t_e - largest t) - (s_e - largest of these)) in units of a loss (infinite where a
+// listed score is -infinity), and of p_e.
 constexpr int kWords = 4;
 
 // The weight 2^((x - top) rate), 0 where nothing is left.
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
         if (s == -INFINITY)
           missed = 1.0f;
         else
-          diff = diff + two_product(p, (logit[e] - top_t) - (s - top_in));
+          diff = diff + two_product(p, (logit[e] - top_t) * kPerUnit - (s * kPerUnit - top_in * kPerUnit));
         mass = mass + Pair{p, 0.0f};
       }
     }
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
     const float zi = among(wi == -INFINITY ? of_warp[3][lane] : of_warp[3][lane] * weight_of(wi, ti, rate), plus);
     Pair d{of_warp[6][lane], of_warp[7][lane]};
     if (m > 0.0f && wi > -INFINITY) {
-      const Pair apart = two_sum(ti, -wi), part = two_product(m, apart.h);
+      const Pair apart = two_sum(ti * kPerUnit, -wi * kPerUnit), part = two_product(m, apart.h);
       d = d + Pair{part.h, __fmaf_rn(m, apart.l, part.l)};
     }
 #pragma unroll
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
         l = l + Pair{low(c, 2), high(c, 2)};
         mass = mass + Pair{m, high(c, 3)};
         if (m > 0.0f && low(c, 1) > -INFINITY) {
-          const Pair apart = two_sum(top_s, -low(c, 1)), part = two_product(m, apart.h);
+          const Pair apart = two_sum(top_s * kPerUnit, -low(c, 1) * kPerUnit), part = two_product(m, apart.h);
           l = l + Pair{part.h, __fmaf_rn(m, apart.l, part.l)};
         }
       }
@@ -472,6 +477,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
         const float of_n = static_cast<float>(n);
         const Pair whole = two_product(of_n, kLn2), near = two_sum(whole.h, logf(__int_as_float(bits_r - (n << 23))));
         const Pair log_r{near.h, near.l + whole.l + of_n * kLn2Low + left};
+        mass = {mass.h * kPerUnit, mass.l * kPerUnit};
         const Pair part = two_product(-mass.h, log_r.h);
         l = l + Pair{part.h, __fmaf_rn(-mass.h, log_r.l, __fmaf_rn(-mass.l, log_r.h, part.l))};
       }
@@ -479,20 +485,21 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
       if (p_rest > 0.0f) {
         float ls;
         if (zr_s > 1.0e-30f) {
-          ls = log1pf(zi_s / zr_s);
+          ls = log1pf(zi_s / zr_s) * kPerUnit;
         } else if (zr > 0.0f) {
-          ls = logf(zi / zr) + (ti - tr) * rate * kLn2;
+          ls = logf(zi / zr) * kPerUnit + (ti * kPerUnit - tr * kPerUnit) * rate * kLn2;
         } else {
           ls = INFINITY;
         }
         const float ratio_t = z_t / rest_w;
         const float lt = ratio_t < 1.0e30f ? log1pf(ratio_t) : logf(z_t) - logf(rest_w);
-        l = ls == INFINITY ? Pair{INFINITY, 0.0f} : l + two_product(p_rest, ls - lt);
+        l = ls == INFINITY ? Pair{INFINITY, 0.0f} : l + two_product(p_rest, ls - lt * kPerUnit);
       }
       loss = missed ? INFINITY : l.h + l.l;
       if (l.h == INFINITY) loss = INFINITY;
       if (p_in != p_in || z_s != z_s) loss = p_in + z_s;
-      loss = loss * a.temperature * a.temperature * w_row;
+      loss = loss * a.temperature * a.temperature;
+      loss = fabsf(loss * kUnit) < INFINITY ? loss * kUnit * w_row : loss * w_row * kUnit;
     }
     a.loss[r] = loss;
   }

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import resident_brute_force_gb300 as rbf
+from tests.test_gpu_ops_distill import call, case
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,37 @@ def test_sums_of_long_rows(ops, dtype, vocab, gap):
         assert abs(float(grad[0, j]) - e / whole) <= e / whole * half + tiny, j
     want = math.exp(listed) / whole - 1
     assert abs(float(grad[0, at]) - want) <= abs(want) * half
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("temperature,weight", [(0.5, 1.0), (0.7, 1.0), (2.0, 1 / 512), (1.0, 1e-3), (2.0 ** -20, 1.0), (2.0 ** 20, 2.0 ** -30), (0.3, 1e-30)])
+def test_listed_scores_at_the_lowest_value(ops, dtype, temperature, weight):
+    """A listed score at the type's lowest value makes a large loss, T weight p of it, which is a number wherever that is one:
+    whatever T, on the way there."""
+    c = case(6, 700, 3, dtype, seed=30, temperature=temperature)
+    lowest = torch.finfo(dtype).min
+    c["weight"] = torch.full((6,), weight)
+    c["teacher"] = (torch.tensor([[4.0, 0.0, -1.0]]) * min(temperature, 1.0)).to(dtype).repeat(6, 1)  # p of about 0.98, 0.02 and less
+    c["scores"].scatter_(1, c["index"][:, :1].long(), lowest)
+    c["scores"][2].fill_(1.0)
+    c["scores"][2].scatter_(0, c["index"][2].long(), lowest)             # all of the list
+    c["scores"][3, int(c["index"][3, 0])] = 1.0
+    c["scores"][3, int(c["index"][3, 2])] = lowest                       # an unlikely one alone
+    c["scores"][4].clamp_(-2, 2)
+    c["scores"][4, int(c["index"][4, 1])] = torch.finfo(dtype).max       # and another as far away as can be
+    c["scores"][4, int(c["index"][4, 0])] = lowest
+    c["rest"] = torch.full((6,), -2.0)
+    want = torch.zeros(6, dtype=torch.float64)
+    for i in range(6):  # by logarithms throughout: a mass 1e38 below the largest score has one, but is no 64-bit number
+        z, at = c["scores"][i].double() / temperature, c["index"][i].long()
+        outside = torch.ones(700, dtype=torch.bool).scatter(0, at, False)
+        logq = torch.cat([z[at], torch.logsumexp(z[outside], 0)[None]]) - torch.logsumexp(z, 0)
+        logp = torch.log_softmax(torch.cat([c["teacher"][i].double() / temperature, c["rest"][i:i + 1].double()]), 0)
+        want[i] = float(c["weight"][i]) * temperature ** 2 * (logp.exp() * (logp - logq)).sum()
+    loss, grad = (t.cpu().double() for t in call(ops, c))
+    assert bool(torch.isfinite(grad).all())
+    fits = want.abs() < 3.4e38
+    assert bool(fits[:4].all())
+    # the products p (t - s) / T and their sum in pairs of fp32 numbers, p to 2^-19, and the last factors' roundings
+    assert bool(((loss - want).abs() <= want.abs() * 2.0 ** -18)[fits].all()), (loss, want)
+    assert bool((loss == math.inf)[~fits].all())
