@@ -508,7 +508,10 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillLaunch a
   // ----------------------------------------------------------- the gradient
   const float scale = live ? w_row * a.temperature : 0.0f;
   float factor = 0.0f;  // of a score that is not listed: softmax_rest times this
-  if (live && zr != 0.0f) factor = scale * (p_rest == 0.0f ? q_rest : p_in < 0.5f ? p_in - q_in : q_rest - p_rest) / zr;
+  if (live && zr != 0.0f)
+    factor = scale * (p_rest == 0.0f ? q_rest : p_in < 0.5f ? p_in - q_in : q_rest - p_rest) / zr;
+  else if (live)  // all of them at -infinity: 0, or a NaN of the list, the teacher or the weight
+    factor = scale * (0.0f * (z_s + all_t));
   const float base = tr == -INFINITY ? 0.0f : tr;
   T* out = static_cast<T*>(a.grad) + r * a.ld_grad;
   const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(row) & 15);

@@ -81,3 +81,27 @@ def test_listed_scores_at_the_lowest_value(ops, dtype, temperature, weight):
     # the products p (t - s) / T and their sum in pairs of fp32 numbers, p to 2^-19, and the last factors' roundings
     assert bool(((loss - want).abs() <= want.abs() * 2.0 ** -18)[fits].all()), (loss, want)
     assert bool((loss == math.inf)[~fits].all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_not_a_number_beside_masked_scores(ops, dtype):
+    """Where every score outside of the list is -infinity, a NaN in the list, the teacher's logits, its rest or the weight
+    makes the whole row's gradient NaN all the same."""
+    c = case(7, 300, 4, dtype, seed=31, weighted=True)
+    for i in range(7):
+        row = c["scores"][i].clone()
+        c["scores"][i] = -math.inf
+        c["scores"][i, c["index"][i].long()] = row[c["index"][i].long()]
+    c["rest"] = torch.full((7,), -math.inf)
+    c["scores"][0, int(c["index"][0, 1])] = math.nan
+    c["scores"][1, int(c["index"][1, 1])] = math.inf
+    c["teacher"][2, 3] = math.nan
+    c["teacher"][3, 0] = math.inf
+    c["rest"][4] = math.nan
+    c["weight"][5] = math.nan
+    loss, grad = call(ops, c)
+    assert bool(loss[:6].isnan().all()) and bool(grad[:6].isnan().all())
+    assert bool(torch.isfinite(loss[6])) and bool(torch.isfinite(grad[6]).all())
+    outside = torch.ones(300, dtype=torch.bool)
+    outside[c["index"][6].long()] = False
+    assert bool((grad[6].cpu()[outside] == 0).all())
