@@ -53,10 +53,11 @@ typedef enum rbf_dtype {
   RBF_DTYPE_E5M2 = 6  /* 8-bit floating point, largest number 57344 */
 } rbf_dtype;
 
-/* Largest depth (values of one row) of an 8-bit matrix: every sum of that
- * many products fits 32 bits. */
+/* Largest depth (values of one row) of an 8-bit integer matrix: every sum of
+ * that many products fits 32 bits. */
 #define RBF_OPS_MAX_DEPTH 65536
-/* Largest row that sample_dev draws from, and of verify_dev and distill_dev. */
+/* Largest row that sample_dev draws from, and of verify_dev and distill_dev;
+ * largest depth of matmul_f8_dev, as a head's gradient has its vocabulary for one. */
 #define RBF_OPS_MAX_VOCAB (1 << 26)
 /* Most drafted tokens of a sequence of verify_dev. */
 #define RBF_OPS_MAX_DRAFTS 1024
@@ -66,7 +67,7 @@ typedef enum rbf_dtype {
 /* Create a handle for products of up to max_rows rows of up to max_depth
  * values (1 .. 2^20 and 1 .. RBF_OPS_MAX_DEPTH; max_rows counts the rows of
  * the first operand, the queries or tokens; the second operand's rows are not
- * limited). Its workspace is max_rows x max_depth 16-bit numbers, and up to
+ * limited, nor is matmul_f8_dev's depth by max_depth). Its workspace is max_rows x max_depth 16-bit numbers, and up to
  * 40 MB for partial sums, 32 MB for rows that are put on 16-byte boundaries and
  * 0.3 MB (64 bytes a row more) for verify_dev's sums.
  *   cuda_stream  stream of every call (NULL: the handle creates its own;
@@ -206,7 +207,10 @@ rbf_status quantize_f8_dev(rbf_ops* ops, const void* d_x, rbf_dtype x_dtype, int
  * A linear layer's gradients are two more calls: for its input's, the output's
  * gradient times the transposed weights, for its weights' the transposed
  * gradient times the transposed input, each quantised along its rows.
- * k = 0: the sums are 0. k <= max_depth.
+ * k = 0: the sums are 0. k <= RBF_OPS_MAX_VOCAB, with (m / 256 + 1)(k / 128 + 1)
+ * below 10^9 (m / 32 up to 128 rows). Rows off 16-byte boundaries are refused where the workspace does not hold
+ * them on such: all of a's, of k bytes rounded up to 16, in max_rows x max_depth 16-bit
+ * numbers; of b's 256 in 32 MB (k up to 131,072).
  * Errors: INVALID_VALUE, CUDA; a device-side timeout through
  * rbf_ops_check_device_error. */
 rbf_status matmul_f8_dev(rbf_ops* ops, const void* d_a, rbf_dtype a_dtype, int64_t ld_a, const float* d_a_scale,

@@ -438,7 +438,7 @@ rbf_status matmul_f8_dev(rbf_ops* o, const void* d_a, rbf_dtype a_dtype, int64_t
     return RBF_ERR_INVALID_VALUE;
   o->launches = 0;
   if (!on_its_device(o)) return RBF_ERR_INVALID_VALUE;
-  if (m < 0 || n < 0 || k < 0 || m > o->max_rows || n > INT32_MAX || k > o->max_depth) return RBF_ERR_INVALID_VALUE;
+  if (m < 0 || n < 0 || k < 0 || m > o->max_rows || n > INT32_MAX || k > RBF_OPS_MAX_VOCAB) return RBF_ERR_INVALID_VALUE;
   const int64_t b_scale_rows = block_rows == 1 ? n : blocks_of(n);
   if (!matrix_ok(d_a, 1, m, k, ld_a) || !matrix_ok(d_b, 1, n, k, ld_b) ||
       !matrix_ok(d_out, dtype_bytes(out_dtype), m, n, ld_out) || !matrix_ok(d_a_scale, 4, m, blocks_of(k), ld_a_scale) ||
@@ -483,18 +483,19 @@ rbf_status matmul_f8_dev(rbf_ops* o, const void* d_a, rbf_dtype a_dtype, int64_t
   w.timeout_ns = o->timeout_ns;
   const int pitch = (k + 15) / 16 * 16;
   if (m == 1) a.ld_a = pitch;
-  if (!aligned(a.a, 16) || a.ld_a % 16 != 0) {
-    // The product's other room for rows of a: max_rows x max_depth 16-bit numbers.
+  // As many rows of b as a launch takes and, where they do not start on 16-byte
+  // boundaries, as the room holds in which they are put on them. Rows of a have the
+  // other products' room, max_rows x max_depth 16-bit numbers.
+  const bool staged_a = !aligned(a.a, 16) || a.ld_a % 16 != 0, staged = !aligned(d_b, 16) || (n > 1 && ld_b % 16 != 0);
+  int64_t most = std::min(n, matmul_f8_rows(m, k));
+  if (staged) most = std::min<int64_t>(most, static_cast<int64_t>(kStagedBytes / pitch / 256 * 256));
+  if (most < 1 || (staged_a && m * pitch > o->max_rows * matmul_i8_pitch(o->max_depth) * 2)) return RBF_ERR_INVALID_VALUE;
+  if (staged_a) {
     OPS_LAUNCH(o, launch_pitch_rows(reinterpret_cast<const int8_t*>(a.a), a.ld_a, m, k, static_cast<int8_t*>(o->rows_f16), pitch,
                                     o->num_sms, o->stream));
     a.a = static_cast<const uint8_t*>(o->rows_f16);
     a.ld_a = pitch;
   }
-  // As many rows of b as a launch takes and, where they do not start on 16-byte
-  // boundaries, as the room holds in which they are put on them.
-  const bool staged = !aligned(d_b, 16) || (n > 1 && ld_b % 16 != 0);
-  int64_t most = std::min(n, matmul_f8_rows(m, k));
-  if (staged) most = std::min<int64_t>(most, static_cast<int64_t>(kStagedBytes / pitch / 256 * 256));
   for (int64_t j = 0; j < n; j += most) {
     MatmulF8Launch part = a;
     part.n = std::min(most, n - j);

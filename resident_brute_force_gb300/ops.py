@@ -190,7 +190,8 @@ def _same(got, want, what: str) -> None:
 
 class Ops:
     """A handle with its stream and workspace (``rbf_ops_create``): products of
-    up to ``max_rows`` rows of up to ``max_depth`` values. Like an engine, one
+    up to ``max_rows`` rows of up to ``max_depth`` values (8-bit floating-point ones
+    of any). Like an engine, one
     handle serves one call at a time; every call is enqueued on the handle's
     stream (``stream``: a torch stream or a raw handle; None: a stream of its
     own). The handle belongs to the device that was current then: tensors are on
@@ -327,7 +328,8 @@ class Ops:
     def matmul_f8_dev(self, d_a, d_a_scale, d_b, d_b_scale, d_out, bias=None) -> None:
         """d_out [m, n] = d_a [m, k] times d_b [n, k] transposed, both 8-bit floating point (either type), plus bias
         [n]. Each 128 values of a row of d_a have a scale, in d_a_scale [m, ceil(k / 128)], and so have those of d_b in
-        d_b_scale [n, ceil(k / 128)], or those of 128 rows of it in d_b_scale [ceil(n / 128), ceil(k / 128)]."""
+        d_b_scale [n, ceil(k / 128)], or those of 128 rows of it in d_b_scale [ceil(n / 128), ceil(k / 128)]. k may pass
+        the handle's max_depth (up to RBF_OPS_MAX_VOCAB) where the rows start on 16-byte boundaries."""
         on = self._device
         a, ld_a, m, k, a_dtype = _f8_matrix(d_a, "d_a", on)
         b, ld_b, n, b_cols, b_dtype = _f8_matrix(d_b, "d_b", on)
