@@ -192,7 +192,10 @@ rbf_status quantize_f8_dev(rbf_ops* ops, const void* d_x, rbf_dtype x_dtype, int
 
 /* out[i, j] = sum_c a_scale[i, c] * b_scale[j / block_rows, c] * sum_{k in block c} a[i, k] b[j, k] + bias[j],
  * block c being the values 128 c .. 128 c + 127 of a row. A block's products are
- * summed in fp32, and the blocks' sums with their scales too; the result is
+ * summed in fp32; the two scales are multiplied, in fp32, and their product with the sum.
+ * So scales whose product leaves fp32's normal numbers (2^-126 .. 2^128) lose bits, or the
+ * block, below them, and make it infinite above, NaN where its sum is 0. The blocks' sums
+ * with their scales are added in fp32; the result is
  * rounded once to out_dtype. It is the same for every replay. Rows of a and b are
  * read fastest from a 16-byte boundary with a stride that is a multiple of 16: others
  * are first put on such boundaries in the handle's workspace, a's with one more
@@ -251,7 +254,9 @@ rbf_status matmul_f8_dev(rbf_ops* ops, const void* d_a, rbf_dtype a_dtype, int64
  *   d_logprob      [seqs, drafts + 1] fp32 (may be NULL): log p of each of
  *                  d_token's entries, -infinity where that is -1
  * The sums that a token's acceptance depends on are fp32 ones; the drawn
- * index is decided by 64-bit integers that hold each probability to 2^-29 of itself.
+ * index is decided by 64-bit integers that hold each probability to 2^-29 of itself
+ * and 2^-60 of the whole. The former depend, in their last bits, on how the rows
+ * lie on 16-byte boundaries; a call made again with the same tensors gives the same bits.
  * seqs * (drafts + 1) <= max_rows, drafts <= RBF_OPS_MAX_DRAFTS,
  * vocab <= RBF_OPS_MAX_VOCAB. Errors: INVALID_VALUE, CUDA. */
 rbf_status verify_dev(rbf_ops* ops, const void* d_target, int64_t ld_target_seq, int64_t ld_target, const void* d_draft,

@@ -18,8 +18,9 @@
 // part that does not fit is taken in pieces, which are read twice.
 //
 // What bounds it: HBM, whose two directions are not both busy all the time: bf16 4096 x
-// 128000 457 us (2.1 GB at 4.6 TB/s; 310 at the copy rate), its loss alone 264 (155). Clusters that
-// go on to the next row took 340 for that.
+// 128000 458 us (2.1 GB at 4.6 TB/s; 310 at the copy rate), its loss alone 267 (155). Clusters that
+// go on to the next row took 340 for that. With long lists, the search for entries of the
+// same index, which grows with the square of their number: 2591 us at 1024 entries a row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,7 +37,7 @@ namespace {
 constexpr int kMaxCluster = 16;
 constexpr int kPiece = 64 * 1024;  // bytes of a row in a CTA's shared memory, at most
 // Up to this a CTA takes the row alone: three CTAs an SM, one of which reads while
-// another writes. With 32 KB, in us: bf16 4096 x 128000 524 in place of 457 (310 for the
+// another writes. With 32 KB, in us: bf16 4096 x 128000 524 in place of 458 (310 for the
 // bytes), fp32 4096 x 10000 95 in place of 64 (49), fp16 509 x 100003 68 in place of 52.
 constexpr int kAim = kPiece;
 // Up to this a CTA has 64 threads: it is bound by its steps, and many run at once. bf16 4096 x 1000
@@ -88,7 +89,7 @@ __device__ __forceinline__ uint4 pack_vec(const float (&g)[Vec<T>::kLen]) {
 // scores that are not listed over a row's pieces (256 in a row of 2^26, whose roundings may
 // all be alike), the sums of p_e and of the products with it, and what follows from
 // them. Threads' sums are joined in fp32, up to twelve additions of half a step each (in
-// pairs: bf16 4096 x 128000 471 us in place of 457, fp32 1 x 10000 8.3 in place of 7.4), and
+// pairs: bf16 4096 x 128000 471 us in place of 458, fp32 1 x 10000 8.3 in place of 7.4), and
 // so are the at most 1024 weights of a list; the last addition keeps what it leaves out.
 struct Pair {
   float h = 0.0f, l = 0.0f;

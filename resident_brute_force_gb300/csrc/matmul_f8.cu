@@ -7,6 +7,9 @@
 // The tensor cores sum a block's 128 products (kind::f8f6f4, fp32 accumulator in
 // tensor memory); the scales, which differ from block to block, are applied to each
 // block's sums on their way into the running sums, which threads hold in registers.
+// The two scales are multiplied first: one FMA a sum is left, and with a scale for 128
+// channels that product is made once for all of them. (The sum times either
+// scale would leave fp32's range for other scales, no fewer.)
 //
 // One kernel, clusters of two CTAs, one CTA per SM, tcgen05.mma.cta_group::2 with
 // M = 256 channels (rows of b, 128 per CTA) and N = NT tokens (rows of a, half per
@@ -56,8 +59,8 @@ constexpr int kFirstWorker = 4;  // from the second warpgroup on
 constexpr int kScaleBlocks = 4;  // blocks whose scales are in a slot
 constexpr int kScaleSlots = 2;
 constexpr int kMaxSmem = 227 * 1024;
-// Stages' time that an exchange of partial sums takes. With it, and never / always
-// sharing, in us: 1 x 4096 x 4096 11.1 / 12.3, 1 x 8192 x 8192 16.4 / 21.0, 128 x 1024 x 8192
+// Stages' time that an exchange of partial sums takes, measured at sizes of one round of
+// tiles. With it, and never / always sharing, in us: 1 x 4096 x 4096 11.1 / 12.3, 1 x 8192 x 8192 16.4 / 21.0, 128 x 1024 x 8192
 // 18.6 / 25.9 (it shares); 100 x 8192 x 4096 15.7, 17.8 shared, 256 x 4096 x 4096 14.6, 16.9 shared (it does not).
 template <int NT>
 constexpr int kSplitCost = NT <= 64 ? 20 : 32;

@@ -7,12 +7,15 @@
 // wherever they are computed. |x| times the factor is at most MAX (1 + 2^-22), which
 // rounds to MAX. A block so small that the factor passes 2^127 takes that and 2^-127.
 //
-// One pass: a block is held in registers between its maximum and its rounding.
+// One pass: a block is held between its maximum and its rounding.
 // Blocks of a row: 16 lanes (fp32: 32) a block, 16 bytes a lane, four blocks a
-// lane under way, and no division but the scales'. Blocks of 128 x 128: a CTA each,
-// 32 KB (fp32: 64) in its threads' registers.
-// What bounds it: HBM. 8192 x 8192 bf16: 40.5 us by rows, 38.5 by blocks (30 for the
-// bytes at the copy rate); fp32 4096 x 8192 33.8 and 29.8 (25).
+// lane under way in registers, and no division but the scales'. Blocks of 128 x 128: a CTA each,
+// 32 KB (fp32: 64) in its threads' registers and, as six CTAs of 256 threads an SM leave 40
+// of those a thread and two of 512 leave 64, partly in local memory: bf16 stores 80 bytes a
+// thread there, fp16, whose values are unpacked by conversions, 384, fp32 24.
+// What bounds it: HBM, and for fp16's blocks that local memory. 8192 x 8192 bf16 and fp16: 40.0 and
+// 39.5 us by rows, 37.5 and 44.8 by blocks (30 for the bytes at the copy rate); fp32 4096 x 8192
+// 33.1 and 29.5 (25).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -17,12 +17,12 @@
 //
 // The draw lies between running sums of up to 2^26 numbers, so its sums are of
 // 64-bit integers, exact and in any order, and each number in them is right to
-// 2^-29 of itself: weights in fp32 would put some draws in a thousand on another
-// index than 64 bits do, where the tail is long. 2^z is taken by z's whole 32nds (a
+// 2^-29 of itself and 2^-60 of the whole (what falls off their last place): weights in
+// fp32 would put some draws in a thousand on another index than 64 bits do, where the tail is long. 2^z is taken by z's whole 32nds (a
 // table of 31-bit integers) and a rest of at most 2^-6 (a polynomial, as a 32-bit fraction).
 //
 // What bounds it: of 64 sequences of 7 tokens over 128000 bf16 scores the rows' sums take
-// 43 us (246 MB, 36 at the copy rate), the draws 45: some 5 for the accepted tokens,
+// 44 us (246 MB, 36 at the copy rate), the draws 46: some 5 for the accepted tokens,
 // about 18 for either pass over the drawn rows (18 instructions a weight, 4 weights an index,
 // and as much again around them), 3 for the index itself. Tried without gain: the rows
 // kept in shared memory between the passes, or copied there ahead (cp.async), vectors
@@ -249,7 +249,9 @@ __constant__ uint32_t kRoots[32] = {
 // x - top is formed, whose rounding would have to be followed. Where top * rate
 // passes 2^16 it is, and exact: scores that have any weight are within 2^-8 of top then.
 // A weight is right to 2^-29 of itself: 2^-31 each for the rest's two roundings,
-// the polynomial's last one and the table's, 2^-30 for the product with it.
+// the polynomial's last one and the table's, 2^-30 for the product with it; and to
+// what is shifted past its last place, 2^-60 of the whole: a probability of 2^-40 keeps
+// 20 bits, one below 2^-60 may be none.
 // At `one`, the weight 1 is 2^(30 + one): a sum of weights is set to stay below 2^64.
 // The 32 roots are a warp's own in shared memory (as a register of each lane they
 // would cost a shuffle, and a convergence check, a weight).
