@@ -226,18 +226,20 @@ rbf_status matmul_f8_dev(rbf_ops* ops, const void* d_a, rbf_dtype a_dtype, int64
  * With p_i the softmax of the target's scores at place i divided by the
  * sequence's temperature T, and q_i that of the draft's (without draft scores:
  * all of it on the drafted token), drafted token x_i is accepted if all before
- * it are and u_i q_i(x_i) < p_i(x_i); one outside of [0, vocab) is not. The answer
- * goes on with one more token: at the first place r whose token is not accepted
- * drawn from max(0, p_r - q_r) (from p_r where that is no more than 2^-28 in all, to
- * which the two probabilities are held together), behind the
+ * it are and u_i q_i(x_i) < p_i(x_i); one outside of [0, vocab) is not. The
+ * answer goes on with one more token: at the first place r whose token is not
+ * accepted drawn from max(0, p_r - q_r) (from p_r where that is no more than
+ * 2^-28 in all, to which the two probabilities are held together), behind the
  * last accepted one from p. It is the first index, in index order, at which the
  * running sum exceeds u times the total. So the tokens are distributed as the
- * target's own. A NaN score counts as -infinity, which has no probability; where
- * +infinity is a row's largest score only the scores that equal it have any. A
- * place whose scores are all -infinity accepts no token and answers -1. At an
- * infinite T every finite score has the same probability. At a T not above 0, or
- * NaN, p has all of it on the first of the best indices, a token is accepted if it
- * is that one, and log-probabilities are 0.
+ * target's own. A NaN score counts as -infinity, which has no probability, nor
+ * has one of less than 2^-1074 of the row's largest (64 bits hold no such
+ * number: a mask of the type's lowest value is one); where +infinity is a row's
+ * largest score only the scores that equal it have any. A place whose scores are
+ * all -infinity accepts no token and answers -1. At an infinite T every finite
+ * score has the same probability. At a T not above 0, or NaN, p has all of it on
+ * the first of the best indices, a token is accepted if it is that one, and
+ * log-probabilities are 0.
  * Scores that were masked to -infinity stand for any filter of either side.
  *   d_target       [seqs, drafts + 1, vocab] of dtype (F32, BF16 or F16): ld_target
  *                  from place to place, ld_target_seq from sequence to sequence

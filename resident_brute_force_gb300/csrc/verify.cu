@@ -53,6 +53,7 @@ constexpr float kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);  /
 // 107 and 69 (as CTAs of 256 99 and 72), with 256 104 and 75; CTAs of 256 and 512 threads 92 and 68, 89 and 67.
 constexpr int kDrawThreads = 512;
 constexpr int kDrawCta = 128;
+constexpr float kLeastOctave = -1074.0f;  // a weight below 2^this is 0
 constexpr unsigned long long kRounding = 1ull << 34;  // of shares of 2^62: 2^-28
 
 // A sequence's temperature. From 2^100 on scores and T are taken 2^-64 times as large,
@@ -435,7 +436,8 @@ __global__ void __launch_bounds__(kDrawCta, kDrawThreads / kDrawCta) verify_draw
       // u q / p < 1, with the difference of the exponents as the sum of two numbers
       // (64-bit arithmetic runs at a 64th of fp32's rate).
       const float dp = less_top(xp, p.top), up = less_rest(xp, p.top, dp), dq = less_top(xq, q.top), uq = less_rest(xq, q.top, dq);
-      ok = dp > -INFINITY;  // p(x) > 0: not for a finite score beside +infinity
+      // p(x) > 0, as in 64 bits: not for a finite score beside +infinity, nor for a mask of the type's lowest value.
+      ok = dp * rate >= kLeastOctave;
       const float d = __fsub_rn(dq, dp), back = __fsub_rn(d, dq);
       const float lost = __fadd_rn(__fsub_rn(__fsub_rn(dq, __fsub_rn(d, back)), __fadd_rn(dp, back)), __fsub_rn(uq, up));
       const float e = __fmul_rn(d, rate), n = rintf(fminf(fmaxf(e, -1000.0f), 1000.0f));

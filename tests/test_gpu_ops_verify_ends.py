@@ -100,3 +100,29 @@ def test_rows_that_agree_but_for_rounding(ops, dtype, shift):
     c["temperature"] = torch.linspace(0.3, 2.0, 40)
     _, accepted, _ = check(ops, c)
     assert bool((accepted == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heat", [0.02, 1.0, 3.0])
+def test_masks_of_the_lowest_value(ops, dtype, heat):
+    """A score at the type's lowest value has a probability of 0, as in 64 bits: its token is refused whatever the random
+    number and the draft's own mask; a row that holds nothing else has equal ones."""
+    c = case(8, 2, 500, dtype, seed=24)
+    lowest = torch.finfo(dtype).min
+    c["temperature"] = torch.full((8,), heat)
+    c["tokens"][:, 0] = 13
+    c["u"][:, 0] = 0.5
+    c["u"][0, 0] = 0.0
+    c["target"][:4, 0, 13] = lowest                       # 0: u = 0
+    c["draft"][1, 0, 13] = lowest                         # masked on both sides
+    c["draft"][2, 0, 13], c["target"][2, 0, 13] = lowest / 2, lowest  # less so on the draft's
+    c["draft"][3, 0, 13] = -math.inf
+    c["draft"][4, 0, 13] = lowest                         # on the draft's alone: accepted
+    c["target"][5, 0], c["draft"][5, 0] = lowest, lowest  # all of either row: equal probabilities
+    c["u"][6, 0], c["target"][6, 0, 13], c["target"][6, 0, 0] = 0.0, -700 * heat, 0.0  # 2^-1010, but for the row's own largest
+    c["target"][6, 0, 1:13], c["target"][6, 0, 14:] = -1.0, -1.0
+    token, accepted, _ = check(ops, c)
+    assert accepted[:4].tolist() == [0] * 4 and bool((accepted[4:7] > 0).all())
+    assert bool((token[:4, 0] != 13).all())
+    _, accepted, _ = check(ops, dict(c, draft=None))
+    assert accepted[:4].tolist() == [0] * 4
