@@ -191,15 +191,16 @@ rbf_status quantize_f8_dev(rbf_ops* ops, const void* d_x, rbf_dtype x_dtype, int
                            int64_t ld_scale);
 
 /* out[i, j] = sum_c a_scale[i, c] * b_scale[j / block_rows, c] * sum_{k in block c} a[i, k] b[j, k] + bias[j],
- * block c being the values 128 c .. 128 c + 127 of a row. A block's products are
- * summed in fp32; the two scales are multiplied, in fp32, and their product with the sum.
- * So scales whose product leaves fp32's normal numbers (2^-126 .. 2^128) lose bits, or the
- * block, below them, and make it infinite above, NaN where its sum is 0. The blocks' sums
- * with their scales are added in fp32; the result is
- * rounded once to out_dtype. It is the same for every replay. Rows of a and b are
- * read fastest from a 16-byte boundary with a stride that is a multiple of 16: others
- * are first put on such boundaries in the handle's workspace, a's with one more
- * launch, b's up to 32 MB at a time with one more launch each.
+ * block c being the values 128 c .. 128 c + 127 of a row. A block's products
+ * are summed in fp32; the two scales are multiplied, in fp32, and their
+ * product with the sum. So scales whose product leaves fp32's normal numbers
+ * (2^-126 .. 2^128) lose bits, or the block, below them, and make it infinite
+ * above, NaN where its sum is 0. The blocks' sums with their scales are added
+ * in fp32; the result is rounded once to out_dtype. It is the same for every
+ * replay. Rows of a and b are read fastest from a 16-byte boundary with a
+ * stride that is a multiple of 16: others are first put on such boundaries in
+ * the handle's workspace, a's with one more launch, b's up to 32 MB at a time
+ * with one more launch each.
  *   d_a        [m, k] of a_dtype (E4M3 or E5M2), stride ld_a; m <= max_rows
  *   d_a_scale  [m, ceil(k / 128)] fp32, stride ld_a_scale
  *   d_b        [n, k] of b_dtype (E4M3 or E5M2), stride ld_b
@@ -210,10 +211,11 @@ rbf_status quantize_f8_dev(rbf_ops* ops, const void* d_x, rbf_dtype x_dtype, int
  * A linear layer's gradients are two more calls: for its input's, the output's
  * gradient times the transposed weights, for its weights' the transposed
  * gradient times the transposed input, each quantised along its rows.
- * k = 0: the sums are 0. k <= RBF_OPS_MAX_VOCAB, with (m / 256 + 1)(k / 128 + 1)
- * below 10^9 (m / 32 up to 128 rows). Rows off 16-byte boundaries are refused where the workspace does not hold
- * them on such: all of a's, of k bytes rounded up to 16, in max_rows x max_depth 16-bit
- * numbers; of b's 256 in 32 MB (k up to 131,072).
+ * k = 0: the sums are 0. k <= RBF_OPS_MAX_VOCAB, with (m / 256 + 1)(k / 128 +
+ * 1) below 10^9 (m / 32 up to 128 rows). Rows off 16-byte boundaries are
+ * refused where the workspace does not hold them on such: all of a's, of k
+ * bytes rounded up to 16, in max_rows x max_depth 16-bit numbers; of b's 256
+ * in 32 MB (k up to 131,072).
  * Errors: INVALID_VALUE, CUDA; a device-side timeout through
  * rbf_ops_check_device_error. */
 rbf_status matmul_f8_dev(rbf_ops* ops, const void* d_a, rbf_dtype a_dtype, int64_t ld_a, const float* d_a_scale,

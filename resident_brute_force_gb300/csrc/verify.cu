@@ -15,11 +15,12 @@
 //    cluster draws from that one row (every place's sums are needed ahead of it; which
 //    row is drawn from is only known here).
 //
-// The draw lies between running sums of up to 2^26 numbers, so its sums are of
-// 64-bit integers, exact and in any order, and each number in them is right to
-// 2^-29 of itself and 2^-60 of the whole (what falls off their last place): weights in
-// fp32 would put some draws in a thousand on another index than 64 bits do, where the tail is long. 2^z is taken by z's whole 32nds (a
-// table of 31-bit integers) and a rest of at most 2^-6 (a polynomial, as a 32-bit fraction).
+// The draw lies between running sums of up to 2^26 numbers, so its sums are of 64-bit
+// integers, exact and in any order, and each number in them is right to 2^-29 of itself
+// and 2^-60 of the whole (what falls off their last place): weights in fp32 would put some
+// draws in a thousand on another index than 64 bits do, where the tail is long. 2^z is
+// taken by z's whole 32nds (a table of 31-bit integers) and a rest of at most 2^-6 (a
+// polynomial, as a 32-bit fraction).
 //
 // What bounds it: of 64 sequences of 7 tokens over 128000 bf16 scores the rows' sums take
 // 44 us (246 MB, 36 at the copy rate), the draws 46: some 5 for the accepted tokens,
